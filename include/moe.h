@@ -647,6 +647,133 @@ int moe_experts_backward(const void *x_disp, const int32_t *offsets, int64_t row
                          float *grad_up, float *grad_down, void *workspace,
                          size_t workspace_bytes, void *stream);
 
+/* ======================================================================
+ * Grouped products and the 8-bit SwiGLU checkpoint, for experts built from
+ * parts: another activation or no gate, stacked gate / up weights, a backward
+ * of one's own (ruDNN user guide, section 5: rows grouped by expert as
+ * moe_dispatch leaves them; section 12: the order of an expert's backward).
+ *
+ * Common to these calls: a matrix of dispatched rows has unit column stride
+ * and its rows lie `ld` elements apart (ld >= its columns; a half of a
+ * stacked [rows, 2I] matrix is one). No output may overlap an input. No call
+ * needs a workspace, and every result is bit-reproducible.
+ * `offsets` [E + 1] int32 (device) is that of moe_dispatch: expert e has the
+ * rows [offsets[e], offsets[e + 1]). An expert whose offsets fall, are
+ * negative or pass `rows` is taken as one without rows and the status word
+ * records MOE_ERR_BAD_INDEX; nothing outside the matrices is touched. Rows
+ * that belong to no expert are not read, and their outputs are left as they
+ * were.
+ * ====================================================================== */
+
+/* Storage of an expert's matrix in a grouped product. */
+typedef enum moe_weight_layout {
+    MOE_WEIGHT_NK = 0,          /* [E, N, K]: out = a w^T (as gate, up, down) */
+    MOE_WEIGHT_KN = 1           /* [E, K, N]: out = a w (the input gradient of a
+                                   product whose weights are [E, K, N]) */
+} moe_weight_layout;
+
+/*
+ * moe_grouped_gemm -- the product of every row with its expert's matrix.
+ *
+ *   a    [rows, K] in dtype, row stride lda, read only.
+ *   w    [E, N, K] (MOE_WEIGHT_NK) or [E, K, N] (MOE_WEIGHT_KN) in dtype,
+ *        dense, read only.
+ *   out  [rows, N] in out_dtype (dtype or MOE_F32), row stride ldo, written
+ *        for the rows of every expert: out[r, n] = sum_k a[r, k] w[e][n, k]
+ *        (or w[e][k, n]), accumulated in FP32, rounded once.
+ *   BF16 / F16 run on tcgen05 tensor cores, F32 in true FP32 on CUDA cores.
+ *   rows >= 0, 1 <= E <= 1024, N and K >= 1. K, lda and, with MOE_WEIGHT_KN,
+ *   N take whole multiples of 16 bytes (8 elements of BF16 / F16, 4 of F32);
+ *   other N, and any ldo >= N, are fine.
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_VALUE (layout),
+ * MOE_ERR_ALIGN, MOE_ERR_CUDA.
+ */
+int moe_grouped_gemm(const void *a, int64_t lda, const int32_t *offsets, int64_t rows,
+                     const void *w, int weight_layout, int64_t E, int64_t N, int64_t K,
+                     int dtype, void *out, int64_t ldo, int out_dtype, void *stream);
+
+/*
+ * moe_grouped_gemm_weight_grad -- the weight gradient of a grouped product.
+ *
+ *   grad    [rows, N] in dtype, row stride ldg, read only: gradient of out.
+ *   a       [rows, K] in dtype, row stride lda, read only.
+ *   grad_w  [E, N, K] in grad_dtype (dtype or MOE_F32), dense, written in
+ *           full: grad_w[e][n, k] = sum over the expert's rows of
+ *           grad[r, n] a[r, k], accumulated in FP32, rounded once; zeros for an
+ *           expert without rows. With accumulate != 0 the sum is added, in
+ *           FP32, to what grad_w holds and the result rounded once. A NaN in
+ *           one expert's rows stays in that expert's gradient.
+ *   For weights stored [E, K, N] the gradient is the same call with grad and a
+ *   exchanged. N, K, ldg and lda take whole multiples of 16 bytes.
+ *   rows == 0 zeroes grad_w (or, accumulating, leaves it).
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_ALIGN,
+ * MOE_ERR_CUDA.
+ */
+int moe_grouped_gemm_weight_grad(const void *grad, int64_t ldg, const void *a, int64_t lda,
+                                 const int32_t *offsets, int64_t rows, int64_t E, int64_t N,
+                                 int64_t K, int dtype, void *grad_w, int grad_dtype,
+                                 int accumulate, void *stream);
+
+/*
+ * moe_swiglu_checkpoint -- h = SiLU(g) * u, keeping g and u in 8 bits.
+ *
+ *   g, u  [rows, I] in dtype (F32/BF16/F16), row stride ld, read only: the
+ *         gate and up products.
+ *   h     [rows, I] in dtype, row stride ldh, written: g / (1 + exp(-g)) * u,
+ *         FP32 arithmetic, rounded once.
+ *   ckpt  moe_swiglu_checkpoint_size(rows, I) bytes, 256-byte aligned, written:
+ *         four planes (moe_swiglu_checkpoint_layout): e4m3 codes of g and of u
+ *         [rows, P], P = I rounded up to 32 (codes past I are 0), and a scale
+ *         byte per block of 32 columns [rows, P / 32]. A block's scale is 2^x,
+ *         byte x + 127: the smallest with -127 <= x <= 119 and
+ *         max |v| <= 448 * 2^x over the block's finite values. A value v is
+ *         kept as e4m3(v / 2^x) (to nearest even; magnitudes above
+ *         448 * 2^119 as 448): within 2^-4 of itself, or 2^(x-10) where the
+ *         code is subnormal. NaN and infinities are kept as NaN.
+ *   offsets  NULL (every row), or [E + 1] int32: rows from offsets[E] on are
+ *         left alone, in h and in ckpt (E is unused without offsets).
+ *   2.06 bytes per value instead of moe_experts_forward_training's 8.
+ *   rows >= 0, I >= 1. g, u and h need only their elements' alignment; rows
+ *   that all start on 16 bytes are read and written in vectors.
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_ALIGN,
+ * MOE_ERR_WORKSPACE (ckpt too small or not aligned), MOE_ERR_CUDA.
+ */
+typedef struct moe_checkpoint_layout {
+    size_t gate_codes;          /* byte offsets of the planes in ckpt */
+    size_t up_codes;
+    size_t gate_scales;
+    size_t up_scales;
+    size_t row_codes;           /* P: bytes of codes per row */
+    size_t row_scales;          /* P / 32 */
+    size_t total;
+} moe_checkpoint_layout;
+
+size_t moe_swiglu_checkpoint_size(int64_t rows, int64_t I);
+int moe_swiglu_checkpoint_layout(int64_t rows, int64_t I, moe_checkpoint_layout *layout);
+int moe_swiglu_checkpoint(const void *g, const void *u, int64_t ld, const int32_t *offsets,
+                          int64_t E, int64_t rows, int64_t I, int dtype, void *h, int64_t ldh,
+                          void *ckpt, size_t ckpt_bytes, void *stream);
+
+/*
+ * moe_swiglu_checkpoint_backward -- backward of SwiGLU from the checkpoint.
+ *
+ *   grad_h  [rows, I] in dtype, row stride ld, read only.
+ *   ckpt, offsets, E, rows, I: as moe_swiglu_checkpoint wrote / was given.
+ *   grad_g, grad_u  [rows, I] in dtype, row stride ldg, written. With g, u the
+ *           checkpoint's values and t = 1 / (1 + exp(-g)):
+ *           grad_g = grad_h u t (1 + g (1 - t)), grad_u = grad_h g t.
+ *   h       NULL, or [rows, I] in dtype, row stride ldh, written: g t u, what
+ *           the following weight gradient needs, so that h is not kept.
+ *   FP32 arithmetic, each output rounded once. A NaN code makes the outputs
+ *   that depend on it NaN.
+ * Errors as moe_swiglu_checkpoint.
+ */
+int moe_swiglu_checkpoint_backward(const void *grad_h, int64_t ld, const void *ckpt,
+                                   size_t ckpt_bytes, const int32_t *offsets, int64_t E,
+                                   int64_t rows, int64_t I, int dtype, void *grad_g,
+                                   void *grad_u, int64_t ldg, void *h, int64_t ldh,
+                                   void *stream);
+
 /*
  * moe_device_status -- read the current device's status word.
  * Synchronises `stream`, then returns MOE_OK, MOE_ERR_BAD_INDEX,

@@ -65,11 +65,16 @@ EXPORTED = ["moe_status_string", "moe_abi_version", "moe_last_error_detail",
             "moe_experts_forward_training", "moe_experts_backward_workspace_size",
             "moe_experts_backward", "moe_forward_workspace_size_ex", "moe_forward_ex",
             "moe_forward_workspace_layout", "moe_set_wait_limit_ns", "moe_wait_limit_ns",
-            "moe_selftest_wait_expiry_workspace_size", "moe_selftest_wait_expiry"]
+            "moe_selftest_wait_expiry_workspace_size", "moe_selftest_wait_expiry",
+            "moe_grouped_gemm", "moe_grouped_gemm_weight_grad", "moe_swiglu_checkpoint_size",
+            "moe_swiglu_checkpoint_layout", "moe_swiglu_checkpoint",
+            "moe_swiglu_checkpoint_backward"]
 
 MOE_FORWARD_DETERMINISTIC = 1
 
 MOE_SCORING_SOFTMAX, MOE_SCORING_SIGMOID = 0, 1
+MOE_WEIGHT_NK, MOE_WEIGHT_KN = 0, 1
+
 SCORING_CODES = {"softmax": MOE_SCORING_SOFTMAX, "sigmoid": MOE_SCORING_SIGMOID}
 INDEX_CODES = {torch.int32: 1, torch.int64: 2}
 if hasattr(torch, "uint32"):
@@ -109,6 +114,12 @@ class ForwardLayout(ctypes.Structure):
     """Mirror of ``moe_forward_layout`` (include/moe.h)."""
     _fields_ = [(n, ctypes.c_size_t) for n in ("expert_indices", "weights", "counts", "offsets",
                                                "row_of", "src_of", "x_disp", "total")]
+
+
+class CheckpointLayout(ctypes.Structure):
+    """Mirror of ``moe_checkpoint_layout`` (include/moe.h)."""
+    _fields_ = [(n, ctypes.c_size_t) for n in ("gate_codes", "up_codes", "gate_scales", "up_scales",
+                                               "row_codes", "row_scales", "total")]
 
 
 class MoeError(RuntimeError):
@@ -175,6 +186,16 @@ def _bind(lib):
         "moe_wait_limit_ns": ([], ctypes.c_uint64),
         "moe_selftest_wait_expiry_workspace_size": ([_I64, _I64, _I64, _I64], _SZ),
         "moe_selftest_wait_expiry": ([_I64, _I64, _I64, _I64, _P, _P, _SZ, _P], _INT),
+        "moe_grouped_gemm": ([_P, _I64, _P, _I64, _P, _INT, _I64, _I64, _I64, _INT, _P, _I64,
+                              _INT, _P], _INT),
+        "moe_grouped_gemm_weight_grad": ([_P, _I64, _P, _I64, _P, _I64, _I64, _I64, _I64, _INT,
+                                          _P, _INT, _INT, _P], _INT),
+        "moe_swiglu_checkpoint_size": ([_I64, _I64], _SZ),
+        "moe_swiglu_checkpoint_layout": ([_I64, _I64, ctypes.POINTER(CheckpointLayout)], _INT),
+        "moe_swiglu_checkpoint": ([_P, _P, _I64, _P, _I64, _I64, _I64, _INT, _P, _I64, _P, _SZ,
+                                   _P], _INT),
+        "moe_swiglu_checkpoint_backward": ([_P, _I64, _P, _SZ, _P, _I64, _I64, _I64, _INT, _P,
+                                            _P, _I64, _P, _I64, _P], _INT),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -757,3 +778,178 @@ def moe_experts_backward(x_disp: torch.Tensor, offsets: torch.Tensor, gate: torc
         _ptr(grad_up), _ptr(grad_down), _ptr(ws), _nbytes(ws), _stream(stream))
     _check(rc, "moe_experts_backward")
     return grad_x_disp, grad_gate, grad_up, grad_down
+
+
+# ---- grouped products and the 8-bit SwiGLU checkpoint -----------------------
+# These calls run on the device of their tensors, whatever the current device
+# is; stream (default: that device's current stream) must belong to it.
+
+def _on(dev, stream, call):
+    """call(stream handle) with ``dev`` current."""
+    if dev.type != "cuda":
+        raise ValueError("tensors passed to the C ABI must live on a CUDA device")
+    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
+    if dev.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(dev):
+        return call(_stream(stream))
+
+
+def _rows(name: str, t: torch.Tensor, shape, dtype, dev) -> int:
+    """Checks a matrix of dispatched rows; returns its row stride."""
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on {dev}, not "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    rows, cols = shape
+    if cols > 1 and rows > 0 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows (any row stride)")
+    return t.stride(0) if rows > 1 else max(cols, 1)
+
+
+def _offsets(offsets: torch.Tensor, dev) -> int:
+    """Checks expert offsets; returns the number of experts."""
+    if (offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or
+            not offsets.is_contiguous() or offsets.device != dev):
+        raise ValueError(f"offsets must be contiguous int32 of shape [E + 1] on {dev}")
+    return offsets.numel() - 1
+
+
+def moe_grouped_gemm(a: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
+                     transposed: bool = False, out=None, out_dtype: torch.dtype | None = None,
+                     stream=None) -> torch.Tensor:
+    """Every dispatched row times its expert's matrix: ``a [rows, K]`` with
+    ``w [E, N, K]`` (``a w^T``) or, ``transposed``, ``w [E, K, N]`` (``a w``).
+    Returns ``out [rows, N]`` in ``out_dtype`` (default: a's dtype;
+    ``torch.float32`` keeps the FP32 sums). ``a`` and ``out`` may be columns
+    of wider matrices. Rows past ``offsets[E]`` are left as they were."""
+    rows, K = a.shape
+    dev = a.device
+    E = _offsets(offsets, dev)
+    N = w.shape[2 if transposed else 1] if w.dim() == 3 else -1
+    if tuple(w.shape) != ((E, K, N) if transposed else (E, N, K)) or w.dtype != a.dtype or w.device != dev:
+        raise ValueError(f"w must be {a.dtype} of shape {('[E, K, N]' if transposed else '[E, N, K]')}, "
+                         f"E = {E}, K = {K}, on {dev}, not {w.dtype} {tuple(w.shape)} on {w.device}")
+    if out is None:
+        out = torch.empty((rows, N), dtype=out_dtype or a.dtype, device=dev)
+    lda = _rows("a", a, (rows, K), a.dtype, dev)
+    ldo = _rows("out", out, (rows, N), out.dtype if out_dtype is None else out_dtype, dev)
+    rc = _on(dev, stream, lambda s: load_library().moe_grouped_gemm(
+        a.data_ptr(), lda, offsets.data_ptr(), rows, _ptr(w),
+        MOE_WEIGHT_KN if transposed else MOE_WEIGHT_NK, E, N, K, _code(a.dtype), out.data_ptr(),
+        ldo, _code(out.dtype), s))
+    _check(rc, "moe_grouped_gemm")
+    return out
+
+
+def moe_grouped_gemm_weight_grad(grad: torch.Tensor, a: torch.Tensor, offsets: torch.Tensor,
+                                 grad_w=None, grad_dtype: torch.dtype | None = None,
+                                 accumulate: bool = False, stream=None) -> torch.Tensor:
+    """Weight gradient of :func:`moe_grouped_gemm`: ``grad_w [E, N, K]``, per
+    expert the sum over its rows of ``grad[r]^T a[r]`` (``grad [rows, N]``,
+    ``a [rows, K]``), in ``grad_dtype`` (default FP32); zeros for an expert
+    without rows. ``accumulate`` adds to the given ``grad_w``. For ``[E, K, N]``
+    weights exchange ``grad`` and ``a``."""
+    rows, N = grad.shape
+    K = a.shape[1]
+    dev = grad.device
+    E = _offsets(offsets, dev)
+    if grad_w is None:
+        if accumulate:
+            raise ValueError("accumulate needs the grad_w to add to")
+        grad_w = torch.empty((E, N, K), dtype=grad_dtype or torch.float32, device=dev)
+    elif tuple(grad_w.shape) != (E, N, K) or grad_w.device != dev or (
+            grad_dtype is not None and grad_w.dtype != grad_dtype):
+        raise ValueError(f"grad_w must be of shape {(E, N, K)} on {dev} and in grad_dtype")
+    ldg = _rows("grad", grad, (rows, N), grad.dtype, dev)
+    lda = _rows("a", a, (rows, K), grad.dtype, dev)
+    rc = _on(dev, stream, lambda s: load_library().moe_grouped_gemm_weight_grad(
+        grad.data_ptr(), ldg, a.data_ptr(), lda, offsets.data_ptr(), rows, E, N, K,
+        _code(grad.dtype), _ptr(grad_w), _code(grad_w.dtype), int(bool(accumulate)), s))
+    _check(rc, "moe_grouped_gemm_weight_grad")
+    return grad_w
+
+
+def moe_swiglu_checkpoint_size(rows: int, I: int) -> int:
+    return int(load_library().moe_swiglu_checkpoint_size(rows, I))
+
+
+def moe_swiglu_checkpoint_layout(rows: int, I: int) -> CheckpointLayout:
+    """Byte offsets of the checkpoint's planes (see ``include/moe.h``)."""
+    layout = CheckpointLayout()
+    _check(load_library().moe_swiglu_checkpoint_layout(rows, I, ctypes.byref(layout)),
+           "moe_swiglu_checkpoint_layout")
+    return layout
+
+
+def swiglu_checkpoint_views(ckpt: torch.Tensor, rows: int, I: int) -> dict:
+    """The planes of a checkpoint as views: ``gate_codes`` and ``up_codes``
+    (``float8_e4m3fn [rows, P]``, P = I rounded up to 32) and ``gate_scales``,
+    ``up_scales`` (``uint8 [rows, P / 32]``, the scale ``2^(byte - 127)``)."""
+    p = moe_swiglu_checkpoint_layout(rows, I)
+    out = {}
+    for name, at, cols in (("gate_codes", p.gate_codes, p.row_codes), ("up_codes", p.up_codes, p.row_codes),
+                           ("gate_scales", p.gate_scales, p.row_scales),
+                           ("up_scales", p.up_scales, p.row_scales)):
+        v = ckpt[at:at + rows * cols].view(rows, cols)
+        out[name] = v.view(torch.float8_e4m3fn) if name.endswith("codes") else v
+    return out
+
+
+def moe_swiglu_checkpoint(g: torch.Tensor, u: torch.Tensor, offsets=None, h=None, ckpt=None,
+                          stream=None):
+    """``h = SiLU(g) * u`` of the gate and up products ``[rows, I]`` (of equal
+    row stride; the halves of a stacked ``[rows, 2I]`` matrix will do), keeping
+    both in 8 bits. Returns ``(h, ckpt)``; ``ckpt`` (uint8) is what
+    :func:`moe_swiglu_checkpoint_backward` takes. With ``offsets`` the rows past
+    ``offsets[E]`` are left alone."""
+    rows, I = g.shape
+    dev = g.device
+    E = 0 if offsets is None else _offsets(offsets, dev)
+    ld = _rows("g", g, (rows, I), g.dtype, dev)
+    if _rows("u", u, (rows, I), g.dtype, dev) != ld:
+        raise ValueError("g and u must have the same row stride")
+    if h is None:
+        h = torch.empty((rows, I), dtype=g.dtype, device=dev)
+    ldh = _rows("h", h, (rows, I), g.dtype, dev)
+    if ckpt is None:
+        ckpt = torch.empty(moe_swiglu_checkpoint_size(rows, I), dtype=torch.uint8, device=dev)
+    elif ckpt.device != dev:
+        raise ValueError(f"ckpt must be on {dev}")
+    rc = _on(dev, stream, lambda s: load_library().moe_swiglu_checkpoint(
+        g.data_ptr(), u.data_ptr(), ld, None if offsets is None else offsets.data_ptr(), E, rows, I,
+        _code(g.dtype), h.data_ptr(), ldh, _ptr(ckpt), _nbytes(ckpt), s))
+    _check(rc, "moe_swiglu_checkpoint")
+    return h, ckpt
+
+
+def moe_swiglu_checkpoint_backward(grad_h: torch.Tensor, ckpt: torch.Tensor, offsets=None,
+                                   grad_g=None, grad_u=None, h=None, need_h: bool = True,
+                                   stream=None):
+    """Backward of :func:`moe_swiglu_checkpoint` from its checkpoint. Returns
+    ``(grad_g, grad_u, h)``, ``[rows, I]`` each: the gradients by default as
+    halves of one ``[rows, 2I]`` matrix, ``h`` recomputed from the checkpoint
+    (None without ``need_h``)."""
+    rows, I = grad_h.shape
+    dev, dt = grad_h.device, grad_h.dtype
+    E = 0 if offsets is None else _offsets(offsets, dev)
+    if (grad_g is None) != (grad_u is None):
+        raise ValueError("give both grad_g and grad_u, or neither")
+    if grad_g is None:
+        both = torch.empty((rows, 2 * I), dtype=dt, device=dev)
+        grad_g, grad_u = both[:, :I], both[:, I:]
+    if h is None and need_h:
+        h = torch.empty((rows, I), dtype=dt, device=dev)
+    ld = _rows("grad_h", grad_h, (rows, I), dt, dev)
+    ldg = _rows("grad_g", grad_g, (rows, I), dt, dev)
+    if _rows("grad_u", grad_u, (rows, I), dt, dev) != ldg:
+        raise ValueError("grad_g and grad_u must have the same row stride")
+    ldh = I if h is None else _rows("h", h, (rows, I), dt, dev)
+    if ckpt.device != dev:
+        raise ValueError(f"ckpt must be on {dev}")
+    rc = _on(dev, stream, lambda s: load_library().moe_swiglu_checkpoint_backward(
+        grad_h.data_ptr(), ld, _ptr(ckpt), _nbytes(ckpt),
+        None if offsets is None else offsets.data_ptr(), E, rows, I, _code(dt), grad_g.data_ptr(),
+        grad_u.data_ptr(), ldg, None if h is None else h.data_ptr(), ldh, s))
+    _check(rc, "moe_swiglu_checkpoint_backward")
+    return grad_g, grad_u, h

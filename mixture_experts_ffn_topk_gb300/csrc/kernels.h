@@ -204,4 +204,31 @@ cudaError_t launch_selftest_wait_expiry(int E, int rows_per_expert, int64_t H, i
 cudaError_t launch_finalize(const float *y_acc, int64_t T, int64_t H, void *y, int ydt,
                             cudaStream_t s);
 
+// Grouped products of dispatched rows with one matrix per expert:
+// out[r] = a[r] w[e]^T (w [E, N, K]) or a[r] w[e] (transposed: w [E, K, N]).
+// Rows of a lie lda elements apart, rows of out (odt: dt or F32) ldo.
+cudaError_t launch_grouped_gemm_simt(int dt, const void *a, int64_t lda, const int32_t *offsets,
+                                     int64_t rows, const void *w, int E, int64_t N, int64_t K,
+                                     bool transposed, void *out, int64_t ldo, int odt,
+                                     unsigned *status, cudaStream_t s);
+// grad_w[e] (+)= sum over the expert's rows of grad[r]^T a[r], [E, N, K] in odt.
+cudaError_t launch_grouped_weight_grad_simt(int dt, const void *grad, int64_t ldg, const void *a,
+                                            int64_t lda, const int32_t *offsets, int64_t rows,
+                                            int E, int64_t N, int64_t K, void *grad_w, int odt,
+                                            bool accumulate, unsigned *status, cudaStream_t s);
+
+// SwiGLU with the 8-bit checkpoint of g and u (planes inside ckpt, byte
+// offsets), and its backward. end: offsets + E, or nullptr for all rows.
+struct SwigluCheckpointPlanes {
+    size_t gate_codes, up_codes, gate_scales, up_scales, row_codes, row_scales, total;
+};
+SwigluCheckpointPlanes swiglu_checkpoint_planes(int64_t rows, int64_t I);
+cudaError_t launch_swiglu_checkpoint(int dt, const void *g, const void *u, int64_t ld,
+                                     const int32_t *end, int64_t rows, int64_t I, void *h,
+                                     int64_t ldh, void *ckpt, cudaStream_t s);
+cudaError_t launch_swiglu_checkpoint_backward(int dt, const void *grad_h, int64_t ld,
+                                              const void *ckpt, const int32_t *end, int64_t rows,
+                                              int64_t I, void *grad_g, void *grad_u, int64_t ldg,
+                                              void *h, int64_t ldh, cudaStream_t s);
+
 }  // namespace moe

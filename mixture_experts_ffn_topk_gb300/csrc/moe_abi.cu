@@ -89,6 +89,8 @@ size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 constexpr int64_t kMaxE = 1024;
 constexpr uint64_t kMaxWaitLimitNs = 60ull * 1000000000ull;   // moe_set_wait_limit_ns bound
 constexpr int64_t kMaxRows = 0x7fffffff;   // dispatched rows are int32
+constexpr int64_t kMaxGroupedDim = 1 << 24;      // N, K, I of the grouped products and checkpoints
+constexpr int64_t kMaxStride = int64_t(1) << 32; // their row strides (a TMA stride is below 2^40 bytes)
 
 // Vector width rule shared by the experts and combine kernels: rows are moved
 // in 16-byte vectors and TMA strides are 16-byte multiples.
@@ -948,6 +950,160 @@ int moe_experts_backward(const void *x_disp, const int32_t *offsets, int64_t row
             return fail(MOE_ERR_ALIGN, "TMA descriptor rejected (pointer alignment or shape)");
     }
     return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_experts_backward");
+}
+
+// Shared checks of the grouped products. `mult`: elements in 16 bytes.
+static int check_grouped_args(int64_t rows, int64_t E, int64_t N, int64_t K, int dt, int odt)
+{
+    if (!valid_dtype(dt)) return fail(MOE_ERR_DTYPE, "dtype must be F32, BF16 or F16");
+    if (odt != dt && odt != MOE_F32)
+        return fail(MOE_ERR_DTYPE, "the output dtype must be the operands' or F32");
+    if (rows < 0 || rows > kMaxRows || E < 1 || E > kMaxE)
+        return fail(MOE_ERR_SHAPE, "need 0 <= rows < 2^31 and 1 <= E <= 1024");
+    if (N < 1 || K < 1 || N > kMaxGroupedDim || K > kMaxGroupedDim)
+        return fail(MOE_ERR_SHAPE, "need 1 <= N, K <= 2^24");
+    return MOE_OK;
+}
+
+int moe_grouped_gemm(const void *a, int64_t lda, const int32_t *offsets, int64_t rows,
+                     const void *w, int weight_layout, int64_t E, int64_t N, int64_t K,
+                     int dtype, void *out, int64_t ldo, int out_dtype, void *stream)
+{
+    const NvtxRange nvtx("moe_grouped_gemm");
+    int rc = check_grouped_args(rows, E, N, K, dtype, out_dtype);
+    if (rc != MOE_OK) return rc;
+    if (weight_layout != MOE_WEIGHT_NK && weight_layout != MOE_WEIGHT_KN)
+        return fail(MOE_ERR_VALUE, "weight_layout must be MOE_WEIGHT_NK or MOE_WEIGHT_KN");
+    if (!vec_dim_ok(K, dtype) || (weight_layout == MOE_WEIGHT_KN && !vec_dim_ok(N, dtype)))
+        return fail(MOE_ERR_SHAPE, "K, and N of [E, K, N] weights, must be multiples of 16 bytes");
+    if (lda < K || !vec_dim_ok(lda, dtype) || lda > kMaxStride)
+        return fail(MOE_ERR_SHAPE, "lda must be >= K and a multiple of 16 bytes");
+    if (ldo < N || ldo > kMaxStride) return fail(MOE_ERR_SHAPE, "ldo must be >= N");
+    if (rows == 0) return MOE_OK;
+    rc = check_experts_ptrs("moe_grouped_gemm: tensors must be non-NULL and 16-byte aligned",
+                            {a, offsets, w, out});
+    if (rc != MOE_OK) return rc;
+    unsigned *st = status_ptr();
+    if (!st) return fail(MOE_ERR_CUDA, "cannot resolve the device status word");
+    cudaError_t err = launch_grouped_gemm_simt(dtype, a, lda, offsets, rows, w, (int)E, N, K,
+                                               weight_layout == MOE_WEIGHT_KN, out, ldo, out_dtype,
+                                               st, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_grouped_gemm");
+}
+
+int moe_grouped_gemm_weight_grad(const void *grad, int64_t ldg, const void *a, int64_t lda,
+                                 const int32_t *offsets, int64_t rows, int64_t E, int64_t N,
+                                 int64_t K, int dtype, void *grad_w, int grad_dtype,
+                                 int accumulate, void *stream)
+{
+    const NvtxRange nvtx("moe_grouped_gemm_weight_grad");
+    int rc = check_grouped_args(rows, E, N, K, dtype, grad_dtype);
+    if (rc != MOE_OK) return rc;
+    if (!vec_dim_ok(N, dtype) || !vec_dim_ok(K, dtype))
+        return fail(MOE_ERR_SHAPE, "N and K must be multiples of 16 bytes");
+    if (ldg < N || !vec_dim_ok(ldg, dtype) || ldg > kMaxStride || lda < K ||
+        !vec_dim_ok(lda, dtype) || lda > kMaxStride)
+        return fail(MOE_ERR_SHAPE, "ldg >= N and lda >= K must be multiples of 16 bytes");
+    rc = check_experts_ptrs("moe_grouped_gemm_weight_grad: tensors must be non-NULL and 16-byte aligned",
+                            {grad_w});
+    if (rc != MOE_OK) return rc;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t err;
+    if (rows == 0) {
+        if (accumulate) return MOE_OK;
+        err = cudaMemsetAsync(grad_w, 0, (size_t)E * (size_t)N * (size_t)K * elem_bytes(grad_dtype), s);
+        return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_grouped_gemm_weight_grad");
+    }
+    rc = check_experts_ptrs("moe_grouped_gemm_weight_grad: tensors must be non-NULL and 16-byte aligned",
+                            {grad, a, offsets});
+    if (rc != MOE_OK) return rc;
+    unsigned *st = status_ptr();
+    if (!st) return fail(MOE_ERR_CUDA, "cannot resolve the device status word");
+    err = launch_grouped_weight_grad_simt(dtype, grad, ldg, a, lda, offsets, rows, (int)E, N, K,
+                                          grad_w, grad_dtype, accumulate != 0, st, s);
+    return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_grouped_gemm_weight_grad");
+}
+
+static int check_checkpoint_sizes(int64_t rows, int64_t I)
+{
+    if (rows < 0 || rows > kMaxRows || I < 1 || I > kMaxGroupedDim)
+        return fail(MOE_ERR_SHAPE, "need 0 <= rows < 2^31 and 1 <= I <= 2^24");
+    return MOE_OK;
+}
+
+// Sizes, dtype, E and row strides of both checkpoint calls.
+static int check_checkpoint_args(int64_t rows, int64_t I, int dt, const int32_t *offsets, int64_t E,
+                          std::initializer_list<int64_t> strides)
+{
+    if (!valid_dtype(dt)) return fail(MOE_ERR_DTYPE, "dtype must be F32, BF16 or F16");
+    const int rc = check_checkpoint_sizes(rows, I);
+    if (rc != MOE_OK) return rc;
+    if (offsets != nullptr && (E < 1 || E > kMaxE)) return fail(MOE_ERR_SHAPE, "need 1 <= E <= 1024");
+    for (int64_t ld : strides)
+        if (ld < I || ld > kMaxStride) return fail(MOE_ERR_SHAPE, "row strides must be >= I");
+    return MOE_OK;
+}
+
+static int check_checkpoint_ptrs(const char *name, int dt, const int32_t *offsets, const void *ckpt,
+                          size_t ckpt_bytes, size_t need, std::initializer_list<const void *> ptrs)
+{
+    for (const void *q : ptrs)
+        if (!q) return fail(MOE_ERR_NULL, name);
+    for (const void *q : ptrs)
+        if (reinterpret_cast<uintptr_t>(q) % elem_bytes(dt)) return fail(MOE_ERR_ALIGN, name);
+    if (offsets != nullptr && !aligned16(offsets)) return fail(MOE_ERR_ALIGN, name);
+    if (!ckpt || ckpt_bytes < need || (reinterpret_cast<uintptr_t>(ckpt) & 255u))
+        return fail(MOE_ERR_WORKSPACE, "checkpoint too small or not 256-byte aligned");
+    return MOE_OK;
+}
+
+size_t moe_swiglu_checkpoint_size(int64_t rows, int64_t I)
+{
+    if (rows < 0 || rows > kMaxRows || I < 1 || I > kMaxGroupedDim) return 0;
+    return swiglu_checkpoint_planes(rows, I).total;
+}
+
+int moe_swiglu_checkpoint_layout(int64_t rows, int64_t I, moe_checkpoint_layout *layout)
+{
+    const int rc = check_checkpoint_sizes(rows, I);
+    if (rc != MOE_OK) return rc;
+    if (!layout) return fail(MOE_ERR_NULL, "moe_swiglu_checkpoint_layout: NULL layout");
+    const SwigluCheckpointPlanes p = swiglu_checkpoint_planes(rows, I);
+    *layout = {p.gate_codes, p.up_codes, p.gate_scales, p.up_scales, p.row_codes, p.row_scales, p.total};
+    return MOE_OK;
+}
+
+int moe_swiglu_checkpoint(const void *g, const void *u, int64_t ld, const int32_t *offsets,
+                          int64_t E, int64_t rows, int64_t I, int dtype, void *h, int64_t ldh,
+                          void *ckpt, size_t ckpt_bytes, void *stream)
+{
+    const NvtxRange nvtx("moe_swiglu_checkpoint");
+    int rc = check_checkpoint_args(rows, I, dtype, offsets, E, {ld, ldh});
+    if (rc != MOE_OK || rows == 0) return rc;
+    rc = check_checkpoint_ptrs("moe_swiglu_checkpoint: tensors must be non-NULL and aligned", dtype,
+                               offsets, ckpt, ckpt_bytes, moe_swiglu_checkpoint_size(rows, I), {g, u, h});
+    if (rc != MOE_OK) return rc;
+    cudaError_t err = launch_swiglu_checkpoint(dtype, g, u, ld, offsets ? offsets + E : nullptr, rows,
+                                               I, h, ldh, ckpt, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_swiglu_checkpoint");
+}
+
+int moe_swiglu_checkpoint_backward(const void *grad_h, int64_t ld, const void *ckpt,
+                                   size_t ckpt_bytes, const int32_t *offsets, int64_t E,
+                                   int64_t rows, int64_t I, int dtype, void *grad_g,
+                                   void *grad_u, int64_t ldg, void *h, int64_t ldh, void *stream)
+{
+    const NvtxRange nvtx("moe_swiglu_checkpoint_backward");
+    int rc = check_checkpoint_args(rows, I, dtype, offsets, E, {ld, ldg, h ? ldh : I});
+    if (rc != MOE_OK || rows == 0) return rc;
+    rc = check_checkpoint_ptrs("moe_swiglu_checkpoint_backward: tensors must be non-NULL and aligned",
+                               dtype, offsets, ckpt, ckpt_bytes, moe_swiglu_checkpoint_size(rows, I),
+                               {grad_h, grad_g, grad_u, h ? h : grad_g});
+    if (rc != MOE_OK) return rc;
+    cudaError_t err = launch_swiglu_checkpoint_backward(
+        dtype, grad_h, ld, ckpt, offsets ? offsets + E : nullptr, rows, I, grad_g, grad_u, ldg, h, ldh,
+        static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_swiglu_checkpoint_backward");
 }
 
 int moe_device_status(void *stream, int clear)
