@@ -1,4 +1,5 @@
-// grouped_simt.cu -- grouped products on CUDA cores, FP32 arithmetic.
+// grouped_simt.cu -- grouped products of FP32 rows on CUDA cores (true FP32:
+// tensor cores would round the operands to TF32).
 //
 // For the rows r of expert e (offsets[e] <= r < offsets[e + 1]):
 //   product       out[r, n] = sum_k a[r, k] w[e][n, k]   (or w[e][k, n])
@@ -9,8 +10,6 @@
 // twice in shared memory (k-major, so that a thread's TM and TN values are
 // vector loads); the next step's global loads are in flight during the
 // current one's products.
-#include <type_traits>
-
 #include "common.cuh"
 #include "grouped.cuh"
 #include "kernels.h"
@@ -19,21 +18,8 @@ namespace moe {
 
 namespace {
 
-// Four consecutive elements as FP32 (the caller checks bounds and alignment).
-template <int DT>
-__device__ __forceinline__ float4 load4(const typename Elem<DT>::T *p)
-{
-    if constexpr (DT == DT_F32) return *reinterpret_cast<const float4 *>(p);
-    else {
-        const uint2 v = *reinterpret_cast<const uint2 *>(p);
-        const float2 a = DT == DT_BF16 ? bf16x2_to_float2(v.x) : f16x2_to_float2(v.x);
-        const float2 b = DT == DT_BF16 ? bf16x2_to_float2(v.y) : f16x2_to_float2(v.y);
-        return make_float4(a.x, a.y, b.x, b.y);
-    }
-}
-
 struct SimtOperand {
-    const void *p;          // element (0, 0) of the whole operand
+    const float *p;         // element (0, 0) of the whole operand
     int64_t ld;             // elements between rows
     int64_t per_expert;     // elements between experts' matrices (0: rows of a dispatched matrix)
 };
@@ -41,13 +27,12 @@ struct SimtOperand {
 // WG: the reduction runs over the expert's rows (X = grad, Y = a, both stored
 // with the output index contiguous). Otherwise X = a (k contiguous), Y = w,
 // k contiguous unless Y_MAJOR.
-template <int DT, bool WG, bool Y_MAJOR, int BM, int BN, int TM, int TN>
+template <bool WG, bool Y_MAJOR, int BM, int BN, int TM, int TN>
 __global__ void __launch_bounds__(BM / TM * (BN / TN))
 grouped_simt_kernel(SimtOperand x, SimtOperand y, const int32_t *__restrict__ offsets, int E,
-                    int rows, int M, int N, int K, void *__restrict__ out, int64_t ldo, int odt,
+                    int rows, int M, int N, int K, float *__restrict__ out, int64_t ldo,
                     int accumulate, unsigned *status)
 {
-    using T = typename Elem<DT>::T;
     constexpr int BK = 16, THREADS = BM / TM * (BN / TN);
     constexpr int XV = BM * BK / 4 / THREADS, YV = BN * BK / 4 / THREADS;
     static_assert(XV >= 1 && YV >= 1, "each thread loads at least one vector of each operand");
@@ -71,19 +56,19 @@ grouped_simt_kernel(SimtOperand x, SimtOperand y, const int32_t *__restrict__ of
         const int m0 = loc / nt * BM, n0 = loc % nt * BN;
         const int m_end = WG ? M : cnt, k_end = WG ? cnt : K;
         // element (0, 0) of this unit's operands
-        const T *xp = static_cast<const T *>(x.p) + (int64_t)first * x.ld;
-        const T *yp = static_cast<const T *>(y.p) + (WG ? (int64_t)first * y.ld : (int64_t)e * y.per_expert);
+        const float *xp = x.p + (int64_t)first * x.ld;
+        const float *yp = y.p + (WG ? (int64_t)first * y.ld : (int64_t)e * y.per_expert);
 
         float4 xr[XV], yr[YV];
         // one vector of four: along k (k contiguous) or along the output index
-        auto fetch = [&](const T *p, int64_t ld, bool major, int i0, int i_end, int k0, int v, int B) {
+        auto fetch = [&](const float *p, int64_t ld, bool major, int i0, int i_end, int k0, int v, int B) {
             int i, k;
             if (major) { k = v / (B / 4); i = v % (B / 4) * 4; }
             else { i = v / (BK / 4); k = v % (BK / 4) * 4; }
             float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
             if (i0 + i < i_end && k0 + k < k_end)
-                r = load4<DT>(p + (major ? (int64_t)(k0 + k) * ld + i0 + i
-                                         : (int64_t)(i0 + i) * ld + k0 + k));
+                r = *reinterpret_cast<const float4 *>(
+                    p + (major ? (int64_t)(k0 + k) * ld + i0 + i : (int64_t)(i0 + i) * ld + k0 + k));
             return r;
         };
         auto fetch_all = [&](int k0) {
@@ -160,66 +145,54 @@ grouped_simt_kernel(SimtOperand x, SimtOperand y, const int32_t *__restrict__ of
                 const int n = n0 + tn * TN + j;
                 if (n >= N) continue;
                 const int64_t at = out0 + (int64_t)m * ldo + n;
-                const float old = accumulate ? load_as_float(out, odt, at) : 0.0f;
-                store_from_float(out, odt, at, accumulate ? old + acc[i][j] : acc[i][j]);
+                out[at] = accumulate ? out[at] + acc[i][j] : acc[i][j];
             }
         }
     }
 }
 
-template <int DT, bool WG, bool Y_MAJOR, int BM, int BN, int TM, int TN>
+template <bool WG, bool Y_MAJOR, int BM, int BN, int TM, int TN>
 cudaError_t launch_tile(const SimtOperand &x, const SimtOperand &y, const int32_t *offsets, int E,
-                        int64_t rows, int M, int N, int K, void *out, int64_t ldo, int odt,
+                        int64_t rows, int M, int N, int K, float *out, int64_t ldo,
                         int accumulate, unsigned *status, cudaStream_t s)
 {
     const int64_t nt = (N + BN - 1) / BN;
     const int64_t mt = WG ? (int64_t)E * ((M + BM - 1) / BM) : rows / BM + (rows < E ? rows : E);
     const int64_t units = mt * nt, most = (int64_t)device_sm_count() * 4;
-    return launch_pdl(grouped_simt_kernel<DT, WG, Y_MAJOR, BM, BN, TM, TN>,
+    return launch_pdl(grouped_simt_kernel<WG, Y_MAJOR, BM, BN, TM, TN>,
                       dim3((unsigned)(units < most ? units : most)), dim3(BM / TM * (BN / TN)), 0, s,
-                      x, y, offsets, E, (int)rows, M, N, K, out, ldo, odt, accumulate, status);
+                      x, y, offsets, E, (int)rows, M, N, K, out, ldo, accumulate, status);
 }
 
-template <int DT, bool WG, bool Y_MAJOR>
+template <bool WG, bool Y_MAJOR>
 cudaError_t launch_sizes(const SimtOperand &x, const SimtOperand &y, const int32_t *offsets, int E,
-                         int64_t rows, int M, int N, int K, void *out, int64_t ldo, int odt,
+                         int64_t rows, int M, int N, int K, float *out, int64_t ldo,
                          int accumulate, unsigned *status, cudaStream_t s)
 {
-    return launch_tile<DT, WG, Y_MAJOR, 64, 64, 4, 4>(x, y, offsets, E, rows, M, N, K, out, ldo,
-                                                     odt, accumulate, status, s);
+    return launch_tile<WG, Y_MAJOR, 64, 64, 4, 4>(x, y, offsets, E, rows, M, N, K, out, ldo,
+                                                     accumulate, status, s);
 }
 
 }  // namespace
 
-cudaError_t launch_grouped_gemm_simt(int dt, const void *a, int64_t lda, const int32_t *offsets,
-                                     int64_t rows, const void *w, int E, int64_t N, int64_t K,
-                                     bool transposed, void *out, int64_t ldo, int odt,
-                                     unsigned *status, cudaStream_t s)
+cudaError_t launch_grouped_gemm_simt(const float *a, int64_t lda, const int32_t *offsets,
+                                     int64_t rows, const float *w, int E, int64_t N, int64_t K,
+                                     bool transposed, float *out, int64_t ldo, unsigned *status,
+                                     cudaStream_t s)
 {
     const SimtOperand x{a, lda, 0}, y{w, transposed ? N : K, N * K};
-    auto go = [&](auto dtc) {
-        constexpr int DT = decltype(dtc)::value;
-        return transposed ? launch_sizes<DT, false, true>(x, y, offsets, E, rows, 0, (int)N, (int)K, out, ldo, odt, 0, status, s)
-                          : launch_sizes<DT, false, false>(x, y, offsets, E, rows, 0, (int)N, (int)K, out, ldo, odt, 0, status, s);
-    };
-    if (dt == DT_F32) return go(std::integral_constant<int, DT_F32>{});
-    if (dt == DT_BF16) return go(std::integral_constant<int, DT_BF16>{});
-    return go(std::integral_constant<int, DT_F16>{});
+    if (transposed)
+        return launch_sizes<false, true>(x, y, offsets, E, rows, 0, (int)N, (int)K, out, ldo, 0, status, s);
+    return launch_sizes<false, false>(x, y, offsets, E, rows, 0, (int)N, (int)K, out, ldo, 0, status, s);
 }
 
-cudaError_t launch_grouped_weight_grad_simt(int dt, const void *grad, int64_t ldg, const void *a,
+cudaError_t launch_grouped_weight_grad_simt(const float *grad, int64_t ldg, const float *a,
                                             int64_t lda, const int32_t *offsets, int64_t rows,
-                                            int E, int64_t N, int64_t K, void *grad_w, int odt,
+                                            int E, int64_t N, int64_t K, float *grad_w,
                                             bool accumulate, unsigned *status, cudaStream_t s)
 {
     const SimtOperand x{grad, ldg, 0}, y{a, lda, 0};
-    auto go = [&](auto dtc) {
-        constexpr int DT = decltype(dtc)::value;
-        return launch_sizes<DT, true, true>(x, y, offsets, E, rows, (int)N, (int)K, 0, grad_w, K, odt, accumulate, status, s);
-    };
-    if (dt == DT_F32) return go(std::integral_constant<int, DT_F32>{});
-    if (dt == DT_BF16) return go(std::integral_constant<int, DT_BF16>{});
-    return go(std::integral_constant<int, DT_F16>{});
+    return launch_sizes<true, true>(x, y, offsets, E, rows, (int)N, (int)K, 0, grad_w, K, accumulate, status, s);
 }
 
 }  // namespace moe

@@ -1,0 +1,490 @@
+// grouped_tc.cu -- grouped products of BF16 / F16 rows on tcgen05 tensor cores.
+//
+// For the rows r of expert e (offsets[e] <= r < offsets[e + 1]):
+//   out[r, n] = sum_k a[r, k] w[e][n, k]   (MOE_WEIGHT_NK), or w[e][k, n].
+// The product is computed transposed, out^T = w a^T: the weights' n, whose
+// extent is the same for every expert, takes the MMA's fixed side (M = 128 per
+// CTA), and the expert's rows take the side whose width is chosen per
+// instruction (N = 16, 32, ..., 256). So a ragged segment wastes at most 15 (on
+// a pair 31) columns of one instruction instead of most of a 128-row tile,
+// and a decode step's one or two rows per expert cost a 16-wide MMA over a
+// weight tile that is loaded whole: the kernel streams weights.
+//
+// Per CTA (one per SM, 192 threads, persistent over the units):
+//   warp 0     TMA producer: 128 weight columns x 64 k (16 KiB; one box of
+//              K-major rows, or two MN-major boxes of 64 n for [E, K, N]) and
+//              the unit's rows x 64 k, into a ring of 192 KiB;
+//   warp 1     tcgen05.mma issuer, K = 16 per instruction, two accumulators of
+//              256 TMEM columns in turn;
+//   warps 2-5  epilogue: TMEM lane = n, column = row of the segment. 32 rows
+//              (16 of FP32) at a time are rounded, transposed through shared
+//              memory and stored as 256 (512) consecutive bytes per row.
+// CTA pairs (CG = 2): M = 256, each CTA holds its 128 weight columns and half
+// of the unit's rows; the even CTA issues the MMAs for both.
+// An expert's rows are cut into units of equal width, at most tok_cap; units
+// run over (expert, block of row units, weight tile, row unit), the row unit
+// fastest, so that CTAs at work share a weight tile in L2; a block's rows are
+// held to what stays in L2 while all weight tiles pass.
+//
+// Every wait is bounded (wait_ns); on expiry the kernel records ST_TIMEOUT,
+// stops issuing work, drains its own copies and MMAs, frees TMEM and exits.
+#include <atomic>
+
+#include "common.cuh"
+#include "grouped.cuh"
+#include "kernels.h"
+#include "tc_ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int BM = 128;                  // weight columns per CTA
+constexpr int BK = 64;                   // k per stage: 128 bytes
+constexpr int UK = 16;                   // k per tcgen05.mma
+constexpr int W_BYTES = BM * BK * 2;     // 16 KiB
+constexpr int RING_BYTES = 192 << 10;
+constexpr int MAX_STAGES = 10;
+constexpr int ACC_COLS = 256;
+constexpr int TMEM_COLS = 2 * ACC_COLS;
+constexpr int THREADS = 192;
+constexpr int STG_BYTES = 8192;          // one epilogue staging buffer
+constexpr uint64_t kDrainLimitNs = 100000000ull;
+// Bytes of rows a block of row units may cover, well inside the 129 MB L2
+// that also carries the streamed weights and the output.
+constexpr int64_t kRowBlockBytes = 48ll << 20;
+
+struct __align__(1024) Smem {
+    uint8_t ring[RING_BYTES];
+    uint8_t stg[2][STG_BYTES];
+    uint64_t full[MAX_STAGES];
+    uint64_t empty[MAX_STAGES];
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    int warp_sum[THREADS / 32];
+    Segments seg;
+};
+constexpr size_t kSmemBytes = sizeof(Smem) + 1024;       // + alignment slack
+static_assert(kSmemBytes <= 232448, "one CTA's shared memory");
+
+struct GemmParams {
+    const int32_t *offsets;
+    int E, rows, N, K;
+    int w_tiles;             // weight tiles of 128 * CG columns
+    int tok_cap;             // rows per unit at most (a multiple of 16 * CG)
+    int row_block;           // row units per block
+    int slot_bytes;          // ring slot: W_BYTES + this CTA's rows of a full unit
+    int stages;
+    uint8_t *out;
+    int64_t out_row_bytes;
+    int vec;                 // rows of out start on 16 bytes
+    unsigned *status;
+    uint64_t wait_ns;
+};
+
+// Four maps of the rows, for boxes of 128, 64, 32 and 16 of them.
+struct RowMaps {
+    CUtensorMap m[4];
+};
+
+struct Unit {
+    int e;
+    int row0;        // first row (in the dispatched matrix)
+    int rows;        // rows to store
+    int mma_n;       // the same rounded up to the MMA's width
+    int w0;          // first weight column of this CTA
+};
+
+template <int CG>
+__device__ __forceinline__ Unit unit_of(const Segments &S, const GemmParams &p, int unit, int rank)
+{
+    Unit u;
+    u.e = expert_of(S, p.E, unit);
+    const int cnt = S.count[u.e], local = unit - S.unit[u.e];
+    const int n_units = (cnt + p.tok_cap - 1) / p.tok_cap;
+    const int span = p.row_block * p.w_tiles;
+    const int b = local / span, rem = local - b * span;
+    const int left = n_units - b * p.row_block, width = left < p.row_block ? left : p.row_block;
+    const int wt = rem / width, j = b * p.row_block + rem - wt * width;
+    // equal widths: at most tok_cap, which is a multiple of the quantum, so
+    // that none of the n_units comes out empty
+    constexpr int Q = 16 * CG;
+    const int each = ((cnt + n_units - 1) / n_units + Q - 1) / Q * Q;
+    const int at = j * each;
+    u.rows = cnt - at < each ? cnt - at : each;
+    u.row0 = S.first[u.e] + at;
+    u.mma_n = (u.rows + Q - 1) / Q * Q;
+    u.w0 = (wt * CG + rank) * BM;
+    return u;
+}
+
+// Barrier over the four epilogue warps.
+__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// The same, true in all of them if `ok` is in all.
+__device__ __forceinline__ bool epi_all(bool ok)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)ok)
+        : "memory");
+    return r != 0;
+}
+
+template <int DT, int CG, bool KN, bool OUT_F32>
+__global__ void __launch_bounds__(THREADS, 1)
+grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_a,
+                    const GemmParams p)
+{
+    extern __shared__ uint8_t smem_raw[];
+    Smem &S = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = CG == 2 ? (int)cluster_ctarank() : 0;
+    const bool leader = rank == 0;
+    const int unit0 = (int)blockIdx.x / CG, unit_step = (int)gridDim.x / CG;
+    const int num_kb = (p.K + BK - 1) / BK;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < p.stages; ++s) { mbar_init(&S.full[s], 1); mbar_init(&S.empty[s], 1); }
+        for (int a = 0; a < 2; ++a) { mbar_init(&S.acc_full[a], 1); mbar_init(&S.acc_empty[a], 4 * CG); }
+        mbar_init(&S.drain, 1);
+        S.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        tmem_alloc<CG>(&S.tmem_base, TMEM_COLS);
+        tmem_relinquish<CG>();
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    load_segments<THREADS>(S.seg, S.warp_sum, p.offsets, p.E, p.rows, p.status,
+                           [&](int cnt) { return (cnt + p.tok_cap - 1) / p.tok_cap * p.w_tiles; });
+    tc_fence_before();
+    // a pair also makes each CTA's barrier initialisation visible to the
+    // other before any copy or arrival targets it
+    if constexpr (CG == 2) cluster_sync();
+    else __syncthreads();
+    tc_fence_after();
+
+    const uint32_t tmem_base = S.tmem_base;
+    const int total = S.seg.unit[p.E];
+    volatile int *abort_flag = &S.abort;
+    uint32_t filled_mask = 0, filled_parity = 0;       // producer: stages in flight
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------------ TMA producer
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int unit = unit0; unit < total && ok; unit += unit_step) {
+            const Unit u = unit_of<CG>(S.seg, p, unit, rank);
+            const int mine = u.mma_n / CG;               // rows this CTA loads
+            const int row0 = u.row0 + rank * mine;
+            const uint32_t bytes = W_BYTES + mine * BK * 2;
+            for (int kb = 0; kb < num_kb; ++kb) {
+                if (!mbar_wait<CG>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns)) { ok = false; break; }
+                uint8_t *sw = S.ring + stage * p.slot_bytes;
+                // both CTAs' copies complete on the leader's barrier, which
+                // expects both; a peer's copy may land before the leader arms
+                // it (the phase cannot complete while its arrival is pending)
+                if (leader) mbar_arrive_expect_tx(&S.full[stage], CG * bytes);
+                const uint32_t bar = CG == 2 ? mapa_shared(smem_u32(&S.full[stage]), 0) : 0u;
+                auto load_w = [&](void *dst, int c0, int c1) {
+                    if constexpr (CG == 2) tma_load_3d_pair(dst, &map_w, bar, c0, c1, u.e);
+                    else tma_load_3d(dst, &map_w, &S.full[stage], c0, c1, u.e);
+                };
+                if constexpr (KN) {
+                    load_w(sw, u.w0, kb * BK);
+                    load_w(sw + W_BYTES / 2, u.w0 + 64, kb * BK);
+                } else {
+                    load_w(sw, kb * BK, u.w0);
+                }
+                uint8_t *sa = sw + W_BYTES;
+                auto load_a = [&](int box, int at) {
+                    uint8_t *dst = sa + at * BK * 2;
+                    if constexpr (CG == 2) tma_load_2d_pair(dst, &map_a.m[box], bar, kb * BK, row0 + at);
+                    else tma_load_2d(dst, &map_a.m[box], &S.full[stage], kb * BK, row0 + at);
+                };
+                int at = 0;
+                for (; mine - at >= 128; at += 128) load_a(0, at);
+                if (mine & 64) { load_a(1, at); at += 64; }
+                if (mine & 32) { load_a(2, at); at += 32; }
+                if (mine & 16) load_a(3, at);
+                filled_mask |= 1u << stage;
+                filled_parity = (filled_parity & ~(1u << stage)) | (phase << stage);
+                if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+            }
+        }
+    } else if (warp == 1 && lane == 0 && leader) {
+        // ------------------------------------------------------ MMA issuer
+        constexpr uint32_t idesc0 = idesc_f16_major<DT>(BM * CG, 0, KN, false);
+        int stage = 0;
+        uint32_t phase = 0;
+        int it = 0;
+        bool ok = true;
+        for (int unit = unit0; unit < total && ok; unit += unit_step, ++it) {
+            const Unit u = unit_of<CG>(S.seg, p, unit, rank);
+            const uint32_t idesc = idesc0 | ((uint32_t)(u.mma_n >> 3) << 17);
+            const int acc = it & 1;
+            const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
+            if (!mbar_wait<CG>(&S.acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_ns)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t d = tmem_base + (uint32_t)(acc * ACC_COLS);
+            for (int kb = 0; kb < num_kb; ++kb) {
+                if (!mbar_wait<CG>(&S.full[stage], phase, abort_flag, p.status, p.wait_ns)) { ok = false; break; }
+                tc_fence_after();
+                const uint32_t w = smem_u32(S.ring + stage * p.slot_bytes), a = w + W_BYTES;
+#pragma unroll
+                for (int k = 0; k < BK / UK; ++k)
+                    umma_f16<CG>(d, KN ? sdesc_mn_sw128(w + k * UK * 128, W_BYTES / 2) : sdesc_k_sw128(w + k * UK * 2),
+                                 sdesc_k_sw128(a + k * UK * 2), idesc, (kb | k) != 0 ? 1u : 0u);
+                if constexpr (CG == 2) umma_commit_pair(&S.empty[stage]);
+                else umma_commit<1>(&S.empty[stage]);
+                if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+            }
+            if (ok) {
+                if constexpr (CG == 2) umma_commit_pair(&S.acc_full[acc]);
+                else umma_commit<1>(&S.acc_full[acc]);
+            }
+        }
+        if (*abort_flag) {
+            // every MMA issued so far must finish before TMEM is released
+            umma_commit<CG>(&S.drain);
+            mbar_wait(&S.drain, 0, nullptr, p.status, kDrainLimitNs);
+        }
+    } else if (warp >= 2) {
+        // ------------------------------------------------------ epilogue
+        const int q = warp & 3;                          // TMEM lane quadrant of this warp
+        const int tid = threadIdx.x - 64;                // 0..127
+        constexpr int CH = OUT_F32 ? 16 : 32;            // rows per staging buffer
+        constexpr int ESZ = OUT_F32 ? 4 : 2;
+        constexpr int ROW_BYTES = BM * ESZ;              // staged bytes per row: 512 / 256
+        constexpr int PIECES = ROW_BYTES / 16, PER_IT = 128 / PIECES;
+        int it = 0, buf = 0;
+        for (int unit = unit0; unit < total; unit += unit_step, ++it) {
+            const Unit u = unit_of<CG>(S.seg, p, unit, rank);
+            const int acc = it & 1;
+            const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
+            // the four warps leave together: none may wait at a barrier for
+            // one that has given up
+            if (!epi_all(mbar_wait<CG>(&S.acc_full[acc], acc_phase, abort_flag, p.status, p.wait_ns))) break;
+            tc_fence_after();
+            const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
+            const int piece = tid % PIECES, col = u.w0 + piece * (16 / ESZ);
+            uint8_t *out0 = p.out + (int64_t)u.row0 * p.out_row_bytes + (int64_t)col * ESZ;
+            const bool whole = p.vec && col + 16 / ESZ <= p.N;
+            for (int t0 = 0; t0 < u.rows; t0 += CH, buf ^= 1) {
+                uint8_t *mine = S.stg[buf] + (q * 32 + lane) * ESZ;
+                if constexpr (OUT_F32) {
+                    uint32_t v[16];
+                    tmem_ld16(tbase + t0, v);
+                    tmem_ld_wait16(v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) *reinterpret_cast<uint32_t *>(mine + i * ROW_BYTES) = v[i];
+                } else {
+                    uint32_t v[32];
+                    tmem_ld32(tbase + t0, v);
+                    tmem_ld_wait(v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const uint32_t w = pack2<DT>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+                        *reinterpret_cast<uint16_t *>(mine + 2 * i * ROW_BYTES) = (uint16_t)w;
+                        *reinterpret_cast<uint16_t *>(mine + (2 * i + 1) * ROW_BYTES) = (uint16_t)(w >> 16);
+                    }
+                }
+                if (t0 + CH >= u.rows) {
+                    // the accumulator is read: the next unit but one may have it
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (CG == 2 && !leader) mbar_arrive_cluster(mapa_shared(smem_u32(&S.acc_empty[acc]), 0));
+                        else mbar_arrive(&S.acc_empty[acc]);
+                    }
+                }
+                // one barrier per buffer: who passes it has read the other one
+                epi_sync();
+#pragma unroll
+                for (int i = 0; i < CH / PER_IT; ++i) {
+                    const int t = i * PER_IT + tid / PIECES;
+                    const uint4 v = *reinterpret_cast<const uint4 *>(S.stg[buf] + t * ROW_BYTES + piece * 16);
+                    if (t0 + t >= u.rows) continue;
+                    uint8_t *dst = out0 + (int64_t)(t0 + t) * p.out_row_bytes;
+                    if (whole) {
+                        *reinterpret_cast<uint4 *>(dst) = v;
+                    } else {
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int c = 0; c < 16 / ESZ; ++c) {
+                            if (col + c >= p.N) continue;
+                            if constexpr (OUT_F32) reinterpret_cast<uint32_t *>(dst)[c] = w[c];
+                            else reinterpret_cast<uint16_t *>(dst)[c] = (uint16_t)(w[c / 2] >> (c & 1) * 16);
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    // ------------------------------------------------------------ teardown
+    __syncthreads();
+    if (*abort_flag && warp == 0 && lane == 0) {
+        if (CG == 1 || leader) {
+            // let the outstanding TMA copies land before shared memory goes
+            for (int s = 0; s < p.stages; ++s)
+                if (filled_mask >> s & 1u)
+                    mbar_wait(&S.full[s], filled_parity >> s & 1u, nullptr, p.status, kDrainLimitNs);
+        } else {
+            // a peer's copies complete on the leader's barriers, which it
+            // cannot wait on: give them the same bounded time to land
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < kDrainLimitNs) { }
+        }
+    }
+    // a pair keeps both CTAs (their shared memory is read by the leader's
+    // MMAs and signalled by its commits) until both are done
+    if constexpr (CG == 2) cluster_sync();
+    else __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc<CG>(tmem_base, TMEM_COLS);
+    }
+}
+
+// ---- host side ---------------------------------------------------------------
+
+// Opts this kernel instance in to its shared memory, and (pairs) asks how many
+// clusters the GPU holds at once, once per device.
+template <typename Kernel>
+cudaError_t prepare_kernel(Kernel kernel, int cg, std::atomic<int> *cache, int *ctas)
+{
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const bool cached = dev >= 0 && dev < kCachedDevices;
+    int n = cached ? cache[dev].load() : 0;
+    if (n == 0) {
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
+        if (err != cudaSuccess) return err;
+        n = device_sm_count();
+        if (cg == 2) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3((unsigned)(n & ~1));
+            cfg.blockDim = dim3(THREADS);
+            cfg.dynamicSmemBytes = kSmemBytes;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 2;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int pairs = 0;
+            err = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg);
+            if (err != cudaSuccess) return err;
+            if (pairs < 1) return cudaErrorInvalidConfiguration;
+            n = 2 * pairs;
+        }
+        if (cached) cache[dev].store(n);
+    }
+    *ctas = n;
+    return cudaSuccess;
+}
+
+template <int DT, int CG, bool KN, bool OUT_F32>
+cudaError_t launch_kernel(int64_t units, const CUtensorMap &mw, const RowMaps &ma, const GemmParams &p,
+                          cudaStream_t s)
+{
+    static std::atomic<int> cache[kCachedDevices];
+    int ctas = 0;
+    cudaError_t err = prepare_kernel(grouped_gemm_kernel<DT, CG, KN, OUT_F32>, CG, cache, &ctas);
+    if (err != cudaSuccess) return err;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(CG * units < ctas ? CG * units : ctas));
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = kSmemBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = CG == 2 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, grouped_gemm_kernel<DT, CG, KN, OUT_F32>, mw, ma, p);
+}
+
+template <int DT, int CG>
+cudaError_t launch_cg(const void *a, int64_t lda, const int32_t *offsets, int64_t rows, const void *w,
+                      int E, int64_t N, int64_t K, bool kn, void *out, int64_t ldo, bool out_f32,
+                      int tok_cap, unsigned *status, cudaStream_t s)
+{
+    const CUtensorMapDataType tdt =
+        DT == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    CUtensorMap mw;
+    RowMaps ma;
+    bool ok = kn ? encode_3d(&mw, tdt, w, (uint64_t)N, (uint64_t)K, (uint64_t)E, 64, BK)
+                 : encode_3d(&mw, tdt, w, (uint64_t)K, (uint64_t)N, (uint64_t)E, BK, BM);
+    for (int i = 0; i < 4; ++i)
+        ok = ok && encode_2d_strided(&ma.m[i], tdt, a, (uint64_t)K, (uint64_t)rows, (uint64_t)lda * 2, BK, 128u >> i);
+    if (!ok) return cudaErrorInvalidValue;
+    GemmParams p{};
+    p.offsets = offsets;
+    p.E = E;
+    p.rows = (int)rows;
+    p.N = (int)N;
+    p.K = (int)K;
+    p.w_tiles = (int)((N + BM * CG - 1) / (BM * CG));
+    p.tok_cap = tok_cap;
+    const int64_t block = kRowBlockBytes / (tok_cap * K * 2), most = (rows + tok_cap - 1) / tok_cap;
+    p.row_block = (int)(block < 1 ? 1 : block > most ? most : block);
+    p.slot_bytes = W_BYTES + tok_cap / CG * BK * 2;
+    p.stages = RING_BYTES / p.slot_bytes < MAX_STAGES ? RING_BYTES / p.slot_bytes : MAX_STAGES;
+    p.out = static_cast<uint8_t *>(out);
+    p.out_row_bytes = ldo * (out_f32 ? 4 : 2);
+    p.vec = p.out_row_bytes % 16 == 0;
+    p.status = status;
+    p.wait_ns = wait_limit_ns();
+    // an upper bound: every expert adds at most one unit that is not full
+    const int64_t units = (rows / tok_cap + (rows < E ? rows : E)) * p.w_tiles;
+    if (out_f32)
+        return kn ? launch_kernel<DT, CG, true, true>(units, mw, ma, p, s)
+                  : launch_kernel<DT, CG, false, true>(units, mw, ma, p, s);
+    return kn ? launch_kernel<DT, CG, true, false>(units, mw, ma, p, s)
+              : launch_kernel<DT, CG, false, false>(units, mw, ma, p, s);
+}
+
+template <int DT>
+cudaError_t launch_dt(const void *a, int64_t lda, const int32_t *offsets, int64_t rows, const void *w,
+                      int E, int64_t N, int64_t K, bool kn, void *out, int64_t ldo, bool out_f32,
+                      unsigned *status, cudaStream_t s)
+{
+    if (rows >= 192 * (int64_t)E)
+        return launch_cg<DT, 2>(a, lda, offsets, rows, w, E, N, K, kn, out, ldo, out_f32, 256, status, s);
+    return launch_cg<DT, 1>(a, lda, offsets, rows, w, E, N, K, kn, out, ldo, out_f32,
+                            rows >= 32 * (int64_t)E ? 128 : 64, status, s);
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_gemm_tc(int dt, const void *a, int64_t lda, const int32_t *offsets,
+                                   int64_t rows, const void *w, int E, int64_t N, int64_t K,
+                                   bool transposed, void *out, int64_t ldo, bool out_f32,
+                                   unsigned *status, cudaStream_t s)
+{
+    if (dt == DT_BF16)
+        return launch_dt<DT_BF16>(a, lda, offsets, rows, w, E, N, K, transposed, out, ldo, out_f32, status, s);
+    return launch_dt<DT_F16>(a, lda, offsets, rows, w, E, N, K, transposed, out, ldo, out_f32, status, s);
+}
+
+}  // namespace moe

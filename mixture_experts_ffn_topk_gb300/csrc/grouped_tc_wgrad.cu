@@ -1,0 +1,477 @@
+// grouped_tc_wgrad.cu -- weight gradient of a grouped product on tcgen05.
+//
+//   grad_w[e][n, k] (+)= sum over the rows r of expert e of grad[r, n] a[r, k]
+//
+// BF16 / F16 operands, FP32 accumulation in tensor memory, FP32 or 16-bit
+// output. Both operands are read across their rows: TMA boxes of 64 columns
+// (128 bytes) by 64 rows, 128-byte swizzle, described to the MMA as MN-major.
+// An expert's rows start and end anywhere, so its last box of 64 rows runs
+// into the next expert's. The MMA reduces 16 rows at a time: steps past the
+// segment are left out, and the at most 15 foreign rows of the last step are
+// set to zero in shared memory, in both operands (a NaN there would survive
+// a zero in one), by a warp that stands between that stage's copies and its
+// MMAs. No tensor map depends on the offsets, no workspace is needed.
+//
+// Per CTA (one per SM, 224 threads, persistent over the units):
+//   warp 0     TMA producer: 128 columns of grad (16 KiB) and 256 / CG of a;
+//   warp 1     tcgen05.mma issuer, M = 128 * CG by N = up to 256;
+//   warps 2-5  epilogue: 32 rows x 128 bytes at a time through a swizzled
+//              staging buffer, so that stores write whole lines;
+//   warp 6     zeroes foreign rows of a segment's last stage.
+// CTA pairs (CG = 2): M = 256, each CTA holds 128 columns of grad and half of
+// a's; the even CTA issues the MMAs.
+// Units run over (expert, tile of the wider matrix, tile of the narrower one),
+// the last fastest: the narrower operand's segment stays in L2 while the wider
+// one passes once.
+//
+// Every wait is bounded, as in grouped_tc.cu.
+#include <atomic>
+
+#include "common.cuh"
+#include "grouped.cuh"
+#include "kernels.h"
+#include "tc_ptx.cuh"
+
+namespace moe {
+
+namespace {
+
+constexpr int BM = 128;                  // rows of grad_w per CTA
+constexpr int BN = 256;                  // columns of grad_w per unit
+constexpr int BK = 64;                   // rows reduced per stage
+constexpr int UK = 16;                   // rows reduced per tcgen05.mma
+constexpr int BOX_BYTES = 64 * BK * 2;   // 64 columns x 64 rows
+constexpr int G_BYTES = 2 * BOX_BYTES;
+template <int CG>
+constexpr int SLOT_BYTES = G_BYTES + 4 / CG * BOX_BYTES;
+template <int CG>
+constexpr int STAGES = CG == 2 ? 6 : 4;
+constexpr int ACC_COLS = 256;
+constexpr int TMEM_COLS = 2 * ACC_COLS;
+constexpr int THREADS = 224;
+constexpr int STG_ROW_BYTES = 128;
+constexpr uint64_t kDrainLimitNs = 100000000ull;
+
+template <int CG>
+struct __align__(1024) Smem {
+    uint8_t ring[STAGES<CG>][SLOT_BYTES<CG>];
+    uint8_t stg[4][32 * STG_ROW_BYTES];
+    uint64_t full[STAGES<CG>];
+    uint64_t empty[STAGES<CG>];
+    uint64_t tail_in[STAGES<CG>];        // this CTA's copies of a stage with foreign rows
+    uint64_t tail_out[STAGES<CG>];       // (leader) the rows of both CTAs are zeroed
+    uint64_t acc_full[2];
+    uint64_t acc_empty[2];
+    uint64_t drain;
+    uint32_t tmem_base;
+    int abort;
+    int warp_sum[THREADS / 32];
+    Segments seg;
+};
+template <int CG>
+constexpr size_t kSmemBytes = sizeof(Smem<CG>) + 1024;   // + alignment slack
+static_assert(kSmemBytes<1> <= 232448 && kSmemBytes<2> <= 232448, "one CTA's shared memory");
+
+struct WgradParams {
+    const int32_t *offsets;
+    int E, rows, N, K;
+    int n_tiles, k_tiles;
+    int n_fast;              // the n tile runs fastest (grad is the narrower operand)
+    uint8_t *out;
+    int64_t out_row_bytes;
+    int accumulate;
+    unsigned *status;
+    uint64_t wait_ns;
+};
+
+struct Unit {
+    int e, row0, cnt;        // expert, its first row and number of rows
+    int nkb;                 // stages: blocks of 64 rows
+    int tail;                // rows of the last block that are the expert's
+    int n0;                  // this CTA's first row of grad_w
+    int k0, mma_n;           // the unit's columns of grad_w, and how wide the MMA is
+};
+
+template <int CG>
+__device__ __forceinline__ Unit unit_of(const Segments &S, const WgradParams &p, int unit, int rank)
+{
+    Unit u;
+    const int per = p.n_tiles * p.k_tiles;
+    u.e = unit / per;
+    const int rem = unit - u.e * per;
+    const int nt = p.n_fast ? rem % p.n_tiles : rem / p.k_tiles;
+    const int kt = p.n_fast ? rem / p.n_tiles : rem % p.k_tiles;
+    u.row0 = S.first[u.e];
+    u.cnt = S.count[u.e];
+    u.nkb = (u.cnt + BK - 1) / BK;
+    u.tail = u.cnt - (u.nkb - 1) * BK;
+    u.n0 = (nt * CG + rank) * BM;
+    u.k0 = kt * BN;
+    // whole 64-column boxes for each CTA: an MN-major operand's 128-byte rows
+    const int left = p.K - u.k0;
+    u.mma_n = left >= BN ? BN : (left + 64 * CG - 1) / (64 * CG) * (64 * CG);
+    return u;
+}
+
+template <int DT, int CG, bool OUT_F32>
+__global__ void __launch_bounds__(THREADS, 1)
+grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_a,
+                     const WgradParams p)
+{
+    constexpr int NS = STAGES<CG>;
+    extern __shared__ uint8_t smem_raw[];
+    Smem<CG> &S = *reinterpret_cast<Smem<CG> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = CG == 2 ? (int)cluster_ctarank() : 0;
+    const bool leader = rank == 0;
+    const int unit0 = (int)blockIdx.x / CG, unit_step = (int)gridDim.x / CG;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < NS; ++s) {
+            mbar_init(&S.full[s], 1);
+            mbar_init(&S.empty[s], 1);
+            mbar_init(&S.tail_in[s], 1);
+            mbar_init(&S.tail_out[s], CG);
+        }
+        for (int a = 0; a < 2; ++a) { mbar_init(&S.acc_full[a], 1); mbar_init(&S.acc_empty[a], 4 * CG); }
+        mbar_init(&S.drain, 1);
+        S.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 1) {
+        tmem_alloc<CG>(&S.tmem_base, TMEM_COLS);
+        tmem_relinquish<CG>();
+    }
+    pdl_wait();
+    pdl_launch_dependents();
+    load_segments<THREADS>(S.seg, S.warp_sum, p.offsets, p.E, p.rows, p.status,
+                           [&](int) { return p.n_tiles * p.k_tiles; });
+    tc_fence_before();
+    // a pair also makes each CTA's barrier initialisation visible to the
+    // other before any copy or arrival targets it
+    if constexpr (CG == 2) cluster_sync();
+    else __syncthreads();
+    tc_fence_after();
+
+    const uint32_t tmem_base = S.tmem_base;
+    const int total = p.E * p.n_tiles * p.k_tiles;
+    volatile int *abort_flag = &S.abort;
+    // producer: stages in flight, their parities, and (tails) on which barrier
+    uint32_t filled_mask = 0, filled_parity = 0, tail_mask = 0, tail_parity = 0;
+
+    if (warp == 0 && lane == 0) {
+        // ------------------------------------------------------ TMA producer
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int unit = unit0; unit < total && ok; unit += unit_step) {
+            const Unit u = unit_of<CG>(S.seg, p, unit, rank);
+            const int mine = u.mma_n / CG;                    // columns of a this CTA loads
+            const int boxes = mine / 64, col0 = u.k0 + rank * mine;
+            const uint32_t bytes = G_BYTES + boxes * BOX_BYTES;
+            for (int kb = 0; kb < u.nkb; ++kb) {
+                if (!mbar_wait<CG>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns)) { ok = false; break; }
+                uint8_t *sg = S.ring[stage];
+                // a stage with foreign rows completes in its own CTA, where
+                // warp 6 zeroes them; any other on the leader's barrier, which
+                // expects both CTAs' bytes (a peer's copy may land before the
+                // leader arms it: the phase cannot complete while its arrival
+                // is pending)
+                const bool tail = kb == u.nkb - 1 && u.tail % UK != 0;
+                const uint32_t bit = 1u << stage;
+                if (tail) {
+                    mbar_arrive_expect_tx(&S.tail_in[stage], bytes);
+                    if (leader) mbar_arrive(&S.full[stage]);
+                    tail_mask |= bit;
+                    tail_parity ^= bit;           // set while an odd use (parity 0) is in flight
+                } else {
+                    if (leader) mbar_arrive_expect_tx(&S.full[stage], CG * bytes);
+                    tail_mask &= ~bit;
+                }
+                uint64_t *local = tail ? &S.tail_in[stage] : &S.full[stage];
+                const uint32_t bar = CG == 2 ? mapa_shared(smem_u32(local), tail ? (uint32_t)rank : 0u) : 0u;
+                auto load = [&](void *dst, const CUtensorMap *m, int c) {
+                    if constexpr (CG == 2) tma_load_2d_pair(dst, m, bar, c, u.row0 + kb * BK);
+                    else tma_load_2d(dst, m, local, c, u.row0 + kb * BK);
+                };
+                load(sg, &map_g, u.n0);
+                load(sg + BOX_BYTES, &map_g, u.n0 + 64);
+                for (int j = 0; j < boxes; ++j) load(sg + G_BYTES + j * BOX_BYTES, &map_a, col0 + j * 64);
+                filled_mask |= bit;
+                filled_parity = (filled_parity & ~bit) | (phase << stage);
+                if (++stage == NS) { stage = 0; phase ^= 1u; }
+            }
+        }
+    } else if (warp == 1 && lane == 0 && leader) {
+        // ------------------------------------------------------ MMA issuer
+        constexpr uint32_t idesc0 = idesc_f16_major<DT>(BM * CG, 0, true, true);
+        int stage = 0;
+        uint32_t phase = 0, tails = 0;
+        int it = 0;
+        bool ok = true;
+        for (int unit = unit0; unit < total && ok; unit += unit_step, ++it) {
+            const Unit u = unit_of<CG>(S.seg, p, unit, rank);
+            const uint32_t idesc = idesc0 | ((uint32_t)(u.mma_n >> 3) << 17);
+            const int acc = it & 1;
+            const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
+            if (!mbar_wait<CG>(&S.acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_ns)) { ok = false; break; }
+            tc_fence_after();
+            const uint32_t d = tmem_base + (uint32_t)(acc * ACC_COLS);
+            for (int kb = 0; kb < u.nkb; ++kb) {
+                if (!mbar_wait<CG>(&S.full[stage], phase, abort_flag, p.status, p.wait_ns)) { ok = false; break; }
+                const int valid = kb == u.nkb - 1 ? u.tail : BK;
+                if (valid % UK != 0) {
+                    if (!mbar_wait<CG>(&S.tail_out[stage], tails >> stage & 1u, abort_flag, p.status, p.wait_ns)) { ok = false; break; }
+                    tails ^= 1u << stage;
+                }
+                tc_fence_after();
+                const uint32_t g = smem_u32(S.ring[stage]), a = g + G_BYTES;
+                const int steps = (valid + UK - 1) / UK;
+                for (int k = 0; k < steps; ++k)
+                    umma_f16<CG>(d, sdesc_mn_sw128(g + k * UK * 128, BOX_BYTES),
+                                 sdesc_mn_sw128(a + k * UK * 128, BOX_BYTES), idesc, (kb | k) != 0 ? 1u : 0u);
+                if constexpr (CG == 2) umma_commit_pair(&S.empty[stage]);
+                else umma_commit<1>(&S.empty[stage]);
+                if (++stage == NS) { stage = 0; phase ^= 1u; }
+            }
+            // (an expert without rows commits with no MMA: its epilogue writes zeros)
+            if (ok) {
+                if constexpr (CG == 2) umma_commit_pair(&S.acc_full[acc]);
+                else umma_commit<1>(&S.acc_full[acc]);
+            }
+        }
+        if (*abort_flag) {
+            // every MMA issued so far must finish before TMEM is released
+            umma_commit<CG>(&S.drain);
+            mbar_wait(&S.drain, 0, nullptr, p.status, kDrainLimitNs);
+        }
+    } else if (warp == 6) {
+        // ------------------------------------------------------ foreign rows
+        int stage = 0;
+        uint32_t tails = 0;
+        for (int unit = unit0; unit < total; unit += unit_step) {
+            const Unit u = unit_of<CG>(S.seg, p, unit, rank);
+            if (u.nkb == 0) continue;
+            stage = (stage + u.nkb - 1) % NS;                 // the unit's last stage
+            if (u.tail % UK != 0) {
+                const bool ready = mbar_wait<CG>(&S.tail_in[stage], tails >> stage & 1u, abort_flag, p.status, p.wait_ns);
+                if (!__all_sync(0xffffffffu, ready)) break;
+                tails ^= 1u << stage;
+                // whole 128-byte rows of every box: the swizzle stays inside a row
+                const int nrows = UK - u.tail % UK;
+                const int boxes = 2 + u.mma_n / CG / 64;
+                for (int i = lane; i < boxes * nrows * 8; i += 32) {
+                    const int box = i / (nrows * 8), c = i - box * (nrows * 8);
+                    *reinterpret_cast<uint4 *>(S.ring[stage] + box * BOX_BYTES + u.tail * 128 + c * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                }
+                // the MMA reads shared memory through the async proxy
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    if (CG == 2 && !leader) mbar_arrive_cluster(mapa_shared(smem_u32(&S.tail_out[stage]), 0));
+                    else mbar_arrive(&S.tail_out[stage]);
+                }
+            }
+            if (++stage == NS) stage = 0;
+        }
+    } else if (warp >= 2) {
+        // ------------------------------------------------------ epilogue
+        const int q = warp & 3;                    // TMEM lane quadrant of this warp
+        uint8_t *stg = S.stg[warp - 2];
+        constexpr int ESZ = OUT_F32 ? 4 : 2;
+        constexpr int COLS = STG_ROW_BYTES / ESZ;  // columns per round: 32 / 64
+        const int cch = lane & 7;
+        int it = 0;
+        for (int unit = unit0; unit < total; unit += unit_step, ++it) {
+            const Unit u = unit_of<CG>(S.seg, p, unit, rank);
+            const int acc = it & 1;
+            const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
+            const bool ready = mbar_wait<CG>(&S.acc_full[acc], acc_phase, abort_flag, p.status, p.wait_ns);
+            if (!__all_sync(0xffffffffu, ready)) break;
+            tc_fence_after();
+            const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
+            const int row0 = u.n0 + q * 32, rows_valid = p.N - row0;
+            uint8_t *base = p.out + ((int64_t)u.e * p.N + row0) * p.out_row_bytes;
+            const bool empty = u.cnt == 0;
+            const int width = p.K - u.k0 < BN ? p.K - u.k0 : BN;
+            for (int c0 = 0; c0 < width && !(empty && p.accumulate); c0 += COLS) {
+                float v[COLS];
+#pragma unroll
+                for (int h = 0; h < COLS / 32; ++h) {
+                    uint32_t r[32];
+                    tmem_ld32(tbase + c0 + h * 32, r);
+                    tmem_ld_wait(r);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[h * 32 + i] = empty ? 0.0f : __uint_as_float(r[i]);
+                }
+                const int64_t col_byte = (int64_t)(u.k0 + c0) * ESZ;
+                if (p.accumulate && lane < rows_valid) {
+                    const uint8_t *old = base + lane * p.out_row_bytes + col_byte;
+#pragma unroll
+                    for (int c = 0; c < 8; ++c) {
+                        if (col_byte + c * 16 >= p.out_row_bytes) continue;
+                        Vec16 o;
+                        o.u = *reinterpret_cast<const uint4 *>(old + c * 16);
+                        if constexpr (OUT_F32) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) v[c * 4 + i] += o.f[i];
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 f = DT == DT_BF16 ? bf16x2_to_float2(o.w[i]) : f16x2_to_float2(o.w[i]);
+                                v[c * 8 + 2 * i] += f.x;
+                                v[c * 8 + 2 * i + 1] += f.y;
+                            }
+                        }
+                    }
+                }
+                // this lane's row into the staging buffer, its 16-byte pieces
+                // rotated by the row so that neither side meets bank conflicts
+#pragma unroll
+                for (int c = 0; c < 8; ++c) {
+                    Vec16 o;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (OUT_F32) o.f[i] = v[c * 4 + i];
+                        else o.w[i] = pack2<DT>(v[c * 8 + 2 * i], v[c * 8 + 2 * i + 1]);
+                    }
+                    *reinterpret_cast<uint4 *>(stg + lane * STG_ROW_BYTES + ((c ^ (lane & 7)) << 4)) = o.u;
+                }
+                __syncwarp();
+                const int64_t cb = col_byte + cch * 16;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int rr = 4 * j + (lane >> 3);
+                    const uint4 o = *reinterpret_cast<const uint4 *>(stg + rr * STG_ROW_BYTES + ((cch ^ (rr & 7)) << 4));
+                    if (rr < rows_valid && cb < p.out_row_bytes)
+                        *reinterpret_cast<uint4 *>(base + rr * p.out_row_bytes + cb) = o;
+                }
+                __syncwarp();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2 && !leader) mbar_arrive_cluster(mapa_shared(smem_u32(&S.acc_empty[acc]), 0));
+                else mbar_arrive(&S.acc_empty[acc]);
+            }
+        }
+    }
+
+    // ------------------------------------------------------------ teardown
+    __syncthreads();
+    if (*abort_flag && warp == 0 && lane == 0) {
+        // let the outstanding TMA copies land before shared memory goes
+        for (int s = 0; s < NS; ++s)
+            if ((filled_mask >> s & 1u) && (tail_mask >> s & 1u))
+                mbar_wait(&S.tail_in[s], (tail_parity >> s & 1u) ^ 1u, nullptr, p.status, kDrainLimitNs);
+            else if ((filled_mask >> s & 1u) && leader)
+                mbar_wait(&S.full[s], filled_parity >> s & 1u, nullptr, p.status, kDrainLimitNs);
+        if (!leader) {
+            // a peer's other copies complete on the leader's barriers, which
+            // it cannot wait on: give them the same bounded time to land
+            const uint64_t t0 = global_timer_ns();
+            while (global_timer_ns() - t0 < kDrainLimitNs) { }
+        }
+    }
+    // a pair keeps both CTAs (their shared memory is read by the leader's
+    // MMAs and signalled by its commits) until both are done
+    if constexpr (CG == 2) cluster_sync();
+    else __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tc_fence_after();
+        tmem_dealloc<CG>(tmem_base, TMEM_COLS);
+    }
+}
+
+// ---- host side ---------------------------------------------------------------
+
+template <int DT, int CG, bool OUT_F32>
+cudaError_t launch_kernel(const CUtensorMap &mg, const CUtensorMap &ma, WgradParams p, cudaStream_t s)
+{
+    // CTAs the GPU holds at once, per device; 0: the kernel is not yet opted
+    // in to its shared memory there
+    static std::atomic<int> cache[kCachedDevices];
+    auto kernel = grouped_wgrad_kernel<DT, CG, OUT_F32>;
+    p.n_tiles = (p.N + BM * CG - 1) / (BM * CG);
+    p.k_tiles = (p.K + BN - 1) / BN;
+    p.n_fast = p.N <= p.K;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = kSmemBytes<CG>;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const bool cached = dev >= 0 && dev < kCachedDevices;
+    int ctas = cached ? cache[dev].load() : 0;
+    if (ctas == 0) {
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<CG>);
+        if (err != cudaSuccess) return err;
+        ctas = device_sm_count();
+        if (CG == 2) {
+            int pairs = 0;
+            cfg.gridDim = dim3((unsigned)(ctas & ~1));
+            cfg.numAttrs = 1;
+            err = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg);
+            if (err != cudaSuccess) return err;
+            if (pairs < 1) return cudaErrorInvalidConfiguration;
+            ctas = 2 * pairs;
+        }
+        if (cached) cache[dev].store(ctas);
+    }
+    const int64_t units = (int64_t)p.E * p.n_tiles * p.k_tiles;
+    cfg.gridDim = dim3((unsigned)(CG * units < ctas ? CG * units : ctas));
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, mg, ma, p);
+}
+
+template <int DT>
+cudaError_t launch_dt(const void *grad, int64_t ldg, const void *a, int64_t lda, const int32_t *offsets,
+                      int64_t rows, int E, int64_t N, int64_t K, void *grad_w, bool out_f32,
+                      bool accumulate, unsigned *status, cudaStream_t s)
+{
+    const CUtensorMapDataType tdt =
+        DT == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
+    CUtensorMap mg, ma;
+    if (!encode_2d_strided(&mg, tdt, grad, (uint64_t)N, (uint64_t)rows, (uint64_t)ldg * 2, 64, BK) ||
+        !encode_2d_strided(&ma, tdt, a, (uint64_t)K, (uint64_t)rows, (uint64_t)lda * 2, 64, BK))
+        return cudaErrorInvalidValue;
+    WgradParams p{};
+    p.offsets = offsets;
+    p.E = E;
+    p.rows = (int)rows;
+    p.N = (int)N;
+    p.K = (int)K;
+    p.out = static_cast<uint8_t *>(grad_w);
+    p.out_row_bytes = K * (out_f32 ? 4 : 2);
+    p.accumulate = accumulate;
+    p.status = status;
+    p.wait_ns = wait_limit_ns();
+    if (rows >= 1024 * (int64_t)E)
+        return out_f32 ? launch_kernel<DT, 2, true>(mg, ma, p, s) : launch_kernel<DT, 2, false>(mg, ma, p, s);
+    return out_f32 ? launch_kernel<DT, 1, true>(mg, ma, p, s) : launch_kernel<DT, 1, false>(mg, ma, p, s);
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_weight_grad_tc(int dt, const void *grad, int64_t ldg, const void *a,
+                                          int64_t lda, const int32_t *offsets, int64_t rows, int E,
+                                          int64_t N, int64_t K, void *grad_w, bool out_f32,
+                                          bool accumulate, unsigned *status, cudaStream_t s)
+{
+    if (dt == DT_BF16)
+        return launch_dt<DT_BF16>(grad, ldg, a, lda, offsets, rows, E, N, K, grad_w, out_f32, accumulate, status, s);
+    return launch_dt<DT_F16>(grad, ldg, a, lda, offsets, rows, E, N, K, grad_w, out_f32, accumulate, status, s);
+}
+
+}  // namespace moe

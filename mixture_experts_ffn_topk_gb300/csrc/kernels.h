@@ -206,16 +206,25 @@ cudaError_t launch_finalize(const float *y_acc, int64_t T, int64_t H, void *y, i
 
 // Grouped products of dispatched rows with one matrix per expert:
 // out[r] = a[r] w[e]^T (w [E, N, K]) or a[r] w[e] (transposed: w [E, K, N]).
-// Rows of a lie lda elements apart, rows of out (odt: dt or F32) ldo.
-cudaError_t launch_grouped_gemm_simt(int dt, const void *a, int64_t lda, const int32_t *offsets,
-                                     int64_t rows, const void *w, int E, int64_t N, int64_t K,
-                                     bool transposed, void *out, int64_t ldo, int odt,
-                                     unsigned *status, cudaStream_t s);
-// grad_w[e] (+)= sum over the expert's rows of grad[r]^T a[r], [E, N, K] in odt.
-cudaError_t launch_grouped_weight_grad_simt(int dt, const void *grad, int64_t ldg, const void *a,
+// Rows of a lie lda elements apart, rows of out ldo. F32 on CUDA cores.
+cudaError_t launch_grouped_gemm_simt(const float *a, int64_t lda, const int32_t *offsets,
+                                     int64_t rows, const float *w, int E, int64_t N, int64_t K,
+                                     bool transposed, float *out, int64_t ldo, unsigned *status,
+                                     cudaStream_t s);
+// BF16 / F16 on tcgen05 (cudaErrorInvalidValue: a tensor map was refused).
+cudaError_t launch_grouped_gemm_tc(int dt, const void *a, int64_t lda, const int32_t *offsets,
+                                   int64_t rows, const void *w, int E, int64_t N, int64_t K,
+                                   bool transposed, void *out, int64_t ldo, bool out_f32,
+                                   unsigned *status, cudaStream_t s);
+// grad_w[e] (+)= sum over the expert's rows of grad[r]^T a[r], [E, N, K].
+cudaError_t launch_grouped_weight_grad_simt(const float *grad, int64_t ldg, const float *a,
                                             int64_t lda, const int32_t *offsets, int64_t rows,
-                                            int E, int64_t N, int64_t K, void *grad_w, int odt,
+                                            int E, int64_t N, int64_t K, float *grad_w,
                                             bool accumulate, unsigned *status, cudaStream_t s);
+cudaError_t launch_grouped_weight_grad_tc(int dt, const void *grad, int64_t ldg, const void *a,
+                                          int64_t lda, const int32_t *offsets, int64_t rows, int E,
+                                          int64_t N, int64_t K, void *grad_w, bool out_f32,
+                                          bool accumulate, unsigned *status, cudaStream_t s);
 
 // SwiGLU with the 8-bit checkpoint of g and u (planes inside ckpt, byte
 // offsets), and its backward. end: offsets + E, or nullptr for all rows.

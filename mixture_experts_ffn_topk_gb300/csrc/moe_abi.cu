@@ -985,9 +985,18 @@ int moe_grouped_gemm(const void *a, int64_t lda, const int32_t *offsets, int64_t
     if (rc != MOE_OK) return rc;
     unsigned *st = status_ptr();
     if (!st) return fail(MOE_ERR_CUDA, "cannot resolve the device status word");
-    cudaError_t err = launch_grouped_gemm_simt(dtype, a, lda, offsets, rows, w, (int)E, N, K,
-                                               weight_layout == MOE_WEIGHT_KN, out, ldo, out_dtype,
-                                               st, static_cast<cudaStream_t>(stream));
+    const bool kn = weight_layout == MOE_WEIGHT_KN;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t err;
+    if (dtype == MOE_F32) {
+        err = launch_grouped_gemm_simt(static_cast<const float *>(a), lda, offsets, rows,
+                                       static_cast<const float *>(w), (int)E, N, K, kn,
+                                       static_cast<float *>(out), ldo, st, s);
+    } else {
+        err = launch_grouped_gemm_tc(dtype, a, lda, offsets, rows, w, (int)E, N, K, kn, out, ldo,
+                                     out_dtype == MOE_F32, st, s);
+        if (err == cudaErrorInvalidValue) return fail(MOE_ERR_SHAPE, "TMA descriptor rejected (matrix too large)");
+    }
     return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_grouped_gemm");
 }
 
@@ -1019,8 +1028,15 @@ int moe_grouped_gemm_weight_grad(const void *grad, int64_t ldg, const void *a, i
     if (rc != MOE_OK) return rc;
     unsigned *st = status_ptr();
     if (!st) return fail(MOE_ERR_CUDA, "cannot resolve the device status word");
-    err = launch_grouped_weight_grad_simt(dtype, grad, ldg, a, lda, offsets, rows, (int)E, N, K,
-                                          grad_w, grad_dtype, accumulate != 0, st, s);
+    if (dtype == MOE_F32) {
+        err = launch_grouped_weight_grad_simt(static_cast<const float *>(grad), ldg,
+                                              static_cast<const float *>(a), lda, offsets, rows, (int)E,
+                                              N, K, static_cast<float *>(grad_w), accumulate != 0, st, s);
+    } else {
+        err = launch_grouped_weight_grad_tc(dtype, grad, ldg, a, lda, offsets, rows, (int)E, N, K,
+                                            grad_w, grad_dtype == MOE_F32, accumulate != 0, st, s);
+        if (err == cudaErrorInvalidValue) return fail(MOE_ERR_SHAPE, "TMA descriptor rejected (matrix too large)");
+    }
     return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_grouped_gemm_weight_grad");
 }
 
