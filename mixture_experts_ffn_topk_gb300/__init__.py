@@ -782,37 +782,52 @@ def moe_experts_backward(x_disp: torch.Tensor, offsets: torch.Tensor, gate: torc
 
 # ---- grouped products and the 8-bit SwiGLU checkpoint -----------------------
 # These calls run on the device of their tensors, whatever the current device
-# is; stream (default: that device's current stream) must belong to it.
+# is; stream (default: that device's current stream) must belong to it. A call
+# on a few rows lasts a few microseconds on the GPU, so the checks are kept to
+# attribute reads and integer comparisons: 5 to 9 us of host time per call.
 
-def _on(dev, stream, call):
-    """call(stream handle) with ``dev`` current."""
-    if dev.type != "cuda":
-        raise ValueError("tensors passed to the C ABI must live on a CUDA device")
-    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _enqueue(name: str, dev: torch.device, stream, *args):
+    """Calls the C entry point with ``dev`` current and its stream last."""
+    fn = getattr(_lib or load_library(), name)
+    if stream is not None and isinstance(stream, torch.cuda.Stream) and stream.device != dev:
         raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
-    if dev.index == torch.cuda.current_device():
-        return call(_stream(stream))
-    with torch.cuda.device(dev):
-        return call(_stream(stream))
+    index = dev.index
+    if index == torch.cuda.current_device():
+        rc = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
+    if rc != 0:
+        _check(rc, name)
 
 
-def _rows(name: str, t: torch.Tensor, shape, dtype, dev) -> int:
+def _cuda(t: torch.Tensor) -> torch.device:
+    if not t.is_cuda:
+        raise ValueError("tensors passed to the C ABI must live on a CUDA device")
+    return t.device
+
+
+def _ld(name: str, t: torch.Tensor, rows: int, cols: int, dtype, dev) -> int:
     """Checks a matrix of dispatched rows; returns its row stride."""
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev:
-        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)} on {dev}, not "
+    if t.dim() != 2 or t.size(0) != rows or t.size(1) != cols or t.dtype != dtype or t.device != dev:
+        raise ValueError(f"{name} must be {dtype} of shape {(rows, cols)} on {dev}, not "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    rows, cols = shape
-    if cols > 1 and rows > 0 and t.stride(1) != 1:
+    ld, unit = t.stride()
+    if unit != 1 and cols > 1 and rows > 0:
         raise ValueError(f"{name} must have contiguous rows (any row stride)")
-    return t.stride(0) if rows > 1 else max(cols, 1)
+    return ld if rows > 1 else cols
 
 
-def _offsets(offsets: torch.Tensor, dev) -> int:
+def _experts(offsets: torch.Tensor, dev) -> int:
     """Checks expert offsets; returns the number of experts."""
-    if (offsets.dtype != torch.int32 or offsets.dim() != 1 or offsets.numel() < 2 or
-            not offsets.is_contiguous() or offsets.device != dev):
+    n = offsets.numel()
+    if (offsets.dtype != torch.int32 or offsets.dim() != 1 or n < 2 or offsets.device != dev or
+            not offsets.is_contiguous()):
         raise ValueError(f"offsets must be contiguous int32 of shape [E + 1] on {dev}")
-    return offsets.numel() - 1
+    return n - 1
 
 
 def moe_grouped_gemm(a: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
@@ -823,22 +838,26 @@ def moe_grouped_gemm(a: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
     Returns ``out [rows, N]`` in ``out_dtype`` (default: a's dtype;
     ``torch.float32`` keeps the FP32 sums). ``a`` and ``out`` may be columns
     of wider matrices. Rows past ``offsets[E]`` are left as they were."""
+    dev, dt = _cuda(a), a.dtype
     rows, K = a.shape
-    dev = a.device
-    E = _offsets(offsets, dev)
-    N = w.shape[2 if transposed else 1] if w.dim() == 3 else -1
-    if tuple(w.shape) != ((E, K, N) if transposed else (E, N, K)) or w.dtype != a.dtype or w.device != dev:
-        raise ValueError(f"w must be {a.dtype} of shape {('[E, K, N]' if transposed else '[E, N, K]')}, "
-                         f"E = {E}, K = {K}, on {dev}, not {w.dtype} {tuple(w.shape)} on {w.device}")
+    E = _experts(offsets, dev)
+    if w.dim() != 3 or w.dtype != dt or w.device != dev or not w.is_contiguous():
+        raise ValueError(f"w must be a contiguous {dt} tensor of three dimensions on {dev}")
+    e, N, k = w.shape
+    if transposed:
+        N, k = k, N
+    if e != E or k != K:
+        raise ValueError(f"w must be {'[E, K, N]' if transposed else '[E, N, K]'} with E = {E} and "
+                         f"K = {K}, not {tuple(w.shape)}")
+    lda = _ld("a", a, rows, K, dt, dev)
     if out is None:
-        out = torch.empty((rows, N), dtype=out_dtype or a.dtype, device=dev)
-    lda = _rows("a", a, (rows, K), a.dtype, dev)
-    ldo = _rows("out", out, (rows, N), out.dtype if out_dtype is None else out_dtype, dev)
-    rc = _on(dev, stream, lambda s: load_library().moe_grouped_gemm(
-        a.data_ptr(), lda, offsets.data_ptr(), rows, _ptr(w),
-        MOE_WEIGHT_KN if transposed else MOE_WEIGHT_NK, E, N, K, _code(a.dtype), out.data_ptr(),
-        ldo, _code(out.dtype), s))
-    _check(rc, "moe_grouped_gemm")
+        out = torch.empty((rows, N), dtype=out_dtype or dt, device=dev)
+        ldo = N
+    else:
+        ldo = _ld("out", out, rows, N, out_dtype or out.dtype, dev)
+    _enqueue("moe_grouped_gemm", dev, stream, a.data_ptr(), lda, offsets.data_ptr(), rows,
+             w.data_ptr(), MOE_WEIGHT_KN if transposed else MOE_WEIGHT_NK, E, N, K, _code(dt),
+             out.data_ptr(), ldo, _code(out.dtype))
     return out
 
 
@@ -850,23 +869,22 @@ def moe_grouped_gemm_weight_grad(grad: torch.Tensor, a: torch.Tensor, offsets: t
     ``a [rows, K]``), in ``grad_dtype`` (default FP32); zeros for an expert
     without rows. ``accumulate`` adds to the given ``grad_w``. For ``[E, K, N]``
     weights exchange ``grad`` and ``a``."""
+    dev, dt = _cuda(grad), grad.dtype
     rows, N = grad.shape
-    K = a.shape[1]
-    dev = grad.device
-    E = _offsets(offsets, dev)
+    K = a.shape[-1]
+    E = _experts(offsets, dev)
+    ldg = _ld("grad", grad, rows, N, dt, dev)
+    lda = _ld("a", a, rows, K, dt, dev)
     if grad_w is None:
         if accumulate:
             raise ValueError("accumulate needs the grad_w to add to")
         grad_w = torch.empty((E, N, K), dtype=grad_dtype or torch.float32, device=dev)
-    elif tuple(grad_w.shape) != (E, N, K) or grad_w.device != dev or (
-            grad_dtype is not None and grad_w.dtype != grad_dtype):
-        raise ValueError(f"grad_w must be of shape {(E, N, K)} on {dev} and in grad_dtype")
-    ldg = _rows("grad", grad, (rows, N), grad.dtype, dev)
-    lda = _rows("a", a, (rows, K), grad.dtype, dev)
-    rc = _on(dev, stream, lambda s: load_library().moe_grouped_gemm_weight_grad(
-        grad.data_ptr(), ldg, a.data_ptr(), lda, offsets.data_ptr(), rows, E, N, K,
-        _code(grad.dtype), _ptr(grad_w), _code(grad_w.dtype), int(bool(accumulate)), s))
-    _check(rc, "moe_grouped_gemm_weight_grad")
+    elif (grad_w.shape != (E, N, K) or grad_w.device != dev or not grad_w.is_contiguous() or
+          (grad_dtype is not None and grad_w.dtype != grad_dtype)):
+        raise ValueError(f"grad_w must be contiguous, of shape {(E, N, K)}, on {dev} and in grad_dtype")
+    _enqueue("moe_grouped_gemm_weight_grad", dev, stream, grad.data_ptr(), ldg, a.data_ptr(), lda,
+             offsets.data_ptr(), rows, E, N, K, _code(dt), grad_w.data_ptr(), _code(grad_w.dtype),
+             int(bool(accumulate)))
     return grad_w
 
 
@@ -887,13 +905,20 @@ def swiglu_checkpoint_views(ckpt: torch.Tensor, rows: int, I: int) -> dict:
     (``float8_e4m3fn [rows, P]``, P = I rounded up to 32) and ``gate_scales``,
     ``up_scales`` (``uint8 [rows, P / 32]``, the scale ``2^(byte - 127)``)."""
     p = moe_swiglu_checkpoint_layout(rows, I)
-    out = {}
-    for name, at, cols in (("gate_codes", p.gate_codes, p.row_codes), ("up_codes", p.up_codes, p.row_codes),
-                           ("gate_scales", p.gate_scales, p.row_scales),
-                           ("up_scales", p.up_scales, p.row_scales)):
-        v = ckpt[at:at + rows * cols].view(rows, cols)
-        out[name] = v.view(torch.float8_e4m3fn) if name.endswith("codes") else v
-    return out
+    if ckpt.dtype != torch.uint8 or ckpt.dim() != 1 or ckpt.numel() < p.total or not ckpt.is_contiguous():
+        raise ValueError(f"ckpt must be a contiguous uint8 vector of at least {p.total} bytes")
+    codes, P, S, at = ckpt.view(torch.float8_e4m3fn), p.row_codes, p.row_scales, ckpt.storage_offset()
+    return {"gate_codes": codes.as_strided((rows, P), (P, 1), at + p.gate_codes),
+            "up_codes": codes.as_strided((rows, P), (P, 1), at + p.up_codes),
+            "gate_scales": ckpt.as_strided((rows, S), (S, 1), at + p.gate_scales),
+            "up_scales": ckpt.as_strided((rows, S), (S, 1), at + p.up_scales)}
+
+
+def _checkpoint(ckpt: torch.Tensor, dev) -> int:
+    """Checks a checkpoint buffer (its size is the C entry point's to check); returns its bytes."""
+    if ckpt.device != dev or not ckpt.is_contiguous():
+        raise ValueError(f"ckpt must be contiguous on {dev}")
+    return ckpt.numel() * ckpt.element_size()
 
 
 def moe_swiglu_checkpoint(g: torch.Tensor, u: torch.Tensor, offsets=None, h=None, ckpt=None,
@@ -903,23 +928,21 @@ def moe_swiglu_checkpoint(g: torch.Tensor, u: torch.Tensor, offsets=None, h=None
     both in 8 bits. Returns ``(h, ckpt)``; ``ckpt`` (uint8) is what
     :func:`moe_swiglu_checkpoint_backward` takes. With ``offsets`` the rows past
     ``offsets[E]`` are left alone."""
+    dev, dt = _cuda(g), g.dtype
     rows, I = g.shape
-    dev = g.device
-    E = 0 if offsets is None else _offsets(offsets, dev)
-    ld = _rows("g", g, (rows, I), g.dtype, dev)
-    if _rows("u", u, (rows, I), g.dtype, dev) != ld:
+    E = 0 if offsets is None else _experts(offsets, dev)
+    ld = _ld("g", g, rows, I, dt, dev)
+    if _ld("u", u, rows, I, dt, dev) != ld:
         raise ValueError("g and u must have the same row stride")
     if h is None:
-        h = torch.empty((rows, I), dtype=g.dtype, device=dev)
-    ldh = _rows("h", h, (rows, I), g.dtype, dev)
+        h, ldh = torch.empty((rows, I), dtype=dt, device=dev), I
+    else:
+        ldh = _ld("h", h, rows, I, dt, dev)
     if ckpt is None:
         ckpt = torch.empty(moe_swiglu_checkpoint_size(rows, I), dtype=torch.uint8, device=dev)
-    elif ckpt.device != dev:
-        raise ValueError(f"ckpt must be on {dev}")
-    rc = _on(dev, stream, lambda s: load_library().moe_swiglu_checkpoint(
-        g.data_ptr(), u.data_ptr(), ld, None if offsets is None else offsets.data_ptr(), E, rows, I,
-        _code(g.dtype), h.data_ptr(), ldh, _ptr(ckpt), _nbytes(ckpt), s))
-    _check(rc, "moe_swiglu_checkpoint")
+    _enqueue("moe_swiglu_checkpoint", dev, stream, g.data_ptr(), u.data_ptr(), ld,
+             None if offsets is None else offsets.data_ptr(), E, rows, I, _code(dt), h.data_ptr(),
+             ldh, ckpt.data_ptr(), _checkpoint(ckpt, dev))
     return h, ckpt
 
 
@@ -930,26 +953,26 @@ def moe_swiglu_checkpoint_backward(grad_h: torch.Tensor, ckpt: torch.Tensor, off
     ``(grad_g, grad_u, h)``, ``[rows, I]`` each: the gradients by default as
     halves of one ``[rows, 2I]`` matrix, ``h`` recomputed from the checkpoint
     (None without ``need_h``)."""
+    dev, dt = _cuda(grad_h), grad_h.dtype
     rows, I = grad_h.shape
-    dev, dt = grad_h.device, grad_h.dtype
-    E = 0 if offsets is None else _offsets(offsets, dev)
-    if (grad_g is None) != (grad_u is None):
-        raise ValueError("give both grad_g and grad_u, or neither")
-    if grad_g is None:
+    E = 0 if offsets is None else _experts(offsets, dev)
+    ld = _ld("grad_h", grad_h, rows, I, dt, dev)
+    if grad_g is None and grad_u is None:
         both = torch.empty((rows, 2 * I), dtype=dt, device=dev)
-        grad_g, grad_u = both[:, :I], both[:, I:]
-    if h is None and need_h:
+        grad_g, grad_u, ldg = both[:, :I], both[:, I:], 2 * I
+    elif grad_g is None or grad_u is None:
+        raise ValueError("give both grad_g and grad_u, or neither")
+    else:
+        ldg = _ld("grad_g", grad_g, rows, I, dt, dev)
+        if _ld("grad_u", grad_u, rows, I, dt, dev) != ldg:
+            raise ValueError("grad_g and grad_u must have the same row stride")
+    ldh = I
+    if h is not None:
+        ldh = _ld("h", h, rows, I, dt, dev)
+    elif need_h:
         h = torch.empty((rows, I), dtype=dt, device=dev)
-    ld = _rows("grad_h", grad_h, (rows, I), dt, dev)
-    ldg = _rows("grad_g", grad_g, (rows, I), dt, dev)
-    if _rows("grad_u", grad_u, (rows, I), dt, dev) != ldg:
-        raise ValueError("grad_g and grad_u must have the same row stride")
-    ldh = I if h is None else _rows("h", h, (rows, I), dt, dev)
-    if ckpt.device != dev:
-        raise ValueError(f"ckpt must be on {dev}")
-    rc = _on(dev, stream, lambda s: load_library().moe_swiglu_checkpoint_backward(
-        grad_h.data_ptr(), ld, _ptr(ckpt), _nbytes(ckpt),
-        None if offsets is None else offsets.data_ptr(), E, rows, I, _code(dt), grad_g.data_ptr(),
-        grad_u.data_ptr(), ldg, None if h is None else h.data_ptr(), ldh, s))
-    _check(rc, "moe_swiglu_checkpoint_backward")
+    _enqueue("moe_swiglu_checkpoint_backward", dev, stream, grad_h.data_ptr(), ld, ckpt.data_ptr(),
+             _checkpoint(ckpt, dev), None if offsets is None else offsets.data_ptr(), E, rows, I,
+             _code(dt), grad_g.data_ptr(), grad_u.data_ptr(), ldg,
+             None if h is None else h.data_ptr(), ldh)
     return grad_g, grad_u, h

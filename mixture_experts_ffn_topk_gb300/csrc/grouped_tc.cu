@@ -10,10 +10,11 @@
 // and a decode step's one or two rows per expert cost a 16-wide MMA over a
 // weight tile that is loaded whole: the kernel streams weights.
 //
-// Per CTA (one per SM, 192 threads, persistent over the units):
-//   warp 0     TMA producer: 128 weight columns x 64 k (16 KiB; one box of
-//              K-major rows, or two MN-major boxes of 64 n for [E, K, N]) and
-//              the unit's rows x 64 k, into a ring of 192 KiB;
+// Per CTA (one per SM, 224 threads, persistent over the units):
+//   warp 0     TMA producer of the weights: 128 columns x 64 k (16 KiB; one box
+//              of K-major rows, or two MN-major boxes of 64 n for [E, K, N])
+//              per stage of a ring of 192 KiB;
+//   warp 6     TMA producer of the unit's rows x 64 k, into the same stages;
 //   warp 1     tcgen05.mma issuer, K = 16 per instruction, two accumulators of
 //              256 TMEM columns in turn;
 //   warps 2-5  epilogue: TMEM lane = n, column = row of the segment. 32 rows
@@ -47,7 +48,7 @@ constexpr int RING_BYTES = 192 << 10;
 constexpr int MAX_STAGES = 10;
 constexpr int ACC_COLS = 256;
 constexpr int TMEM_COLS = 2 * ACC_COLS;
-constexpr int THREADS = 192;
+constexpr int THREADS = 224;
 constexpr int STG_BYTES = 8192;          // one epilogue staging buffer
 constexpr uint64_t kDrainLimitNs = 100000000ull;
 // Bytes of rows a block of row units may cover, well inside the 129 MB L2
@@ -146,7 +147,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
 {
     extern __shared__ uint8_t smem_raw[];
     Smem &S = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = CG == 2 ? (int)cluster_ctarank() : 0;
     const bool leader = rank == 0;
     const int unit0 = (int)blockIdx.x / CG, unit_step = (int)gridDim.x / CG;
@@ -177,10 +178,9 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     const uint32_t tmem_base = S.tmem_base;
     const int total = S.seg.unit[p.E];
     volatile int *abort_flag = &S.abort;
-    uint32_t filled_mask = 0, filled_parity = 0;       // producer: stages in flight
 
-    if (warp == 0 && lane == 0) {
-        // ------------------------------------------------------ TMA producer
+    if (warp == 0 || warp == 6) {
+        // ------------------------------- TMA producers: weights (0), rows (6)
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -190,40 +190,46 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             const int row0 = u.row0 + rank * mine;
             const uint32_t bytes = W_BYTES + mine * BK * 2;
             for (int kb = 0; kb < num_kb; ++kb) {
-                if (!mbar_wait<CG>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns)) { ok = false; break; }
-                uint8_t *sw = S.ring + stage * p.slot_bytes;
-                // both CTAs' copies complete on the leader's barrier, which
-                // expects both; a peer's copy may land before the leader arms
-                // it (the phase cannot complete while its arrival is pending)
-                if (leader) mbar_arrive_expect_tx(&S.full[stage], CG * bytes);
-                const uint32_t bar = CG == 2 ? mapa_shared(smem_u32(&S.full[stage]), 0) : 0u;
-                auto load_w = [&](void *dst, int c0, int c1) {
-                    if constexpr (CG == 2) tma_load_3d_pair(dst, &map_w, bar, c0, c1, u.e);
-                    else tma_load_3d(dst, &map_w, &S.full[stage], c0, c1, u.e);
-                };
-                if constexpr (KN) {
-                    load_w(sw, u.w0, kb * BK);
-                    load_w(sw + W_BYTES / 2, u.w0 + 64, kb * BK);
-                } else {
-                    load_w(sw, kb * BK, u.w0);
+                ok = __all_sync(0xffffffffu, mbar_wait<CG>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns));
+                if (!ok) break;
+                if (elect_one()) {
+                    uint8_t *sw = S.ring + stage * p.slot_bytes;
+                    // both CTAs' copies complete on the leader's barrier, which
+                    // expects both; the rows' and a peer's copies may land before
+                    // it is armed (the phase cannot complete while the arrival
+                    // is pending)
+                    const uint32_t bar = CG == 2 ? mapa_shared(smem_u32(&S.full[stage]), 0) : 0u;
+                    if (warp == 0) {
+                        if (leader) mbar_arrive_expect_tx(&S.full[stage], CG * bytes);
+                        auto load_w = [&](void *dst, int c0, int c1) {
+                            if constexpr (CG == 2) tma_load_3d_pair(dst, &map_w, bar, c0, c1, u.e);
+                            else tma_load_3d(dst, &map_w, &S.full[stage], c0, c1, u.e);
+                        };
+                        if constexpr (KN) {
+                            load_w(sw, u.w0, kb * BK);
+                            load_w(sw + W_BYTES / 2, u.w0 + 64, kb * BK);
+                        } else {
+                            load_w(sw, kb * BK, u.w0);
+                        }
+                    } else {
+                        uint8_t *sa = sw + W_BYTES;
+                        auto load_a = [&](int box, int at) {
+                            uint8_t *dst = sa + at * BK * 2;
+                            if constexpr (CG == 2) tma_load_2d_pair(dst, &map_a.m[box], bar, kb * BK, row0 + at);
+                            else tma_load_2d(dst, &map_a.m[box], &S.full[stage], kb * BK, row0 + at);
+                        };
+                        int at = 0;
+                        for (; mine - at >= 128; at += 128) load_a(0, at);
+                        if (mine & 64) { load_a(1, at); at += 64; }
+                        if (mine & 32) { load_a(2, at); at += 32; }
+                        if (mine & 16) load_a(3, at);
+                    }
                 }
-                uint8_t *sa = sw + W_BYTES;
-                auto load_a = [&](int box, int at) {
-                    uint8_t *dst = sa + at * BK * 2;
-                    if constexpr (CG == 2) tma_load_2d_pair(dst, &map_a.m[box], bar, kb * BK, row0 + at);
-                    else tma_load_2d(dst, &map_a.m[box], &S.full[stage], kb * BK, row0 + at);
-                };
-                int at = 0;
-                for (; mine - at >= 128; at += 128) load_a(0, at);
-                if (mine & 64) { load_a(1, at); at += 64; }
-                if (mine & 32) { load_a(2, at); at += 32; }
-                if (mine & 16) load_a(3, at);
-                filled_mask |= 1u << stage;
-                filled_parity = (filled_parity & ~(1u << stage)) | (phase << stage);
+                __syncwarp();
                 if (++stage == p.stages) { stage = 0; phase ^= 1u; }
             }
         }
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
         // ------------------------------------------------------ MMA issuer
         constexpr uint32_t idesc0 = idesc_f16_major<DT>(BM * CG, 0, KN, false);
         int stage = 0;
@@ -235,31 +241,38 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             const uint32_t idesc = idesc0 | ((uint32_t)(u.mma_n >> 3) << 17);
             const int acc = it & 1;
             const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
-            if (!mbar_wait<CG>(&S.acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_ns)) { ok = false; break; }
+            ok = __all_sync(0xffffffffu, mbar_wait<CG>(&S.acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_ns));
+            if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem_base + (uint32_t)(acc * ACC_COLS);
             for (int kb = 0; kb < num_kb; ++kb) {
-                if (!mbar_wait<CG>(&S.full[stage], phase, abort_flag, p.status, p.wait_ns)) { ok = false; break; }
+                ok = __all_sync(0xffffffffu, mbar_wait<CG>(&S.full[stage], phase, abort_flag, p.status, p.wait_ns));
+                if (!ok) break;
                 tc_fence_after();
-                const uint32_t w = smem_u32(S.ring + stage * p.slot_bytes), a = w + W_BYTES;
+                if (elect_one()) {
+                    const uint32_t w = smem_u32(S.ring + stage * p.slot_bytes), a = w + W_BYTES;
 #pragma unroll
-                for (int k = 0; k < BK / UK; ++k)
-                    umma_f16<CG>(d, KN ? sdesc_mn_sw128(w + k * UK * 128, W_BYTES / 2) : sdesc_k_sw128(w + k * UK * 2),
-                                 sdesc_k_sw128(a + k * UK * 2), idesc, (kb | k) != 0 ? 1u : 0u);
-                if constexpr (CG == 2) umma_commit_pair(&S.empty[stage]);
-                else umma_commit<1>(&S.empty[stage]);
+                    for (int k = 0; k < BK / UK; ++k)
+                        umma_f16<CG>(d, KN ? sdesc_mn_sw128(w + k * UK * 128, W_BYTES / 2) : sdesc_k_sw128(w + k * UK * 2),
+                                     sdesc_k_sw128(a + k * UK * 2), idesc, (kb | k) != 0 ? 1u : 0u);
+                    if constexpr (CG == 2) umma_commit_pair(&S.empty[stage]);
+                    else umma_commit<1>(&S.empty[stage]);
+                    if (kb + 1 == num_kb) {
+                        if constexpr (CG == 2) umma_commit_pair(&S.acc_full[acc]);
+                        else umma_commit<1>(&S.acc_full[acc]);
+                    }
+                }
+                __syncwarp();
                 if (++stage == p.stages) { stage = 0; phase ^= 1u; }
             }
-            if (ok) {
-                if constexpr (CG == 2) umma_commit_pair(&S.acc_full[acc]);
-                else umma_commit<1>(&S.acc_full[acc]);
-            }
         }
-        if (*abort_flag) {
-            // every MMA issued so far must finish before TMEM is released
+        if (elect_one()) {
+            // every MMA issued must finish before TMEM is released, also where
+            // another role has given up
             umma_commit<CG>(&S.drain);
             mbar_wait(&S.drain, 0, nullptr, p.status, kDrainLimitNs);
         }
+        __syncwarp();
     } else if (warp >= 2) {
         // ------------------------------------------------------ epilogue
         const int q = warp & 3;                          // TMEM lane quadrant of this warp
@@ -335,19 +348,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
 
     // ------------------------------------------------------------ teardown
     __syncthreads();
-    if (*abort_flag && warp == 0 && lane == 0) {
-        if (CG == 1 || leader) {
-            // let the outstanding TMA copies land before shared memory goes
-            for (int s = 0; s < p.stages; ++s)
-                if (filled_mask >> s & 1u)
-                    mbar_wait(&S.full[s], filled_parity >> s & 1u, nullptr, p.status, kDrainLimitNs);
-        } else {
-            // a peer's copies complete on the leader's barriers, which it
-            // cannot wait on: give them the same bounded time to land
-            const uint64_t t0 = global_timer_ns();
-            while (global_timer_ns() - t0 < kDrainLimitNs) { }
-        }
-    }
+    if (*abort_flag) let_copies_land();
     // a pair keeps both CTAs (their shared memory is read by the leader's
     // MMAs and signalled by its commits) until both are done
     if constexpr (CG == 2) cluster_sync();

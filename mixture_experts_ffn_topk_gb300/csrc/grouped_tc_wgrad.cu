@@ -12,8 +12,8 @@
 // a zero in one), by a warp that stands between that stage's copies and its
 // MMAs. No tensor map depends on the offsets, no workspace is needed.
 //
-// Per CTA (one per SM, 224 threads, persistent over the units):
-//   warp 0     TMA producer: 128 columns of grad (16 KiB) and 256 / CG of a;
+// Per CTA (one per SM, 256 threads, persistent over the units):
+//   warps 0, 7 TMA producers: 128 columns of grad (16 KiB), 256 / CG of a;
 //   warp 1     tcgen05.mma issuer, M = 128 * CG by N = up to 256;
 //   warps 2-5  epilogue: 32 rows x 128 bytes at a time through a swizzled
 //              staging buffer, so that stores write whole lines;
@@ -48,7 +48,7 @@ template <int CG>
 constexpr int STAGES = CG == 2 ? 6 : 4;
 constexpr int ACC_COLS = 256;
 constexpr int TMEM_COLS = 2 * ACC_COLS;
-constexpr int THREADS = 224;
+constexpr int THREADS = 256;
 constexpr int STG_ROW_BYTES = 128;
 constexpr uint64_t kDrainLimitNs = 100000000ull;
 
@@ -121,7 +121,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
     constexpr int NS = STAGES<CG>;
     extern __shared__ uint8_t smem_raw[];
     Smem<CG> &S = *reinterpret_cast<Smem<CG> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = CG == 2 ? (int)cluster_ctarank() : 0;
     const bool leader = rank == 0;
     const int unit0 = (int)blockIdx.x / CG, unit_step = (int)gridDim.x / CG;
@@ -156,11 +156,9 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
     const uint32_t tmem_base = S.tmem_base;
     const int total = p.E * p.n_tiles * p.k_tiles;
     volatile int *abort_flag = &S.abort;
-    // producer: stages in flight, their parities, and (tails) on which barrier
-    uint32_t filled_mask = 0, filled_parity = 0, tail_mask = 0, tail_parity = 0;
 
-    if (warp == 0 && lane == 0) {
-        // ------------------------------------------------------ TMA producer
+    if (warp == 0 || warp == 7) {
+        // ----------------------------------- TMA producers: grad (0), a (7)
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
@@ -170,39 +168,40 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
             const int boxes = mine / 64, col0 = u.k0 + rank * mine;
             const uint32_t bytes = G_BYTES + boxes * BOX_BYTES;
             for (int kb = 0; kb < u.nkb; ++kb) {
-                if (!mbar_wait<CG>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns)) { ok = false; break; }
-                uint8_t *sg = S.ring[stage];
-                // a stage with foreign rows completes in its own CTA, where
-                // warp 6 zeroes them; any other on the leader's barrier, which
-                // expects both CTAs' bytes (a peer's copy may land before the
-                // leader arms it: the phase cannot complete while its arrival
-                // is pending)
-                const bool tail = kb == u.nkb - 1 && u.tail % UK != 0;
-                const uint32_t bit = 1u << stage;
-                if (tail) {
-                    mbar_arrive_expect_tx(&S.tail_in[stage], bytes);
-                    if (leader) mbar_arrive(&S.full[stage]);
-                    tail_mask |= bit;
-                    tail_parity ^= bit;           // set while an odd use (parity 0) is in flight
-                } else {
-                    if (leader) mbar_arrive_expect_tx(&S.full[stage], CG * bytes);
-                    tail_mask &= ~bit;
+                ok = __all_sync(0xffffffffu, mbar_wait<CG>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns));
+                if (!ok) break;
+                if (elect_one()) {
+                    uint8_t *sg = S.ring[stage];
+                    // a stage with foreign rows completes in its own CTA, where
+                    // warp 6 zeroes them; any other on the leader's barrier,
+                    // which expects both CTAs' bytes (copies may land before it
+                    // is armed: the phase cannot complete while its arrival is
+                    // pending)
+                    const bool tail = kb == u.nkb - 1 && u.tail % UK != 0;
+                    uint64_t *local = tail ? &S.tail_in[stage] : &S.full[stage];
+                    const uint32_t bar = CG == 2 ? mapa_shared(smem_u32(local), tail ? (uint32_t)rank : 0u) : 0u;
+                    auto load = [&](void *dst, const CUtensorMap *m, int c) {
+                        if constexpr (CG == 2) tma_load_2d_pair(dst, m, bar, c, u.row0 + kb * BK);
+                        else tma_load_2d(dst, m, local, c, u.row0 + kb * BK);
+                    };
+                    if (warp == 0) {
+                        if (tail) {
+                            mbar_arrive_expect_tx(&S.tail_in[stage], bytes);
+                            if (leader) mbar_arrive(&S.full[stage]);
+                        } else if (leader) {
+                            mbar_arrive_expect_tx(&S.full[stage], CG * bytes);
+                        }
+                        load(sg, &map_g, u.n0);
+                        load(sg + BOX_BYTES, &map_g, u.n0 + 64);
+                    } else {
+                        for (int j = 0; j < boxes; ++j) load(sg + G_BYTES + j * BOX_BYTES, &map_a, col0 + j * 64);
+                    }
                 }
-                uint64_t *local = tail ? &S.tail_in[stage] : &S.full[stage];
-                const uint32_t bar = CG == 2 ? mapa_shared(smem_u32(local), tail ? (uint32_t)rank : 0u) : 0u;
-                auto load = [&](void *dst, const CUtensorMap *m, int c) {
-                    if constexpr (CG == 2) tma_load_2d_pair(dst, m, bar, c, u.row0 + kb * BK);
-                    else tma_load_2d(dst, m, local, c, u.row0 + kb * BK);
-                };
-                load(sg, &map_g, u.n0);
-                load(sg + BOX_BYTES, &map_g, u.n0 + 64);
-                for (int j = 0; j < boxes; ++j) load(sg + G_BYTES + j * BOX_BYTES, &map_a, col0 + j * 64);
-                filled_mask |= bit;
-                filled_parity = (filled_parity & ~bit) | (phase << stage);
+                __syncwarp();
                 if (++stage == NS) { stage = 0; phase ^= 1u; }
             }
         }
-    } else if (warp == 1 && lane == 0 && leader) {
+    } else if (warp == 1 && leader) {
         // ------------------------------------------------------ MMA issuer
         constexpr uint32_t idesc0 = idesc_f16_major<DT>(BM * CG, 0, true, true);
         int stage = 0;
@@ -214,37 +213,47 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
             const uint32_t idesc = idesc0 | ((uint32_t)(u.mma_n >> 3) << 17);
             const int acc = it & 1;
             const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
-            if (!mbar_wait<CG>(&S.acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_ns)) { ok = false; break; }
+            ok = __all_sync(0xffffffffu, mbar_wait<CG>(&S.acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_ns));
+            if (!ok) break;
             tc_fence_after();
             const uint32_t d = tmem_base + (uint32_t)(acc * ACC_COLS);
             for (int kb = 0; kb < u.nkb; ++kb) {
-                if (!mbar_wait<CG>(&S.full[stage], phase, abort_flag, p.status, p.wait_ns)) { ok = false; break; }
+                ok = __all_sync(0xffffffffu, mbar_wait<CG>(&S.full[stage], phase, abort_flag, p.status, p.wait_ns));
+                if (!ok) break;
                 const int valid = kb == u.nkb - 1 ? u.tail : BK;
                 if (valid % UK != 0) {
-                    if (!mbar_wait<CG>(&S.tail_out[stage], tails >> stage & 1u, abort_flag, p.status, p.wait_ns)) { ok = false; break; }
+                    ok = __all_sync(0xffffffffu, mbar_wait<CG>(&S.tail_out[stage], tails >> stage & 1u, abort_flag, p.status, p.wait_ns));
+                    if (!ok) break;
                     tails ^= 1u << stage;
                 }
                 tc_fence_after();
-                const uint32_t g = smem_u32(S.ring[stage]), a = g + G_BYTES;
-                const int steps = (valid + UK - 1) / UK;
-                for (int k = 0; k < steps; ++k)
-                    umma_f16<CG>(d, sdesc_mn_sw128(g + k * UK * 128, BOX_BYTES),
-                                 sdesc_mn_sw128(a + k * UK * 128, BOX_BYTES), idesc, (kb | k) != 0 ? 1u : 0u);
-                if constexpr (CG == 2) umma_commit_pair(&S.empty[stage]);
-                else umma_commit<1>(&S.empty[stage]);
+                if (elect_one()) {
+                    const uint32_t g = smem_u32(S.ring[stage]), a = g + G_BYTES;
+#pragma unroll
+                    for (int k = 0; k < BK / UK; ++k)
+                        if (k * UK < valid)
+                            umma_f16<CG>(d, sdesc_mn_sw128(g + k * UK * 128, BOX_BYTES),
+                                         sdesc_mn_sw128(a + k * UK * 128, BOX_BYTES), idesc, (kb | k) != 0 ? 1u : 0u);
+                    if constexpr (CG == 2) umma_commit_pair(&S.empty[stage]);
+                    else umma_commit<1>(&S.empty[stage]);
+                }
+                __syncwarp();
                 if (++stage == NS) { stage = 0; phase ^= 1u; }
             }
             // (an expert without rows commits with no MMA: its epilogue writes zeros)
-            if (ok) {
+            if (ok && elect_one()) {
                 if constexpr (CG == 2) umma_commit_pair(&S.acc_full[acc]);
                 else umma_commit<1>(&S.acc_full[acc]);
             }
+            __syncwarp();
         }
-        if (*abort_flag) {
-            // every MMA issued so far must finish before TMEM is released
+        if (elect_one()) {
+            // every MMA issued must finish before TMEM is released, also where
+            // another role has given up
             umma_commit<CG>(&S.drain);
             mbar_wait(&S.drain, 0, nullptr, p.status, kDrainLimitNs);
         }
+        __syncwarp();
     } else if (warp == 6) {
         // ------------------------------------------------------ foreign rows
         int stage = 0;
@@ -360,20 +369,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
 
     // ------------------------------------------------------------ teardown
     __syncthreads();
-    if (*abort_flag && warp == 0 && lane == 0) {
-        // let the outstanding TMA copies land before shared memory goes
-        for (int s = 0; s < NS; ++s)
-            if ((filled_mask >> s & 1u) && (tail_mask >> s & 1u))
-                mbar_wait(&S.tail_in[s], (tail_parity >> s & 1u) ^ 1u, nullptr, p.status, kDrainLimitNs);
-            else if ((filled_mask >> s & 1u) && leader)
-                mbar_wait(&S.full[s], filled_parity >> s & 1u, nullptr, p.status, kDrainLimitNs);
-        if (!leader) {
-            // a peer's other copies complete on the leader's barriers, which
-            // it cannot wait on: give them the same bounded time to land
-            const uint64_t t0 = global_timer_ns();
-            while (global_timer_ns() - t0 < kDrainLimitNs) { }
-        }
-    }
+    if (*abort_flag) let_copies_land();
     // a pair keeps both CTAs (their shared memory is read by the leader's
     // MMAs and signalled by its commits) until both are done
     if constexpr (CG == 2) cluster_sync();

@@ -31,6 +31,7 @@ namespace {
 constexpr int kBlock = 32;       // columns that share a scale
 constexpr int kLaneCols = 8;     // columns a lane handles
 constexpr int kThreads = 256;
+constexpr int kItems = 2;        // blocks a thread has in flight at once
 
 // Item = one block of one row; a thread walks items first, first + step, ...
 // as (row, blk) pairs without dividing: step = step_row * S + step_blk.
@@ -49,33 +50,40 @@ __device__ __forceinline__ int64_t rows_to_do(const Walk &w)
     return e < 0 ? 0 : (e < w.rows ? e : w.rows);
 }
 
-// Eight consecutive columns of a row as FP32. VEC: the row allows 16-byte
-// access and all eight columns exist; otherwise columns past `left` read 0.
+// Eight consecutive columns of a row as they are stored.
+template <int DT>
+struct Raw8 {
+    uint4 q[DT == DT_F32 ? 2 : 1];
+
+    __device__ __forceinline__ float at(int i) const
+    {
+        const uint32_t *w = reinterpret_cast<const uint32_t *>(q);
+        if constexpr (DT == DT_F32) return __uint_as_float(w[i]);
+        const uint32_t h = w[i >> 1];
+        if constexpr (DT == DT_BF16) return __uint_as_float(i & 1 ? h & 0xffff0000u : h << 16);
+        return __half2float(__ushort_as_half((unsigned short)(i & 1 ? h >> 16 : h)));
+    }
+};
+
+// VEC: rows start on 16 bytes. A piece that is not whole (the end of a row, or
+// any piece without VEC) is read by element; columns past `left` read 0.
 template <int DT, bool VEC>
-__device__ __forceinline__ void load8(const void *row, int col, int left, float (&v)[8])
+__device__ __forceinline__ Raw8<DT> load8(const void *row, int col, int left)
 {
     using T = typename Elem<DT>::T;
     const T *p = static_cast<const T *>(row) + col;
+    Raw8<DT> r;
     if (VEC && left >= 8) {
-        if constexpr (DT == DT_F32) {
-            const float4 a = __ldcs(reinterpret_cast<const float4 *>(p));
-            const float4 b = __ldcs(reinterpret_cast<const float4 *>(p) + 1);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        } else {
-            Vec16 q;
-            q.u = __ldcs(reinterpret_cast<const uint4 *>(p));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = DT == DT_BF16 ? bf16x2_to_float2(q.w[i]) : f16x2_to_float2(q.w[i]);
-                v[2 * i] = f.x;
-                v[2 * i + 1] = f.y;
-            }
-        }
+        for (int i = 0; i < (DT == DT_F32 ? 2 : 1); ++i) r.q[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < left ? Elem<DT>::to_f(p[i]) : 0.0f;
+        for (int i = 0; i < (DT == DT_F32 ? 2 : 1); ++i) r.q[i] = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < left) reinterpret_cast<T *>(&r)[i] = p[i];
     }
+    return r;
 }
 
 template <int DT, bool VEC>
@@ -124,26 +132,55 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top)
     return (uint32_t)min(max(b, 0), 246);
 }
 
-// Codes of this lane's eight values, and the block's scale byte.
-__device__ __forceinline__ uint2 encode8(const float (&v)[8], uint32_t &sb)
+// Largest magnitude of this lane's eight values as FP32 bits; FINITE: of the
+// finite ones only. 16-bit values are compared two at a time.
+template <int DT, bool FINITE>
+__device__ __forceinline__ uint32_t top8(const Raw8<DT> &v)
 {
-    uint32_t top = 0;
+    if constexpr (DT == DT_F32 || FINITE) {
+        uint32_t top = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t a = __float_as_uint(v[i]) & 0x7fffffffu;
-        top = max(top, a < 0x7f800000u ? a : 0u);
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t a = __float_as_uint(v.at(i)) & 0x7fffffffu;
+            top = max(top, !FINITE || a < 0x7f800000u ? a : 0u);
+        }
+        return top;
+    } else {
+        constexpr uint32_t M = 0x7fff7fffu;
+        uint32_t m = __vimax3_u16x2(v.q[0].x & M, v.q[0].y & M, v.q[0].z & M);
+        m = __vimax3_u16x2(m, v.q[0].w & M, m);
+        m = max(m & 0xffffu, m >> 16);
+        if constexpr (DT == DT_BF16) return m << 16;
+        // F16 infinities and NaN stay at or above FP32's infinity
+        return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
     }
+}
+
+// Codes of this lane's eight values, and the block's scale byte. All lanes of
+// the warp call.
+template <int DT>
+__device__ __forceinline__ uint2 encode8(const Raw8<DT> &v, uint32_t &sb)
+{
+    uint32_t top = top8<DT, false>(v);
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    const bool odd = __any_sync(0xffffffffu, top >= 0x7f800000u);     // infinities or NaN: rare
+    if (odd) {
+        top = top8<DT, true>(v);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    }
     sb = scale_byte(top);
     const float inv = __uint_as_float((254u - sb) << 23);       // 2^-x, normal for every byte
     uint32_t c[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float2 f = make_float2(v[2 * i] * inv, v[2 * i + 1] * inv);
-        // the conversion saturates infinities; they are to come back as NaN
-        if (isinf(v[2 * i])) f.x = __uint_as_float(0x7fffffffu);
-        if (isinf(v[2 * i + 1])) f.y = __uint_as_float(0x7fffffffu);
+        float2 f = make_float2(v.at(2 * i) * inv, v.at(2 * i + 1) * inv);
+        if (odd) {
+            // the conversion saturates infinities; they are to come back as NaN
+            if (isinf(v.at(2 * i))) f.x = __uint_as_float(0x7fffffffu);
+            if (isinf(v.at(2 * i + 1))) f.y = __uint_as_float(0x7fffffffu);
+        }
         c[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
     }
     return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
@@ -164,6 +201,28 @@ __device__ __forceinline__ void decode8(uint2 c, uint32_t sb, float (&v)[8])
     }
 }
 
+// Where a thread is in the walk.
+struct Place {
+    int64_t row;
+    int blk;
+
+    __device__ __forceinline__ void advance(const Walk &w)
+    {
+        row += w.step_row;
+        blk += w.step_blk;
+        if (blk >= w.S) { blk -= w.S; ++row; }
+    }
+};
+
+__device__ __forceinline__ Place first_place(const Walk &w)
+{
+    const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 2;
+    Place p;
+    p.row = item / w.S;
+    p.blk = (int)(item - p.row * w.S);
+    return p;
+}
+
 template <int DT, bool VEC>
 __global__ void __launch_bounds__(kThreads)
 swiglu_checkpoint_kernel(const void *__restrict__ g, const void *__restrict__ u, int64_t ld_bytes,
@@ -174,41 +233,45 @@ swiglu_checkpoint_kernel(const void *__restrict__ g, const void *__restrict__ u,
     pdl_wait();
     pdl_launch_dependents();
     const int64_t rows = rows_to_do(w);
-    const int quarter = threadIdx.x & 3;
-    const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 2;
-    int64_t row = item / w.S;
-    int blk = (int)(item - row * w.S);
+    const int part = (threadIdx.x & 3) * kLaneCols;
+    Place at = first_place(w);
     // the four lanes of a block stay together; a warp leaves when all its
     // blocks are done, so the shuffles always have every lane
-    while (__any_sync(0xffffffffu, row < rows)) {
-        const bool live = row < rows;
-        const int64_t r = live ? row : 0;
-        const int col = blk * kBlock + quarter * kLaneCols;
-        const int left = live ? I - col : 0;
-        float a[8], b[8], o[8];
-        load8<DT, VEC>(static_cast<const uint8_t *>(g) + r * ld_bytes, col, left, a);
-        load8<DT, VEC>(static_cast<const uint8_t *>(u) + r * ld_bytes, col, left, b);
-        uint32_t sa, sb;
-        const uint2 ca = encode8(a, sa), cb = encode8(b, sb);
+    while (__any_sync(0xffffffffu, at.row < rows)) {
+        Place p[kItems];
+        Raw8<DT> a[kItems], b[kItems];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float t, not_t;
-            sigmoid_of<DT>(a[i], t, not_t);
-            o[i] = a[i] * t * b[i];
+        for (int k = 0; k < kItems; ++k) {
+            p[k] = at;
+            at.advance(w);
+            const int col = p[k].blk * kBlock + part;
+            const int left = p[k].row < rows ? I - col : 0;
+            const int64_t off = left > 0 ? p[k].row * ld_bytes : 0;
+            a[k] = load8<DT, VEC>(static_cast<const uint8_t *>(g) + off, col, left);
+            b[k] = load8<DT, VEC>(static_cast<const uint8_t *>(u) + off, col, left);
         }
-        if (live) {
-            const int64_t at = r * w.S + blk;
-            *reinterpret_cast<uint2 *>(codes_g + at * kBlock + quarter * kLaneCols) = ca;
-            *reinterpret_cast<uint2 *>(codes_u + at * kBlock + quarter * kLaneCols) = cb;
-            if (quarter == 0) {
-                scales_g[at] = (uint8_t)sa;
-                scales_u[at] = (uint8_t)sb;
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            uint32_t sa, sb;
+            const uint2 ca = encode8<DT>(a[k], sa), cb = encode8<DT>(b[k], sb);
+            if (p[k].row >= rows) continue;
+            float o[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float t, not_t;
+                sigmoid_of<DT>(a[k].at(i), t, not_t);
+                o[i] = a[k].at(i) * t * b[k].at(i);
             }
-            store8<DT, VEC>(static_cast<uint8_t *>(h) + r * ldh_bytes, col, left, o);
+            const int col = p[k].blk * kBlock + part;
+            const int64_t block = p[k].row * w.S + p[k].blk;
+            *reinterpret_cast<uint2 *>(codes_g + block * kBlock + part) = ca;
+            *reinterpret_cast<uint2 *>(codes_u + block * kBlock + part) = cb;
+            if (part == 0) {
+                scales_g[block] = (uint8_t)sa;
+                scales_u[block] = (uint8_t)sb;
+            }
+            store8<DT, VEC>(static_cast<uint8_t *>(h) + p[k].row * ldh_bytes, col, I - col, o);
         }
-        row += w.step_row;
-        blk += w.step_blk;
-        if (blk >= w.S) { blk -= w.S; ++row; }
     }
 }
 
@@ -225,37 +288,47 @@ swiglu_checkpoint_backward_kernel(const void *__restrict__ grad_h, int64_t ld_by
     pdl_wait();
     pdl_launch_dependents();
     const int64_t rows = rows_to_do(w);
-    const int quarter = threadIdx.x & 3;
-    const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 2;
-    int64_t row = item / w.S;
-    int blk = (int)(item - row * w.S);
-    while (row < rows) {
-        const int col = blk * kBlock + quarter * kLaneCols;
-        const int left = I - col;
-        const int64_t at = row * w.S + blk;
-        float d[8], g[8], u[8];
-        load8<DT, VEC>(static_cast<const uint8_t *>(grad_h) + row * ld_bytes, col, left, d);
-        decode8(__ldcs(reinterpret_cast<const uint2 *>(codes_g + at * kBlock + quarter * kLaneCols)),
-                scales_g[at], g);
-        decode8(__ldcs(reinterpret_cast<const uint2 *>(codes_u + at * kBlock + quarter * kLaneCols)),
-                scales_u[at], u);
-        float dg[8], du[8], o[8];
+    const int part = (threadIdx.x & 3) * kLaneCols;
+    Place at = first_place(w);
+    while (at.row < rows) {
+        Place p[kItems];
+        Raw8<DT> d[kItems];
+        uint2 cg[kItems], cu[kItems];
+        uint32_t sg[kItems], su[kItems];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float t, not_t;
-            sigmoid_of<DT>(g[i], t, not_t);
-            const float gt = g[i] * t;
-            dg[i] = d[i] * u[i] * (t * (1.0f + g[i] * not_t));
-            du[i] = d[i] * gt;
-            o[i] = gt * u[i];
+        for (int k = 0; k < kItems; ++k) {
+            p[k] = at;
+            at.advance(w);
+            if (p[k].row >= rows) continue;
+            const int col = p[k].blk * kBlock + part;
+            const int64_t block = p[k].row * w.S + p[k].blk;
+            d[k] = load8<DT, VEC>(static_cast<const uint8_t *>(grad_h) + p[k].row * ld_bytes, col, I - col);
+            cg[k] = __ldcs(reinterpret_cast<const uint2 *>(codes_g + block * kBlock + part));
+            cu[k] = __ldcs(reinterpret_cast<const uint2 *>(codes_u + block * kBlock + part));
+            sg[k] = scales_g[block];
+            su[k] = scales_u[block];
         }
-        store8<DT, VEC>(static_cast<uint8_t *>(grad_g) + row * ldg_bytes, col, left, dg);
-        store8<DT, VEC>(static_cast<uint8_t *>(grad_u) + row * ldg_bytes, col, left, du);
-        if (h != nullptr)
-            store8<DT, VEC>(static_cast<uint8_t *>(h) + row * ldh_bytes, col, left, o);
-        row += w.step_row;
-        blk += w.step_blk;
-        if (blk >= w.S) { blk -= w.S; ++row; }
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+            if (p[k].row >= rows) continue;
+            float g[8], u[8], dg[8], du[8], o[8];
+            decode8(cg[k], sg[k], g);
+            decode8(cu[k], su[k], u);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                float t, not_t;
+                sigmoid_of<DT>(g[i], t, not_t);
+                const float gt = g[i] * t, x = d[k].at(i);
+                dg[i] = x * u[i] * (t * (1.0f + g[i] * not_t));
+                du[i] = x * gt;
+                o[i] = gt * u[i];
+            }
+            const int col = p[k].blk * kBlock + part, left = I - col;
+            store8<DT, VEC>(static_cast<uint8_t *>(grad_g) + p[k].row * ldg_bytes, col, left, dg);
+            store8<DT, VEC>(static_cast<uint8_t *>(grad_u) + p[k].row * ldg_bytes, col, left, du);
+            if (h != nullptr)
+                store8<DT, VEC>(static_cast<uint8_t *>(h) + p[k].row * ldh_bytes, col, left, o);
+        }
     }
 }
 
