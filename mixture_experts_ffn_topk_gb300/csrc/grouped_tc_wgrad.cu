@@ -15,8 +15,10 @@
 // Per CTA (one per SM, 256 threads, persistent over the units):
 //   warps 0, 7 TMA producers: 128 columns of grad (16 KiB), 256 / CG of a;
 //   warp 1     tcgen05.mma issuer, M = 128 * CG by N = up to 256;
-//   warps 2-5  epilogue: 32 rows x 128 bytes at a time through a swizzled
-//              staging buffer, so that stores write whole lines;
+//   warps 2-5  epilogue: 32 rows x 64 bytes at a time into a swizzled staging
+//              buffer that a TMA store carries off, two buffers per warp, so
+//              that the warp only reads tensor memory and fills buffers; the
+//              store clips the tile at the matrix's edges;
 //   warp 6     zeroes foreign rows of a segment's last stage.
 // CTA pairs (CG = 2): M = 256, each CTA holds 128 columns of grad and half of
 // a's; the even CTA issues the MMAs.
@@ -49,13 +51,14 @@ constexpr int STAGES = CG == 2 ? 6 : 4;
 constexpr int ACC_COLS = 256;
 constexpr int TMEM_COLS = 2 * ACC_COLS;
 constexpr int THREADS = 256;
-constexpr int STG_ROW_BYTES = 128;
+constexpr int STG_ROW_BYTES = 64;        // staged bytes per row of grad_w
+constexpr int STG_BYTES = 32 * STG_ROW_BYTES;
 constexpr uint64_t kDrainLimitNs = 100000000ull;
 
 template <int CG>
 struct __align__(1024) Smem {
     uint8_t ring[STAGES<CG>][SLOT_BYTES<CG>];
-    uint8_t stg[4][32 * STG_ROW_BYTES];
+    uint8_t stg[4][2][STG_BYTES];
     uint64_t full[STAGES<CG>];
     uint64_t empty[STAGES<CG>];
     uint64_t tail_in[STAGES<CG>];        // this CTA's copies of a stage with foreign rows
@@ -77,7 +80,7 @@ struct WgradParams {
     int E, rows, N, K;
     int n_tiles, k_tiles;
     int n_fast;              // the n tile runs fastest (grad is the narrower operand)
-    uint8_t *out;
+    const uint8_t *out;      // read where the gradient is added to
     int64_t out_row_bytes;
     int accumulate;
     unsigned *status;
@@ -116,7 +119,7 @@ __device__ __forceinline__ Unit unit_of(const Segments &S, const WgradParams &p,
 template <int DT, int CG, bool OUT_F32>
 __global__ void __launch_bounds__(THREADS, 1)
 grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_a,
-                     const WgradParams p)
+                     const __grid_constant__ CUtensorMap map_out, const WgradParams p)
 {
     constexpr int NS = STAGES<CG>;
     extern __shared__ uint8_t smem_raw[];
@@ -287,11 +290,9 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
     } else if (warp >= 2) {
         // ------------------------------------------------------ epilogue
         const int q = warp & 3;                    // TMEM lane quadrant of this warp
-        uint8_t *stg = S.stg[warp - 2];
         constexpr int ESZ = OUT_F32 ? 4 : 2;
-        constexpr int COLS = STG_ROW_BYTES / ESZ;  // columns per round: 32 / 64
-        const int cch = lane & 7;
-        int it = 0;
+        constexpr int COLS = STG_ROW_BYTES / ESZ;  // columns per staging buffer: 16 / 32
+        int it = 0, buf = 0;
         for (int unit = unit0; unit < total; unit += unit_step, ++it) {
             const Unit u = unit_of<CG>(S.seg, p, unit, rank);
             const int acc = it & 1;
@@ -300,63 +301,71 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
             if (!__all_sync(0xffffffffu, ready)) break;
             tc_fence_after();
             const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
-            const int row0 = u.n0 + q * 32, rows_valid = p.N - row0;
-            uint8_t *base = p.out + ((int64_t)u.e * p.N + row0) * p.out_row_bytes;
+            const int row0 = u.n0 + q * 32;            // this warp's first row of grad_w[e]
             const bool empty = u.cnt == 0;
-            const int width = p.K - u.k0 < BN ? p.K - u.k0 : BN;
-            for (int c0 = 0; c0 < width && !(empty && p.accumulate); c0 += COLS) {
-                float v[COLS];
+            int width = p.K - u.k0 < BN ? p.K - u.k0 : BN;
+            if (row0 >= p.N || (empty && p.accumulate)) width = 0;
+            for (int c0 = 0; c0 < width; c0 += 32) {
+                uint32_t v[32];
+                tmem_ld32(tbase + c0, v);
+                tmem_ld_wait(v);
+                if (empty) {
 #pragma unroll
-                for (int h = 0; h < COLS / 32; ++h) {
-                    uint32_t r[32];
-                    tmem_ld32(tbase + c0 + h * 32, r);
-                    tmem_ld_wait(r);
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[h * 32 + i] = empty ? 0.0f : __uint_as_float(r[i]);
+                    for (int i = 0; i < 32; ++i) v[i] = 0u;
                 }
-                const int64_t col_byte = (int64_t)(u.k0 + c0) * ESZ;
-                if (p.accumulate && lane < rows_valid) {
-                    const uint8_t *old = base + lane * p.out_row_bytes + col_byte;
+                if (p.accumulate && row0 + lane < p.N) {
+                    const int64_t col_byte = (int64_t)(u.k0 + c0) * ESZ;
+                    const uint8_t *old = p.out + ((int64_t)u.e * p.N + row0 + lane) * p.out_row_bytes + col_byte;
 #pragma unroll
-                    for (int c = 0; c < 8; ++c) {
+                    for (int c = 0; c < 32 * ESZ / 16; ++c) {
                         if (col_byte + c * 16 >= p.out_row_bytes) continue;
                         Vec16 o;
                         o.u = *reinterpret_cast<const uint4 *>(old + c * 16);
                         if constexpr (OUT_F32) {
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) v[c * 4 + i] += o.f[i];
+                            for (int i = 0; i < 4; ++i)
+                                v[c * 4 + i] = __float_as_uint(__uint_as_float(v[c * 4 + i]) + o.f[i]);
                         } else {
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const float2 f = DT == DT_BF16 ? bf16x2_to_float2(o.w[i]) : f16x2_to_float2(o.w[i]);
-                                v[c * 8 + 2 * i] += f.x;
-                                v[c * 8 + 2 * i + 1] += f.y;
+                                v[c * 8 + 2 * i] = __float_as_uint(__uint_as_float(v[c * 8 + 2 * i]) + f.x);
+                                v[c * 8 + 2 * i + 1] = __float_as_uint(__uint_as_float(v[c * 8 + 2 * i + 1]) + f.y);
                             }
                         }
                     }
                 }
-                // this lane's row into the staging buffer, its 16-byte pieces
-                // rotated by the row so that neither side meets bank conflicts
 #pragma unroll
-                for (int c = 0; c < 8; ++c) {
-                    Vec16 o;
+                for (int h = 0; h < 32 / COLS; ++h, buf ^= 1) {
+                    uint8_t *stg = S.stg[warp - 2][buf];
+                    // the store before last has read this buffer
+                    if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    __syncwarp();
+                    // this lane's 64 bytes, in the 64-byte swizzle: 16-byte
+                    // piece c of row r at c ^ (r / 2 % 4), free of bank conflicts
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if constexpr (OUT_F32) o.f[i] = v[c * 4 + i];
-                        else o.w[i] = pack2<DT>(v[c * 8 + 2 * i], v[c * 8 + 2 * i + 1]);
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            w[i] = OUT_F32 ? v[(h * COLS + c * 4 + i) % 32]
+                                           : pack2<DT>(__uint_as_float(v[(c * 8 + 2 * i) % 32]),
+                                                       __uint_as_float(v[(c * 8 + 2 * i + 1) % 32]));
+                        *reinterpret_cast<uint4 *>(stg + lane * STG_ROW_BYTES + ((c ^ (lane >> 1 & 3)) << 4)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
                     }
-                    *reinterpret_cast<uint4 *>(stg + lane * STG_ROW_BYTES + ((c ^ (lane & 7)) << 4)) = o.u;
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (elect_one()) {
+                        if (c0 + h * COLS < width)
+                            asm volatile(
+                                "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group"
+                                " [%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(&map_out)),
+                                "r"(smem_u32(stg)), "r"(u.k0 + c0 + h * COLS), "r"(row0), "r"(u.e)
+                                : "memory");
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
                 }
-                __syncwarp();
-                const int64_t cb = col_byte + cch * 16;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const int rr = 4 * j + (lane >> 3);
-                    const uint4 o = *reinterpret_cast<const uint4 *>(stg + rr * STG_ROW_BYTES + ((cch ^ (rr & 7)) << 4));
-                    if (rr < rows_valid && cb < p.out_row_bytes)
-                        *reinterpret_cast<uint4 *>(base + rr * p.out_row_bytes + cb) = o;
-                }
-                __syncwarp();
             }
             tc_fence_before();
             __syncwarp();
@@ -365,6 +374,9 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
                 else mbar_arrive(&S.acc_empty[acc]);
             }
         }
+        // the stores have read their buffers and written what they carried
+        if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        __syncwarp();
     }
 
     // ------------------------------------------------------------ teardown
@@ -383,8 +395,24 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
 
 // ---- host side ---------------------------------------------------------------
 
+// grad_w [E, N, K] in boxes of 64 bytes x 32 rows, 64-byte swizzle.
+bool encode_out(CUtensorMap *m, CUtensorMapDataType dt, void *base, uint64_t K, uint64_t N, uint64_t E,
+                uint32_t esz)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    cuuint64_t dims[3] = {K, N, E};
+    cuuint64_t strides[2] = {K * esz, K * N * esz};
+    cuuint32_t box[3] = {STG_ROW_BYTES / esz, 32, 1};
+    cuuint32_t es[3] = {1, 1, 1};
+    return fn(m, dt, 3, base, dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int DT, int CG, bool OUT_F32>
-cudaError_t launch_kernel(const CUtensorMap &mg, const CUtensorMap &ma, WgradParams p, cudaStream_t s)
+cudaError_t launch_kernel(const CUtensorMap &mg, const CUtensorMap &ma, const CUtensorMap &mo, WgradParams p,
+                          cudaStream_t s)
 {
     // CTAs the GPU holds at once, per device; 0: the kernel is not yet opted
     // in to its shared memory there
@@ -428,7 +456,7 @@ cudaError_t launch_kernel(const CUtensorMap &mg, const CUtensorMap &ma, WgradPar
     const int64_t units = (int64_t)p.E * p.n_tiles * p.k_tiles;
     cfg.gridDim = dim3((unsigned)(CG * units < ctas ? CG * units : ctas));
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, mg, ma, p);
+    return cudaLaunchKernelEx(&cfg, kernel, mg, ma, mo, p);
 }
 
 template <int DT>
@@ -438,9 +466,11 @@ cudaError_t launch_dt(const void *grad, int64_t ldg, const void *a, int64_t lda,
 {
     const CUtensorMapDataType tdt =
         DT == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
-    CUtensorMap mg, ma;
+    CUtensorMap mg, ma, mo;
     if (!encode_2d_strided(&mg, tdt, grad, (uint64_t)N, (uint64_t)rows, (uint64_t)ldg * 2, 64, BK) ||
-        !encode_2d_strided(&ma, tdt, a, (uint64_t)K, (uint64_t)rows, (uint64_t)lda * 2, 64, BK))
+        !encode_2d_strided(&ma, tdt, a, (uint64_t)K, (uint64_t)rows, (uint64_t)lda * 2, 64, BK) ||
+        !encode_out(&mo, out_f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : tdt, grad_w, (uint64_t)K, (uint64_t)N,
+                    (uint64_t)E, out_f32 ? 4 : 2))
         return cudaErrorInvalidValue;
     WgradParams p{};
     p.offsets = offsets;
@@ -448,14 +478,14 @@ cudaError_t launch_dt(const void *grad, int64_t ldg, const void *a, int64_t lda,
     p.rows = (int)rows;
     p.N = (int)N;
     p.K = (int)K;
-    p.out = static_cast<uint8_t *>(grad_w);
+    p.out = static_cast<const uint8_t *>(grad_w);
     p.out_row_bytes = K * (out_f32 ? 4 : 2);
     p.accumulate = accumulate;
     p.status = status;
     p.wait_ns = wait_limit_ns();
     if (rows >= 1024 * (int64_t)E)
-        return out_f32 ? launch_kernel<DT, 2, true>(mg, ma, p, s) : launch_kernel<DT, 2, false>(mg, ma, p, s);
-    return out_f32 ? launch_kernel<DT, 1, true>(mg, ma, p, s) : launch_kernel<DT, 1, false>(mg, ma, p, s);
+        return out_f32 ? launch_kernel<DT, 2, true>(mg, ma, mo, p, s) : launch_kernel<DT, 2, false>(mg, ma, mo, p, s);
+    return out_f32 ? launch_kernel<DT, 1, true>(mg, ma, mo, p, s) : launch_kernel<DT, 1, false>(mg, ma, mo, p, s);
 }
 
 }  // namespace
