@@ -72,29 +72,5 @@ __device__ __forceinline__ int expert_of(const Segments &S, int E, int unit)
     return lo;
 }
 
-// One lane of a converged warp, always the same one. The tensor-core roles keep
-// the whole warp in their loops and elect a lane for each issue, so that
-// addresses and descriptors stay warp-uniform: a loop run by one lane alone
-// moves each operand into the uniform registers again for every instruction
-// (about 60 cycles per tcgen05.mma and 140 per TMA copy).
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(r));
-    return r != 0;
-}
-
-// Failure path only: gives this CTA's TMA copies a bounded time to land before
-// its shared memory goes.
-__device__ __forceinline__ void let_copies_land()
-{
-    const uint64_t t0 = global_timer_ns();
-    while (global_timer_ns() - t0 < 100000000ull) { }
-}
-
 }  // namespace
 }  // namespace moe

@@ -33,8 +33,8 @@
 
 #include "common.cuh"
 #include "grouped.cuh"
+#include "grouped_issue.cuh"
 #include "kernels.h"
-#include "tc_ptx.cuh"
 
 namespace moe {
 
@@ -99,28 +99,51 @@ struct Unit {
     int w0;          // first weight column of this CTA
 };
 
+// Walks a CTA's units in order. What depends on the expert alone is kept, and
+// the common case divides once: with five divisions and a search per unit the
+// MMA warp spent a thousand cycles between short units.
 template <int CG>
-__device__ __forceinline__ Unit unit_of(const Segments &S, const GemmParams &p, int unit, int rank)
-{
-    Unit u;
-    u.e = expert_of(S, p.E, unit);
-    const int cnt = S.count[u.e], local = unit - S.unit[u.e];
-    const int n_units = (cnt + p.tok_cap - 1) / p.tok_cap;
-    const int span = p.row_block * p.w_tiles;
-    const int b = local / span, rem = local - b * span;
-    const int left = n_units - b * p.row_block, width = left < p.row_block ? left : p.row_block;
-    const int wt = rem / width, j = b * p.row_block + rem - wt * width;
-    // equal widths: at most tok_cap, which is a multiple of the quantum, so
-    // that none of the n_units comes out empty
-    constexpr int Q = 16 * CG;
-    const int each = ((cnt + n_units - 1) / n_units + Q - 1) / Q * Q;
-    const int at = j * each;
-    u.rows = cnt - at < each ? cnt - at : each;
-    u.row0 = S.first[u.e] + at;
-    u.mma_n = (u.rows + Q - 1) / Q * Q;
-    u.w0 = (wt * CG + rank) * BM;
-    return u;
-}
+struct UnitWalk {
+    const Segments &S;
+    const GemmParams &p;
+    int rank, e, cnt, n_units, each;
+
+    __device__ __forceinline__ UnitWalk(const Segments &seg, const GemmParams &params, int r)
+        : S(seg), p(params), rank(r), e(-1), cnt(0), n_units(1), each(1) {}
+
+    __device__ __forceinline__ Unit at(int unit)
+    {
+        if (e < 0 || unit >= S.unit[e + 1]) {
+            e = expert_of(S, p.E, unit);
+            cnt = S.count[e];
+            n_units = (cnt + p.tok_cap - 1) / p.tok_cap;
+            // equal widths: at most tok_cap, which is a multiple of the
+            // quantum, so that none of the n_units comes out empty
+            constexpr int Q = 16 * CG;
+            each = ((cnt + n_units - 1) / n_units + Q - 1) / Q * Q;
+        }
+        Unit u;
+        u.e = e;
+        const int local = unit - S.unit[e];
+        int wt, j;
+        if (n_units <= p.row_block) {
+            wt = local / n_units;
+            j = local - wt * n_units;
+        } else {
+            const int span = p.row_block * p.w_tiles;
+            const int b = local / span, rem = local - b * span;
+            const int left = n_units - b * p.row_block, width = left < p.row_block ? left : p.row_block;
+            wt = rem / width;
+            j = b * p.row_block + rem - wt * width;
+        }
+        const int at = j * each;
+        u.rows = cnt - at < each ? cnt - at : each;
+        u.row0 = S.first[e] + at;
+        u.mma_n = (u.rows + 16 * CG - 1) / (16 * CG) * (16 * CG);
+        u.w0 = (wt * CG + rank) * BM;
+        return u;
+    }
+};
 
 // Barrier over the four epilogue warps.
 __device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -178,97 +201,97 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     const uint32_t tmem_base = S.tmem_base;
     const int total = S.seg.unit[p.E];
     volatile int *abort_flag = &S.abort;
+    UnitWalk<CG> walk(S.seg, p, rank);
 
-    if (warp == 0 || warp == 6) {
-        // ------------------------------- TMA producers: weights (0), rows (6)
+    if (warp == 0) {
+        // ------------------------------------------- TMA producer: weights
+        const uint32_t on = elect_lane(), arm = leader ? on : 0u;
+        const uint32_t ring = smem_u32(S.ring);
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (int unit = unit0; unit < total && ok; unit += unit_step) {
-            const Unit u = unit_of<CG>(S.seg, p, unit, rank);
+            const Unit u = walk.at(unit);
+            // both CTAs' copies of weights and rows complete on the leader's
+            // barrier, which expects them all; they may land before it is
+            // armed (the phase cannot complete while the arrival is pending)
+            const uint32_t bytes = CG * (W_BYTES + u.mma_n / CG * BK * 2);
+            for (int kb = 0; kb < num_kb; ++kb) {
+                ok = warp_wait<CG>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns);
+                if (!ok) break;
+                const uint32_t sw = ring + stage * p.slot_bytes, here = smem_u32(&S.full[stage]);
+                const uint32_t bar = CG == 2 ? mapa_shared(here, 0) : here;
+                expect_tx_on(arm, &S.full[stage], bytes);
+                if constexpr (KN) {
+                    load_3d_on<CG>(on, sw, &map_w, bar, u.w0, kb * BK, u.e);
+                    load_3d_on<CG>(on, sw + W_BYTES / 2, &map_w, bar, u.w0 + 64, kb * BK, u.e);
+                } else {
+                    load_3d_on<CG>(on, sw, &map_w, bar, kb * BK, u.w0, u.e);
+                }
+                if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+            }
+        }
+    } else if (warp == 6) {
+        // ------------------------------------------- TMA producer: rows
+        const uint32_t on = elect_lane();
+        const uint32_t ring = smem_u32(S.ring);
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        for (int unit = unit0; unit < total && ok; unit += unit_step) {
+            const Unit u = walk.at(unit);
             const int mine = u.mma_n / CG;               // rows this CTA loads
             const int row0 = u.row0 + rank * mine;
-            const uint32_t bytes = W_BYTES + mine * BK * 2;
             for (int kb = 0; kb < num_kb; ++kb) {
-                ok = __all_sync(0xffffffffu, mbar_wait<CG>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns));
+                ok = warp_wait<CG>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns);
                 if (!ok) break;
-                if (elect_one()) {
-                    uint8_t *sw = S.ring + stage * p.slot_bytes;
-                    // both CTAs' copies complete on the leader's barrier, which
-                    // expects both; the rows' and a peer's copies may land before
-                    // it is armed (the phase cannot complete while the arrival
-                    // is pending)
-                    const uint32_t bar = CG == 2 ? mapa_shared(smem_u32(&S.full[stage]), 0) : 0u;
-                    if (warp == 0) {
-                        if (leader) mbar_arrive_expect_tx(&S.full[stage], CG * bytes);
-                        auto load_w = [&](void *dst, int c0, int c1) {
-                            if constexpr (CG == 2) tma_load_3d_pair(dst, &map_w, bar, c0, c1, u.e);
-                            else tma_load_3d(dst, &map_w, &S.full[stage], c0, c1, u.e);
-                        };
-                        if constexpr (KN) {
-                            load_w(sw, u.w0, kb * BK);
-                            load_w(sw + W_BYTES / 2, u.w0 + 64, kb * BK);
-                        } else {
-                            load_w(sw, kb * BK, u.w0);
-                        }
-                    } else {
-                        uint8_t *sa = sw + W_BYTES;
-                        auto load_a = [&](int box, int at) {
-                            uint8_t *dst = sa + at * BK * 2;
-                            if constexpr (CG == 2) tma_load_2d_pair(dst, &map_a.m[box], bar, kb * BK, row0 + at);
-                            else tma_load_2d(dst, &map_a.m[box], &S.full[stage], kb * BK, row0 + at);
-                        };
-                        int at = 0;
-                        for (; mine - at >= 128; at += 128) load_a(0, at);
-                        if (mine & 64) { load_a(1, at); at += 64; }
-                        if (mine & 32) { load_a(2, at); at += 32; }
-                        if (mine & 16) load_a(3, at);
-                    }
-                }
-                __syncwarp();
+                const uint32_t sa = ring + stage * p.slot_bytes + W_BYTES, here = smem_u32(&S.full[stage]);
+                const uint32_t bar = CG == 2 ? mapa_shared(here, 0) : here;
+                auto load = [&](int box, int at) {
+                    load_2d_on<CG>(on, sa + at * BK * 2, &map_a.m[box], bar, kb * BK, row0 + at);
+                };
+                int at = 0;
+                for (; mine - at >= 128; at += 128) load(0, at);
+                if (mine & 64) { load(1, at); at += 64; }
+                if (mine & 32) { load(2, at); at += 32; }
+                if (mine & 16) load(3, at);
                 if (++stage == p.stages) { stage = 0; phase ^= 1u; }
             }
         }
     } else if (warp == 1 && leader) {
         // ------------------------------------------------------ MMA issuer
         constexpr uint32_t idesc0 = idesc_f16_major<DT>(BM * CG, 0, KN, false);
+        const uint32_t on = elect_lane();
+        const uint32_t ring = smem_u32(S.ring);
         int stage = 0;
         uint32_t phase = 0;
         int it = 0;
         bool ok = true;
         for (int unit = unit0; unit < total && ok; unit += unit_step, ++it) {
-            const Unit u = unit_of<CG>(S.seg, p, unit, rank);
+            const Unit u = walk.at(unit);
             const uint32_t idesc = idesc0 | ((uint32_t)(u.mma_n >> 3) << 17);
             const int acc = it & 1;
             const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
-            ok = __all_sync(0xffffffffu, mbar_wait<CG>(&S.acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_ns));
+            ok = warp_wait<CG>(&S.acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_ns);
             if (!ok) break;
-            tc_fence_after();
             const uint32_t d = tmem_base + (uint32_t)(acc * ACC_COLS);
             for (int kb = 0; kb < num_kb; ++kb) {
-                ok = __all_sync(0xffffffffu, mbar_wait<CG>(&S.full[stage], phase, abort_flag, p.status, p.wait_ns));
+                ok = warp_wait<CG>(&S.full[stage], phase, abort_flag, p.status, p.wait_ns);
                 if (!ok) break;
                 tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t w = smem_u32(S.ring + stage * p.slot_bytes), a = w + W_BYTES;
+                const uint32_t w = ring + stage * p.slot_bytes, a = w + W_BYTES;
 #pragma unroll
-                    for (int k = 0; k < BK / UK; ++k)
-                        umma_f16<CG>(d, KN ? sdesc_mn_sw128(w + k * UK * 128, W_BYTES / 2) : sdesc_k_sw128(w + k * UK * 2),
-                                     sdesc_k_sw128(a + k * UK * 2), idesc, (kb | k) != 0 ? 1u : 0u);
-                    if constexpr (CG == 2) umma_commit_pair(&S.empty[stage]);
-                    else umma_commit<1>(&S.empty[stage]);
-                    if (kb + 1 == num_kb) {
-                        if constexpr (CG == 2) umma_commit_pair(&S.acc_full[acc]);
-                        else umma_commit<1>(&S.acc_full[acc]);
-                    }
-                }
-                __syncwarp();
+                for (int k = 0; k < BK / UK; ++k)
+                    umma_on<CG>(on, d, KN ? sdesc_mn_sw128(w + k * UK * 128, W_BYTES / 2) : sdesc_k_sw128(w + k * UK * 2),
+                                sdesc_k_sw128(a + k * UK * 2), idesc, (kb | k) != 0 ? 1u : 0u);
+                commit_on<CG>(on, &S.empty[stage]);
                 if (++stage == p.stages) { stage = 0; phase ^= 1u; }
             }
+            if (ok) commit_on<CG>(on, &S.acc_full[acc]);
         }
-        if (elect_one()) {
-            // every MMA issued must finish before TMEM is released, also where
-            // another role has given up
+        // every MMA issued must finish before TMEM is released, also where
+        // another role has given up
+        if (on) {
             umma_commit<CG>(&S.drain);
             mbar_wait(&S.drain, 0, nullptr, p.status, kDrainLimitNs);
         }
@@ -283,7 +306,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         constexpr int PIECES = ROW_BYTES / 16, PER_IT = 128 / PIECES;
         int it = 0, buf = 0;
         for (int unit = unit0; unit < total; unit += unit_step, ++it) {
-            const Unit u = unit_of<CG>(S.seg, p, unit, rank);
+            const Unit u = walk.at(unit);
             const int acc = it & 1;
             const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
             // the four warps leave together: none may wait at a barrier for
@@ -470,10 +493,9 @@ cudaError_t launch_dt(const void *a, int64_t lda, const int32_t *offsets, int64_
                       int E, int64_t N, int64_t K, bool kn, void *out, int64_t ldo, bool out_f32,
                       unsigned *status, cudaStream_t s)
 {
-    if (rows >= 192 * (int64_t)E)
+    if (rows >= 64 * (int64_t)E)
         return launch_cg<DT, 2>(a, lda, offsets, rows, w, E, N, K, kn, out, ldo, out_f32, 256, status, s);
-    return launch_cg<DT, 1>(a, lda, offsets, rows, w, E, N, K, kn, out, ldo, out_f32,
-                            rows >= 32 * (int64_t)E ? 128 : 64, status, s);
+    return launch_cg<DT, 1>(a, lda, offsets, rows, w, E, N, K, kn, out, ldo, out_f32, 64, status, s);
 }
 
 }  // namespace

@@ -28,11 +28,12 @@
 //
 // Every wait is bounded, as in grouped_tc.cu.
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "grouped.cuh"
+#include "grouped_issue.cuh"
 #include "kernels.h"
-#include "tc_ptx.cuh"
 
 namespace moe {
 
@@ -95,26 +96,53 @@ struct Unit {
     int k0, mma_n;           // the unit's columns of grad_w, and how wide the MMA is
 };
 
+// Walks a CTA's units, first and then every step-th, as (expert, outer tile,
+// inner tile) without dividing between units.
 template <int CG>
-__device__ __forceinline__ Unit unit_of(const Segments &S, const WgradParams &p, int unit, int rank)
-{
-    Unit u;
-    const int per = p.n_tiles * p.k_tiles;
-    u.e = unit / per;
-    const int rem = unit - u.e * per;
-    const int nt = p.n_fast ? rem % p.n_tiles : rem / p.k_tiles;
-    const int kt = p.n_fast ? rem / p.n_tiles : rem % p.k_tiles;
-    u.row0 = S.first[u.e];
-    u.cnt = S.count[u.e];
-    u.nkb = (u.cnt + BK - 1) / BK;
-    u.tail = u.cnt - (u.nkb - 1) * BK;
-    u.n0 = (nt * CG + rank) * BM;
-    u.k0 = kt * BN;
-    // whole 64-column boxes for each CTA: an MN-major operand's 128-byte rows
-    const int left = p.K - u.k0;
-    u.mma_n = left >= BN ? BN : (left + 64 * CG - 1) / (64 * CG) * (64 * CG);
-    return u;
-}
+struct UnitWalk {
+    const Segments &S;
+    const WgradParams &p;
+    int rank, outer_n, inner_n;          // how many outer and inner tiles
+    int e, outer, inner, de, douter, dinner;
+
+    __device__ __forceinline__ void split(int unit, int &x, int &y, int &z) const
+    {
+        x = unit / (outer_n * inner_n);
+        const int rem = unit - x * (outer_n * inner_n);
+        y = rem / inner_n;
+        z = rem - y * inner_n;
+    }
+    __device__ __forceinline__ UnitWalk(const Segments &seg, const WgradParams &params, int r, int first, int step)
+        : S(seg), p(params), rank(r)
+    {
+        outer_n = p.n_fast ? p.k_tiles : p.n_tiles;
+        inner_n = p.n_fast ? p.n_tiles : p.k_tiles;
+        split(first, e, outer, inner);
+        split(step, de, douter, dinner);
+    }
+    // the current unit; moves on to the next
+    __device__ __forceinline__ Unit next()
+    {
+        Unit u;
+        const int nt = p.n_fast ? inner : outer, kt = p.n_fast ? outer : inner;
+        u.e = e;
+        u.row0 = S.first[e];
+        u.cnt = S.count[e];
+        u.nkb = (u.cnt + BK - 1) / BK;
+        u.tail = u.cnt - (u.nkb - 1) * BK;
+        u.n0 = (nt * CG + rank) * BM;
+        u.k0 = kt * BN;
+        // whole 64-column boxes for each CTA: an MN-major operand's 128-byte rows
+        const int left = p.K - u.k0;
+        u.mma_n = left >= BN ? BN : (left + 64 * CG - 1) / (64 * CG) * (64 * CG);
+        e += de;
+        outer += douter;
+        inner += dinner;
+        if (inner >= inner_n) { inner -= inner_n; ++outer; }
+        if (outer >= outer_n) { outer -= outer_n; ++e; }
+        return u;
+    }
+};
 
 template <int DT, int CG, bool OUT_F32>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -159,100 +187,108 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
     const uint32_t tmem_base = S.tmem_base;
     const int total = p.E * p.n_tiles * p.k_tiles;
     volatile int *abort_flag = &S.abort;
+    UnitWalk<CG> walk(S.seg, p, rank, unit0, unit_step);
 
-    if (warp == 0 || warp == 7) {
-        // ----------------------------------- TMA producers: grad (0), a (7)
+    // A producer's loop: loads(dst, bar, u, row) issues its copies of one
+    // stage; with ARM it also expects both producers' bytes.
+    auto produce = [&](uint32_t on, auto arm, auto loads) {
+        constexpr bool ARM = decltype(arm)::value;
+        const uint32_t ring = smem_u32(S.ring);
         int stage = 0;
         uint32_t phase = 0;
         bool ok = true;
         for (int unit = unit0; unit < total && ok; unit += unit_step) {
-            const Unit u = unit_of<CG>(S.seg, p, unit, rank);
-            const int mine = u.mma_n / CG;                    // columns of a this CTA loads
-            const int boxes = mine / 64, col0 = u.k0 + rank * mine;
-            const uint32_t bytes = G_BYTES + boxes * BOX_BYTES;
+            const Unit u = walk.next();
+            const uint32_t bytes = G_BYTES + u.mma_n / CG / 64 * BOX_BYTES;
             for (int kb = 0; kb < u.nkb; ++kb) {
-                ok = __all_sync(0xffffffffu, mbar_wait<CG>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns));
+                ok = warp_wait<CG>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns);
                 if (!ok) break;
-                if (elect_one()) {
-                    uint8_t *sg = S.ring[stage];
-                    // a stage with foreign rows completes in its own CTA, where
-                    // warp 6 zeroes them; any other on the leader's barrier,
-                    // which expects both CTAs' bytes (copies may land before it
-                    // is armed: the phase cannot complete while its arrival is
-                    // pending)
-                    const bool tail = kb == u.nkb - 1 && u.tail % UK != 0;
-                    uint64_t *local = tail ? &S.tail_in[stage] : &S.full[stage];
-                    const uint32_t bar = CG == 2 ? mapa_shared(smem_u32(local), tail ? (uint32_t)rank : 0u) : 0u;
-                    auto load = [&](void *dst, const CUtensorMap *m, int c) {
-                        if constexpr (CG == 2) tma_load_2d_pair(dst, m, bar, c, u.row0 + kb * BK);
-                        else tma_load_2d(dst, m, local, c, u.row0 + kb * BK);
-                    };
-                    if (warp == 0) {
-                        if (tail) {
-                            mbar_arrive_expect_tx(&S.tail_in[stage], bytes);
-                            if (leader) mbar_arrive(&S.full[stage]);
-                        } else if (leader) {
-                            mbar_arrive_expect_tx(&S.full[stage], CG * bytes);
-                        }
-                        load(sg, &map_g, u.n0);
-                        load(sg + BOX_BYTES, &map_g, u.n0 + 64);
-                    } else {
-                        for (int j = 0; j < boxes; ++j) load(sg + G_BYTES + j * BOX_BYTES, &map_a, col0 + j * 64);
+                // a stage with foreign rows completes in its own CTA, where
+                // warp 6 zeroes them; any other on the leader's barrier, which
+                // expects both CTAs' bytes (copies may land before it is armed:
+                // the phase cannot complete while its arrival is pending)
+                const bool tail = kb == u.nkb - 1 && u.tail % UK != 0;
+                uint32_t bar;
+                if (tail) {
+                    const uint32_t here = smem_u32(&S.tail_in[stage]);
+                    bar = CG == 2 ? mapa_shared(here, (uint32_t)rank) : here;
+                    if (ARM) {
+                        expect_tx_on(on, &S.tail_in[stage], bytes);
+                        if (leader) arrive_on(on, &S.full[stage]);
                     }
+                } else {
+                    const uint32_t here = smem_u32(&S.full[stage]);
+                    bar = CG == 2 ? mapa_shared(here, 0) : here;
+                    if (ARM && leader) expect_tx_on(on, &S.full[stage], CG * bytes);
                 }
-                __syncwarp();
+                loads(ring + stage * SLOT_BYTES<CG>, bar, u, u.row0 + kb * BK);
                 if (++stage == NS) { stage = 0; phase ^= 1u; }
             }
         }
+    };
+    if (warp == 0) {
+        // ------------------------------------------- TMA producer: grad
+        const uint32_t on = elect_lane();
+        produce(on, std::true_type{}, [&](uint32_t dst, uint32_t bar, const Unit &u, int row) {
+            load_2d_on<CG>(on, dst, &map_g, bar, u.n0, row);
+            load_2d_on<CG>(on, dst + BOX_BYTES, &map_g, bar, u.n0 + 64, row);
+        });
+    } else if (warp == 7) {
+        // ------------------------------------------- TMA producer: a
+        const uint32_t on = elect_lane();
+        produce(on, std::false_type{}, [&](uint32_t dst, uint32_t bar, const Unit &u, int row) {
+            const int mine = u.mma_n / CG, col0 = u.k0 + rank * mine;     // columns this CTA loads
+#pragma unroll
+            for (int j = 0; j < 4 / CG; ++j)
+                load_2d_on<CG>(j * 64 < mine ? on : 0u, dst + G_BYTES + j * BOX_BYTES, &map_a, bar, col0 + j * 64, row);
+        });
     } else if (warp == 1 && leader) {
         // ------------------------------------------------------ MMA issuer
         constexpr uint32_t idesc0 = idesc_f16_major<DT>(BM * CG, 0, true, true);
+        const uint32_t on = elect_lane();
+        const uint32_t ring = smem_u32(S.ring);
         int stage = 0;
         uint32_t phase = 0, tails = 0;
         int it = 0;
         bool ok = true;
         for (int unit = unit0; unit < total && ok; unit += unit_step, ++it) {
-            const Unit u = unit_of<CG>(S.seg, p, unit, rank);
+            const Unit u = walk.next();
             const uint32_t idesc = idesc0 | ((uint32_t)(u.mma_n >> 3) << 17);
             const int acc = it & 1;
             const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
-            ok = __all_sync(0xffffffffu, mbar_wait<CG>(&S.acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_ns));
+            ok = warp_wait<CG>(&S.acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_ns);
             if (!ok) break;
-            tc_fence_after();
             const uint32_t d = tmem_base + (uint32_t)(acc * ACC_COLS);
             for (int kb = 0; kb < u.nkb; ++kb) {
-                ok = __all_sync(0xffffffffu, mbar_wait<CG>(&S.full[stage], phase, abort_flag, p.status, p.wait_ns));
+                ok = warp_wait<CG>(&S.full[stage], phase, abort_flag, p.status, p.wait_ns);
                 if (!ok) break;
                 const int valid = kb == u.nkb - 1 ? u.tail : BK;
                 if (valid % UK != 0) {
-                    ok = __all_sync(0xffffffffu, mbar_wait<CG>(&S.tail_out[stage], tails >> stage & 1u, abort_flag, p.status, p.wait_ns));
+                    ok = warp_wait<CG>(&S.tail_out[stage], tails >> stage & 1u, abort_flag, p.status, p.wait_ns);
                     if (!ok) break;
                     tails ^= 1u << stage;
                 }
                 tc_fence_after();
-                if (elect_one()) {
-                    const uint32_t g = smem_u32(S.ring[stage]), a = g + G_BYTES;
+                const uint32_t g = ring + stage * SLOT_BYTES<CG>, a = g + G_BYTES;
+                auto mma = [&](int k) {
+                    umma_on<CG>(on, d, sdesc_mn_sw128(g + k * UK * 128, BOX_BYTES),
+                                sdesc_mn_sw128(a + k * UK * 128, BOX_BYTES), idesc, (kb | k) != 0 ? 1u : 0u);
+                };
+                if (valid == BK) {
 #pragma unroll
-                    for (int k = 0; k < BK / UK; ++k)
-                        if (k * UK < valid)
-                            umma_f16<CG>(d, sdesc_mn_sw128(g + k * UK * 128, BOX_BYTES),
-                                         sdesc_mn_sw128(a + k * UK * 128, BOX_BYTES), idesc, (kb | k) != 0 ? 1u : 0u);
-                    if constexpr (CG == 2) umma_commit_pair(&S.empty[stage]);
-                    else umma_commit<1>(&S.empty[stage]);
+                    for (int k = 0; k < BK / UK; ++k) mma(k);
+                } else {
+                    for (int k = 0; k * UK < valid; ++k) mma(k);
                 }
-                __syncwarp();
+                commit_on<CG>(on, &S.empty[stage]);
                 if (++stage == NS) { stage = 0; phase ^= 1u; }
             }
             // (an expert without rows commits with no MMA: its epilogue writes zeros)
-            if (ok && elect_one()) {
-                if constexpr (CG == 2) umma_commit_pair(&S.acc_full[acc]);
-                else umma_commit<1>(&S.acc_full[acc]);
-            }
-            __syncwarp();
+            if (ok) commit_on<CG>(on, &S.acc_full[acc]);
         }
-        if (elect_one()) {
-            // every MMA issued must finish before TMEM is released, also where
-            // another role has given up
+        // every MMA issued must finish before TMEM is released, also where
+        // another role has given up
+        if (on) {
             umma_commit<CG>(&S.drain);
             mbar_wait(&S.drain, 0, nullptr, p.status, kDrainLimitNs);
         }
@@ -262,7 +298,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
         int stage = 0;
         uint32_t tails = 0;
         for (int unit = unit0; unit < total; unit += unit_step) {
-            const Unit u = unit_of<CG>(S.seg, p, unit, rank);
+            const Unit u = walk.next();
             if (u.nkb == 0) continue;
             stage = (stage + u.nkb - 1) % NS;                 // the unit's last stage
             if (u.tail % UK != 0) {
@@ -292,9 +328,10 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
         const int q = warp & 3;                    // TMEM lane quadrant of this warp
         constexpr int ESZ = OUT_F32 ? 4 : 2;
         constexpr int COLS = STG_ROW_BYTES / ESZ;  // columns per staging buffer: 16 / 32
+        const uint32_t on = elect_lane();
         int it = 0, buf = 0;
         for (int unit = unit0; unit < total; unit += unit_step, ++it) {
-            const Unit u = unit_of<CG>(S.seg, p, unit, rank);
+            const Unit u = walk.next();
             const int acc = it & 1;
             const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
             const bool ready = mbar_wait<CG>(&S.acc_full[acc], acc_phase, abort_flag, p.status, p.wait_ns);
@@ -339,7 +376,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
                 for (int h = 0; h < 32 / COLS; ++h, buf ^= 1) {
                     uint8_t *stg = S.stg[warp - 2][buf];
                     // the store before last has read this buffer
-                    if (elect_one()) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+                    if (on) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
                     __syncwarp();
                     // this lane's 64 bytes, in the 64-byte swizzle: 16-byte
                     // piece c of row r at c ^ (r / 2 % 4), free of bank conflicts
@@ -356,7 +393,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
                     }
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
-                    if (elect_one()) {
+                    if (on) {
                         if (c0 + h * COLS < width)
                             asm volatile(
                                 "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group"
@@ -375,7 +412,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
             }
         }
         // the stores have read their buffers and written what they carried
-        if (elect_one()) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+        if (on) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         __syncwarp();
     }
 
@@ -483,7 +520,7 @@ cudaError_t launch_dt(const void *grad, int64_t ldg, const void *a, int64_t lda,
     p.accumulate = accumulate;
     p.status = status;
     p.wait_ns = wait_limit_ns();
-    if (rows >= 1024 * (int64_t)E)
+    if (rows >= 512 * (int64_t)E)
         return out_f32 ? launch_kernel<DT, 2, true>(mg, ma, mo, p, s) : launch_kernel<DT, 2, false>(mg, ma, mo, p, s);
     return out_f32 ? launch_kernel<DT, 1, true>(mg, ma, mo, p, s) : launch_kernel<DT, 1, false>(mg, ma, mo, p, s);
 }
