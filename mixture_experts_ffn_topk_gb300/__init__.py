@@ -900,18 +900,26 @@ def moe_swiglu_checkpoint_layout(rows: int, I: int) -> CheckpointLayout:
     return layout
 
 
+def _checkpoint_planes(rows: int, I: int):
+    """``moe_swiglu_checkpoint_layout`` in host arithmetic: (row_codes,
+    row_scales, up_codes, gate_scales, up_scales, total)."""
+    S = (I + 31) // 32
+    codes, scales = (rows * S * 32 + 255) & -256, (rows * S + 255) & -256
+    return S * 32, S, codes, 2 * codes, 2 * codes + scales, 2 * (codes + scales)
+
+
 def swiglu_checkpoint_views(ckpt: torch.Tensor, rows: int, I: int) -> dict:
     """The planes of a checkpoint as views: ``gate_codes`` and ``up_codes``
     (``float8_e4m3fn [rows, P]``, P = I rounded up to 32) and ``gate_scales``,
     ``up_scales`` (``uint8 [rows, P / 32]``, the scale ``2^(byte - 127)``)."""
-    p = moe_swiglu_checkpoint_layout(rows, I)
-    if ckpt.dtype != torch.uint8 or ckpt.dim() != 1 or ckpt.numel() < p.total or not ckpt.is_contiguous():
-        raise ValueError(f"ckpt must be a contiguous uint8 vector of at least {p.total} bytes")
-    codes, P, S, at = ckpt.view(torch.float8_e4m3fn), p.row_codes, p.row_scales, ckpt.storage_offset()
-    return {"gate_codes": codes.as_strided((rows, P), (P, 1), at + p.gate_codes),
-            "up_codes": codes.as_strided((rows, P), (P, 1), at + p.up_codes),
-            "gate_scales": ckpt.as_strided((rows, S), (S, 1), at + p.gate_scales),
-            "up_scales": ckpt.as_strided((rows, S), (S, 1), at + p.up_scales)}
+    P, S, up_codes, gate_scales, up_scales, total = _checkpoint_planes(rows, I)
+    if ckpt.dtype != torch.uint8 or ckpt.dim() != 1 or ckpt.numel() < total or not ckpt.is_contiguous():
+        raise ValueError(f"ckpt must be a contiguous uint8 vector of at least {total} bytes")
+    codes, at = ckpt.view(torch.float8_e4m3fn), ckpt.storage_offset()
+    return {"gate_codes": codes.as_strided((rows, P), (P, 1), at),
+            "up_codes": codes.as_strided((rows, P), (P, 1), at + up_codes),
+            "gate_scales": ckpt.as_strided((rows, S), (S, 1), at + gate_scales),
+            "up_scales": ckpt.as_strided((rows, S), (S, 1), at + up_scales)}
 
 
 def _checkpoint(ckpt: torch.Tensor, dev) -> int:
@@ -939,7 +947,7 @@ def moe_swiglu_checkpoint(g: torch.Tensor, u: torch.Tensor, offsets=None, h=None
     else:
         ldh = _ld("h", h, rows, I, dt, dev)
     if ckpt is None:
-        ckpt = torch.empty(moe_swiglu_checkpoint_size(rows, I), dtype=torch.uint8, device=dev)
+        ckpt = torch.empty(_checkpoint_planes(rows, I)[5], dtype=torch.uint8, device=dev)
     _enqueue("moe_swiglu_checkpoint", dev, stream, g.data_ptr(), u.data_ptr(), ld,
              None if offsets is None else offsets.data_ptr(), E, rows, I, _code(dt), h.data_ptr(),
              ldh, ckpt.data_ptr(), _checkpoint(ckpt, dev))

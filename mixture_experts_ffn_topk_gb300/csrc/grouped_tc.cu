@@ -10,16 +10,17 @@
 // and a decode step's one or two rows per expert cost a 16-wide MMA over a
 // weight tile that is loaded whole: the kernel streams weights.
 //
-// Per CTA (one per SM, 224 threads, persistent over the units):
+// Per CTA (one per SM, 352 threads, persistent over the units):
 //   warp 0     TMA producer of the weights: 128 columns x 64 k (16 KiB; one box
 //              of K-major rows, or two MN-major boxes of 64 n for [E, K, N])
 //              per stage of a ring of 192 KiB;
 //   warp 6     TMA producer of the unit's rows x 64 k, into the same stages;
 //   warp 1     tcgen05.mma issuer, K = 16 per instruction, two accumulators of
 //              256 TMEM columns in turn;
-//   warps 2-5  epilogue: TMEM lane = n, column = row of the segment. 32 rows
-//              (16 of FP32) at a time are rounded, transposed through shared
-//              memory and stored as 256 (512) consecutive bytes per row.
+//   warps 2-5, 7-10  epilogue, two groups that take turns: TMEM lane = n,
+//              column = row of the segment. 16 rows (8 of FP32) at a time are
+//              rounded, transposed through shared memory and stored as 256
+//              (512) consecutive bytes per row.
 // CTA pairs (CG = 2): M = 256, each CTA holds its 128 weight columns and half
 // of the unit's rows; the even CTA issues the MMAs for both.
 // An expert's rows are cut into units of equal width, at most tok_cap; units
@@ -48,8 +49,9 @@ constexpr int RING_BYTES = 192 << 10;
 constexpr int MAX_STAGES = 10;
 constexpr int ACC_COLS = 256;
 constexpr int TMEM_COLS = 2 * ACC_COLS;
-constexpr int THREADS = 224;
-constexpr int STG_BYTES = 8192;          // one epilogue staging buffer
+constexpr int THREADS = 352;
+constexpr int EPI_WARPS = 8;             // two groups of four: 2-5 and 7-10
+constexpr int STG_BYTES = 4096;          // one epilogue staging buffer
 constexpr uint64_t kDrainLimitNs = 100000000ull;
 // Bytes of rows a block of row units may cover, well inside the 129 MB L2
 // that also carries the streamed weights and the output.
@@ -57,7 +59,7 @@ constexpr int64_t kRowBlockBytes = 48ll << 20;
 
 struct __align__(1024) Smem {
     uint8_t ring[RING_BYTES];
-    uint8_t stg[2][STG_BYTES];
+    uint8_t stg[2][2][STG_BYTES];        // two per group of epilogue warps
     uint64_t full[MAX_STAGES];
     uint64_t empty[MAX_STAGES];
     uint64_t acc_full[2];
@@ -145,22 +147,39 @@ struct UnitWalk {
     }
 };
 
-// Barrier over the four epilogue warps.
-__device__ __forceinline__ void epi_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Barrier over the four warps of an epilogue group (id: 1 or 2).
+__device__ __forceinline__ void epi_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
 
 // The same, true in all of them if `ok` is in all.
-__device__ __forceinline__ bool epi_all(bool ok)
+__device__ __forceinline__ bool epi_all(int id, bool ok)
 {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.pred q, 1, 128, p;\n\t"
+        "barrier.cta.red.and.pred q, %2, 128, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
-        : "r"((uint32_t)ok)
+        : "r"((uint32_t)ok), "r"(id)
         : "memory");
     return r != 0;
+}
+
+// 32 TMEM lanes x 8 consecutive fp32 columns.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld_wait8(uint32_t (&r)[8])
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+    asm volatile(""
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
+                   "+r"(r[7]));
 }
 
 template <int DT, int CG, bool KN, bool OUT_F32>
@@ -178,7 +197,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) { mbar_init(&S.full[s], 1); mbar_init(&S.empty[s], 1); }
-        for (int a = 0; a < 2; ++a) { mbar_init(&S.acc_full[a], 1); mbar_init(&S.acc_empty[a], 4 * CG); }
+        for (int a = 0; a < 2; ++a) { mbar_init(&S.acc_full[a], 1); mbar_init(&S.acc_empty[a], EPI_WARPS * CG); }
         mbar_init(&S.drain, 1);
         S.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -299,8 +318,9 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     } else if (warp >= 2) {
         // ------------------------------------------------------ epilogue
         const int q = warp & 3;                          // TMEM lane quadrant of this warp
-        const int tid = threadIdx.x - 64;                // 0..127
-        constexpr int CH = OUT_F32 ? 16 : 32;            // rows per staging buffer
+        const int group = warp >= 7 ? 1 : 0;             // takes every second chunk of rows
+        const int tid = threadIdx.x - (group ? 224 : 64);     // 0..127 in the group
+        constexpr int CH = OUT_F32 ? 8 : 16;             // rows per staging buffer
         constexpr int ESZ = OUT_F32 ? 4 : 2;
         constexpr int ROW_BYTES = BM * ESZ;              // staged bytes per row: 512 / 256
         constexpr int PIECES = ROW_BYTES / 16, PER_IT = 128 / PIECES;
@@ -309,48 +329,39 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             const Unit u = walk.at(unit);
             const int acc = it & 1;
             const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
-            // the four warps leave together: none may wait at a barrier for
+            // a group's warps leave together: none may wait at a barrier for
             // one that has given up
-            if (!epi_all(mbar_wait<CG>(&S.acc_full[acc], acc_phase, abort_flag, p.status, p.wait_ns))) break;
+            if (!epi_all(1 + group, mbar_wait<CG>(&S.acc_full[acc], acc_phase, abort_flag, p.status, p.wait_ns))) break;
             tc_fence_after();
             const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
             const int piece = tid % PIECES, col = u.w0 + piece * (16 / ESZ);
             uint8_t *out0 = p.out + (int64_t)u.row0 * p.out_row_bytes + (int64_t)col * ESZ;
             const bool whole = p.vec && col + 16 / ESZ <= p.N;
-            for (int t0 = 0; t0 < u.rows; t0 += CH, buf ^= 1) {
-                uint8_t *mine = S.stg[buf] + (q * 32 + lane) * ESZ;
+            for (int t0 = group * CH; t0 < u.rows; t0 += 2 * CH, buf ^= 1) {
+                uint8_t *stg = S.stg[group][buf], *mine = stg + (q * 32 + lane) * ESZ;
                 if constexpr (OUT_F32) {
+                    uint32_t v[8];
+                    tmem_ld8(tbase + t0, v);
+                    tmem_ld_wait8(v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint32_t *>(mine + i * ROW_BYTES) = v[i];
+                } else {
                     uint32_t v[16];
                     tmem_ld16(tbase + t0, v);
                     tmem_ld_wait16(v);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) *reinterpret_cast<uint32_t *>(mine + i * ROW_BYTES) = v[i];
-                } else {
-                    uint32_t v[32];
-                    tmem_ld32(tbase + t0, v);
-                    tmem_ld_wait(v);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
+                    for (int i = 0; i < 8; ++i) {
                         const uint32_t w = pack2<DT>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
                         *reinterpret_cast<uint16_t *>(mine + 2 * i * ROW_BYTES) = (uint16_t)w;
                         *reinterpret_cast<uint16_t *>(mine + (2 * i + 1) * ROW_BYTES) = (uint16_t)(w >> 16);
                     }
                 }
-                if (t0 + CH >= u.rows) {
-                    // the accumulator is read: the next unit but one may have it
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (CG == 2 && !leader) mbar_arrive_cluster(mapa_shared(smem_u32(&S.acc_empty[acc]), 0));
-                        else mbar_arrive(&S.acc_empty[acc]);
-                    }
-                }
                 // one barrier per buffer: who passes it has read the other one
-                epi_sync();
+                epi_sync(1 + group);
 #pragma unroll
                 for (int i = 0; i < CH / PER_IT; ++i) {
                     const int t = i * PER_IT + tid / PIECES;
-                    const uint4 v = *reinterpret_cast<const uint4 *>(S.stg[buf] + t * ROW_BYTES + piece * 16);
+                    const uint4 v = *reinterpret_cast<const uint4 *>(stg + t * ROW_BYTES + piece * 16);
                     if (t0 + t >= u.rows) continue;
                     uint8_t *dst = out0 + (int64_t)(t0 + t) * p.out_row_bytes;
                     if (whole) {
@@ -365,6 +376,13 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                         }
                     }
                 }
+            }
+            // the accumulator is read: the next unit but one may have it
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2 && !leader) mbar_arrive_cluster(mapa_shared(smem_u32(&S.acc_empty[acc]), 0));
+                else mbar_arrive(&S.acc_empty[acc]);
             }
         }
     }
