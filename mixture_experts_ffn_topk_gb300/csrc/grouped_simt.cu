@@ -5,11 +5,15 @@
 //   product       out[r, n] = sum_k a[r, k] w[e][n, k]   (or w[e][k, n])
 //   weight grad   grad_w[e][n, k] = sum_r grad[r, n] a[r, k]
 // One tiled kernel: C [M, N] = sum_k X(m, k) Y(n, k), where each operand is
-// stored either with k contiguous (X[m][k]) or with m contiguous (X[k][m]).
-// Tiles of BM x BN outputs, TM x TN of them per thread, k in steps of BK kept
-// twice in shared memory (k-major, so that a thread's TM and TN values are
-// vector loads); the next step's global loads are in flight during the
-// current one's products.
+// stored either with k contiguous (X[m][k]) or with m contiguous (X[k][m]), and
+// is kept so in shared memory: a ring of steps filled by 16-byte asynchronous
+// copies, several steps ahead, zero-filled at the edges. A thread computes
+// TM x TN outputs, four k at a time. Its rows and columns lie one thread apart
+// where k is contiguous (padded rows: no bank conflicts), in fours otherwise.
+// Bound: FP32 multiply-adds with many rows per expert, the weights' bytes with
+// few, so the tile's height follows the average number of rows.
+#include <atomic>
+
 #include "common.cuh"
 #include "grouped.cuh"
 #include "kernels.h"
@@ -24,23 +28,86 @@ struct SimtOperand {
     int64_t per_expert;     // elements between experts' matrices (0: rows of a dispatched matrix)
 };
 
+// 16 bytes, or zeros where !ok (then src is any readable address).
+__device__ __forceinline__ void copy16(float *dst, const float *src, bool ok)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     static_cast<uint32_t>(__cvta_generic_to_shared(dst))),
+                 "l"(src), "r"(ok ? 16 : 0)
+                 : "memory");
+}
+
+template <int B, int BK, bool MAJOR>
+constexpr int kTileFloats = MAJOR ? BK * (B + 4) : B * (BK + 4);
+
+// Tile of an operand: `extent` of B indices from i0, k from k0 to k_end.
+template <int B, int BK, bool MAJOR, int THREADS>
+__device__ __forceinline__ void fetch_tile(float *dst, const float *p, int64_t ld, int i0, int i_end,
+                                           int k0, int k_end)
+{
+    constexpr int VECS = B * BK / 4;
+#pragma unroll
+    for (int q = 0; q < (VECS + THREADS - 1) / THREADS; ++q) {
+        const int v = threadIdx.x + q * THREADS;
+        if (VECS % THREADS != 0 && v >= VECS) break;
+        const int i = MAJOR ? v % (B / 4) * 4 : v / (BK / 4);
+        const int k = MAJOR ? v / (B / 4) : v % (BK / 4) * 4;
+        const bool ok = i0 + i < i_end && k0 + k < k_end;
+        const int64_t at = MAJOR ? (int64_t)(k0 + k) * ld + i0 + i : (int64_t)(i0 + i) * ld + k0 + k;
+        copy16(dst + (MAJOR ? k * (B + 4) + i : i * (BK + 4) + k), ok ? p + at : p, ok);
+    }
+}
+
+// Index of a thread's j-th row or column: T of them, `groups` threads side by side.
+template <int T, int GROUPS, bool MAJOR>
+__device__ __forceinline__ int index_of(int j, int t)
+{
+    return MAJOR ? j / 4 * (GROUPS * 4) + t * 4 + j % 4 : j * GROUPS + t;
+}
+
+// A thread's values of an operand at k, ..., k + 3.
+template <int B, int BK, int T, int GROUPS, bool MAJOR>
+__device__ __forceinline__ void frag(const float *tile, int k, int t, float (&f)[T][4])
+{
+    if constexpr (MAJOR) {
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+            for (int j = 0; j < T; j += 4) {
+                const float4 v = *reinterpret_cast<const float4 *>(
+                    tile + (k + kk) * (B + 4) + index_of<T, GROUPS, true>(j, t));
+                f[j][kk] = v.x; f[j + 1][kk] = v.y; f[j + 2][kk] = v.z; f[j + 3][kk] = v.w;
+            }
+    } else {
+#pragma unroll
+        for (int j = 0; j < T; ++j)
+            *reinterpret_cast<float4 *>(f[j]) = *reinterpret_cast<const float4 *>(
+                tile + index_of<T, GROUPS, false>(j, t) * (BK + 4) + k);
+    }
+}
+
 // WG: the reduction runs over the expert's rows (X = grad, Y = a, both stored
 // with the output index contiguous). Otherwise X = a (k contiguous), Y = w,
 // k contiguous unless Y_MAJOR.
-template <bool WG, bool Y_MAJOR, int BM, int BN, int TM, int TN>
+template <bool WG, bool Y_MAJOR, int BM, int BN, int TM, int TN, int BK, int STAGES>
+struct SimtShape {
+    static constexpr int THREADS = BM / TM * (BN / TN);
+    static constexpr int X_FLOATS = kTileFloats<BM, BK, WG>, Y_FLOATS = kTileFloats<BN, BK, Y_MAJOR>;
+    static constexpr size_t SMEM = sizeof(float) * STAGES * (X_FLOATS + Y_FLOATS);
+};
+
+template <bool WG, bool Y_MAJOR, int BM, int BN, int TM, int TN, int BK, int STAGES>
 __global__ void __launch_bounds__(BM / TM * (BN / TN))
 grouped_simt_kernel(SimtOperand x, SimtOperand y, const int32_t *__restrict__ offsets, int E,
                     int rows, int M, int N, int K, float *__restrict__ out, int64_t ldo,
                     int accumulate, unsigned *status)
 {
-    constexpr int BK = 16, THREADS = BM / TM * (BN / TN);
-    constexpr int XV = BM * BK / 4 / THREADS, YV = BN * BK / 4 / THREADS;
-    static_assert(XV >= 1 && YV >= 1, "each thread loads at least one vector of each operand");
-    constexpr bool X_MAJOR = WG;
+    using Shape = SimtShape<WG, Y_MAJOR, BM, BN, TM, TN, BK, STAGES>;
+    constexpr int THREADS = Shape::THREADS, GM = BM / TM, GN = BN / TN;
     __shared__ Segments S;
     __shared__ int warp_sum[THREADS / 32];
-    __shared__ __align__(16) float Xs[2][BK][BM + 4];
-    __shared__ __align__(16) float Ys[2][BK][BN + 4];
+    extern __shared__ __align__(16) float ring[];
+    float *xs = ring, *ys = ring + STAGES * Shape::X_FLOATS;
     pdl_wait();
     pdl_launch_dependents();
     const int nt = (N + BN - 1) / BN;
@@ -49,7 +116,7 @@ grouped_simt_kernel(SimtOperand x, SimtOperand y, const int32_t *__restrict__ of
     });
     __syncthreads();
     const int total = S.unit[E];
-    const int tm = threadIdx.x / (BN / TN), tn = threadIdx.x % (BN / TN);
+    const int tm = threadIdx.x / GN, tn = threadIdx.x % GN;
     for (int unit = blockIdx.x; unit < total; unit += gridDim.x) {
         const int e = expert_of(S, E, unit), loc = unit - S.unit[e];
         const int first = S.first[e], cnt = S.count[e];
@@ -58,119 +125,120 @@ grouped_simt_kernel(SimtOperand x, SimtOperand y, const int32_t *__restrict__ of
         // element (0, 0) of this unit's operands
         const float *xp = x.p + (int64_t)first * x.ld;
         const float *yp = y.p + (WG ? (int64_t)first * y.ld : (int64_t)e * y.per_expert);
-
-        float4 xr[XV], yr[YV];
-        // one vector of four: along k (k contiguous) or along the output index
-        auto fetch = [&](const float *p, int64_t ld, bool major, int i0, int i_end, int k0, int v, int B) {
-            int i, k;
-            if (major) { k = v / (B / 4); i = v % (B / 4) * 4; }
-            else { i = v / (BK / 4); k = v % (BK / 4) * 4; }
-            float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (i0 + i < i_end && k0 + k < k_end)
-                r = *reinterpret_cast<const float4 *>(
-                    p + (major ? (int64_t)(k0 + k) * ld + i0 + i : (int64_t)(i0 + i) * ld + k0 + k));
-            return r;
-        };
-        auto fetch_all = [&](int k0) {
-#pragma unroll
-            for (int q = 0; q < XV; ++q)
-                xr[q] = fetch(xp, x.ld, X_MAJOR, m0, m_end, k0, threadIdx.x + q * THREADS, BM);
-#pragma unroll
-            for (int q = 0; q < YV; ++q)
-                yr[q] = fetch(yp, y.ld, Y_MAJOR, n0, N, k0, threadIdx.x + q * THREADS, BN);
-        };
-        auto put = [&](int buf) {
-#pragma unroll
-            for (int q = 0; q < XV; ++q) {
-                const int v = threadIdx.x + q * THREADS;
-                if (X_MAJOR) {
-                    *reinterpret_cast<float4 *>(&Xs[buf][v / (BM / 4)][v % (BM / 4) * 4]) = xr[q];
-                } else {
-                    const int i = v / (BK / 4), k = v % (BK / 4) * 4;
-                    Xs[buf][k][i] = xr[q].x; Xs[buf][k + 1][i] = xr[q].y;
-                    Xs[buf][k + 2][i] = xr[q].z; Xs[buf][k + 3][i] = xr[q].w;
-                }
+        const int steps = (k_end + BK - 1) / BK;
+        auto fetch = [&](int t) {
+            if (t < steps) {
+                fetch_tile<BM, BK, WG, THREADS>(xs + t % STAGES * Shape::X_FLOATS, xp, x.ld, m0, m_end, t * BK, k_end);
+                fetch_tile<BN, BK, Y_MAJOR, THREADS>(ys + t % STAGES * Shape::Y_FLOATS, yp, y.ld, n0, N, t * BK, k_end);
             }
-#pragma unroll
-            for (int q = 0; q < YV; ++q) {
-                const int v = threadIdx.x + q * THREADS;
-                if (Y_MAJOR) {
-                    *reinterpret_cast<float4 *>(&Ys[buf][v / (BN / 4)][v % (BN / 4) * 4]) = yr[q];
-                } else {
-                    const int i = v / (BK / 4), k = v % (BK / 4) * 4;
-                    Ys[buf][k][i] = yr[q].x; Ys[buf][k + 1][i] = yr[q].y;
-                    Ys[buf][k + 2][i] = yr[q].z; Ys[buf][k + 3][i] = yr[q].w;
-                }
-            }
+            asm volatile("cp.async.commit_group;" ::: "memory");
         };
-
         float acc[TM][TN];
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; ++j) acc[i][j] = 0.0f;
-        const int steps = (k_end + BK - 1) / BK;
-        if (steps > 0) {
-            fetch_all(0);
-            put(0);
-        }
-        __syncthreads();
+        for (int t = 0; t < STAGES - 1; ++t) fetch(t);
         for (int t = 0; t < steps; ++t) {
-            const int buf = t & 1;
-            if (t + 1 < steps) fetch_all((t + 1) * BK);
+            asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+            __syncthreads();            // step t is here, and all are done with step t - 1
+            fetch(t + STAGES - 1);
+            const float *xt = xs + t % STAGES * Shape::X_FLOATS, *yt = ys + t % STAGES * Shape::Y_FLOATS;
 #pragma unroll
-            for (int k = 0; k < BK; ++k) {
-                float a[TM], b[TN];
+            for (int k = 0; k < BK; k += 4) {
+                float a[TM][4], b[TN][4];
+                frag<BM, BK, TM, GM, WG>(xt, k, tm, a);
+                frag<BN, BK, TN, GN, Y_MAJOR>(yt, k, tn, b);
 #pragma unroll
-                for (int i = 0; i < TM; i += 2)
-                    *reinterpret_cast<float2 *>(&a[i]) = *reinterpret_cast<const float2 *>(&Xs[buf][k][tm * TM + i]);
+                for (int kk = 0; kk < 4; ++kk)
 #pragma unroll
-                for (int j = 0; j < TN; j += 2)
-                    *reinterpret_cast<float2 *>(&b[j]) = *reinterpret_cast<const float2 *>(&Ys[buf][k][tn * TN + j]);
+                    for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int i = 0; i < TM; ++i)
-#pragma unroll
-                    for (int j = 0; j < TN; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+                        for (int j = 0; j < TN; ++j) acc[i][j] = fmaf(a[i][kk], b[j][kk], acc[i][j]);
             }
-            if (t + 1 < steps) put(buf ^ 1);
-            __syncthreads();
         }
+        __syncthreads();                // the ring is free for the next unit
         const int64_t out0 = WG ? (int64_t)e * M * ldo : (int64_t)first * ldo;
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-            const int m = m0 + tm * TM + i;
+            const int m = m0 + index_of<TM, GM, WG>(i, tm);
             if (m >= m_end) continue;
+            float *row = out + out0 + (int64_t)m * ldo;
+            if constexpr (WG) {
+                // rows of grad_w are whole vectors
 #pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                const int n = n0 + tn * TN + j;
-                if (n >= N) continue;
-                const int64_t at = out0 + (int64_t)m * ldo + n;
-                out[at] = accumulate ? out[at] + acc[i][j] : acc[i][j];
+                for (int j = 0; j < TN; j += 4) {
+                    const int n = n0 + index_of<TN, GN, true>(j, tn);
+                    if (n >= N) continue;
+                    float4 v = make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+                    if (accumulate) {
+                        const float4 old = *reinterpret_cast<const float4 *>(row + n);
+                        v = make_float4(old.x + v.x, old.y + v.y, old.z + v.z, old.w + v.w);
+                    }
+                    *reinterpret_cast<float4 *>(row + n) = v;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    const int n = n0 + index_of<TN, GN, Y_MAJOR>(j, tn);
+                    if (n < N) row[n] = acc[i][j];
+                }
             }
         }
     }
 }
 
-template <bool WG, bool Y_MAJOR, int BM, int BN, int TM, int TN>
+template <bool WG, bool Y_MAJOR, int BM, int BN, int TM, int TN, int BK, int STAGES>
 cudaError_t launch_tile(const SimtOperand &x, const SimtOperand &y, const int32_t *offsets, int E,
                         int64_t rows, int M, int N, int K, float *out, int64_t ldo,
                         int accumulate, unsigned *status, cudaStream_t s)
 {
+    using Shape = SimtShape<WG, Y_MAJOR, BM, BN, TM, TN, BK, STAGES>;
+    auto kernel = grouped_simt_kernel<WG, Y_MAJOR, BM, BN, TM, TN, BK, STAGES>;
+    static std::atomic<uint64_t> opted{0};          // devices whose shared-memory limit is raised
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
+    if (err != cudaSuccess) return err;
+    const uint64_t bit = dev >= 0 && dev < kCachedDevices ? 1ull << dev : 0ull;
+    if (bit == 0 || !(opted.load() & bit)) {
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Shape::SMEM);
+        if (err != cudaSuccess) return err;
+        opted.fetch_or(bit);
+    }
     const int64_t nt = (N + BN - 1) / BN;
     const int64_t mt = WG ? (int64_t)E * ((M + BM - 1) / BM) : rows / BM + (rows < E ? rows : E);
-    const int64_t units = mt * nt, most = (int64_t)device_sm_count() * 4;
-    return launch_pdl(grouped_simt_kernel<WG, Y_MAJOR, BM, BN, TM, TN>,
-                      dim3((unsigned)(units < most ? units : most)), dim3(BM / TM * (BN / TN)), 0, s,
-                      x, y, offsets, E, (int)rows, M, N, K, out, ldo, accumulate, status);
+    const int64_t units = mt * nt, most = (int64_t)device_sm_count() * 8;
+    return launch_pdl(kernel, dim3((unsigned)(units < most ? units : most)), dim3(Shape::THREADS),
+                      Shape::SMEM, s, x, y, offsets, E, (int)rows, M, N, K, out, ldo, accumulate, status);
 }
+
+// Tile by the extent of C's rows: the average number of an expert's rows, or
+// grad_w's N. Measured on 64 experts, N = K = 1024 (us; average rows 8, 32, 48,
+// 96, 256, 1024):
+//   16 x 128   86.7   206   248   450   1133   4396
+//   64 x 64     227   225   225   439    963   3464
+//   128 x 128   395   397   401   412    917   2952   ([E, K, N]: 425 .. 989 3175,
+//                                                      where 64 x 64 takes 917 3304)
+// so the tall tile is for k-contiguous weights only. Weight gradient, N = 16,
+// 32, 64: 17.7 22.2 33.1 flat, 22.8 22.8 23.7 square; tall 290 to 250 at 1024.
+constexpr int64_t kFlatTile = 40, kTallTile = 80;
 
 template <bool WG, bool Y_MAJOR>
 cudaError_t launch_sizes(const SimtOperand &x, const SimtOperand &y, const int32_t *offsets, int E,
                          int64_t rows, int M, int N, int K, float *out, int64_t ldo,
                          int accumulate, unsigned *status, cudaStream_t s)
 {
-    return launch_tile<WG, Y_MAJOR, 64, 64, 4, 4>(x, y, offsets, E, rows, M, N, K, out, ldo,
-                                                     accumulate, status, s);
+    const int64_t height = WG ? M : rows / E;
+    if (height < kFlatTile)
+        return launch_tile<WG, Y_MAJOR, 16, 128, 4, 4, 32, 4>(x, y, offsets, E, rows, M, N, K, out, ldo,
+                                                              accumulate, status, s);
+    if constexpr (!WG && !Y_MAJOR) {
+        if (height >= kTallTile && N >= 96)
+            return launch_tile<WG, Y_MAJOR, 128, 128, 8, 8, 16, 3>(x, y, offsets, E, rows, M, N, K, out,
+                                                                   ldo, accumulate, status, s);
+    }
+    return launch_tile<WG, Y_MAJOR, 64, 64, 4, 4, 16, 4>(x, y, offsets, E, rows, M, N, K, out, ldo,
+                                                         accumulate, status, s);
 }
 
 }  // namespace
