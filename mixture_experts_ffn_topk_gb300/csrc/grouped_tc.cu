@@ -23,6 +23,10 @@
 //              (512) consecutive bytes per row.
 // CTA pairs (CG = 2): M = 256, each CTA holds its 128 weight columns and half
 // of the unit's rows; the even CTA issues the MMAs for both.
+// Few units (a few rows, a narrow N): a cluster of 2, 4 or 8 single CTAs shares
+// each unit's k (SPLIT), every CTA with its own slice and accumulator; the FP32
+// partial sums meet through distributed shared memory, each CTA adding its
+// share of the rows in rank order, so the result does not depend on timing.
 // An expert's rows are cut into units of equal width, at most tok_cap; units
 // run over (expert, block of row units, weight tile, row unit), the row unit
 // fastest, so that CTAs at work share a weight tile in L2; a block's rows are
@@ -52,6 +56,8 @@ constexpr int TMEM_COLS = 2 * ACC_COLS;
 constexpr int THREADS = 352;
 constexpr int EPI_WARPS = 8;             // two groups of four: 2-5 and 7-10
 constexpr int STG_BYTES = 4096;          // one epilogue staging buffer
+constexpr int SPLIT_CAP = 64;            // rows of a split unit at most
+constexpr int PARTIAL_BYTES = SPLIT_CAP * BM * 4;
 constexpr uint64_t kDrainLimitNs = 100000000ull;
 // Bytes of rows a block of row units may cover, well inside the 129 MB L2
 // that also carries the streamed weights and the output.
@@ -81,6 +87,7 @@ struct GemmParams {
     int row_block;           // row units per block
     int slot_bytes;          // ring slot: W_BYTES + this CTA's rows of a full unit
     int stages;
+    int split;               // SPLIT: CTAs that share a unit's k
     uint8_t *out;
     int64_t out_row_bytes;
     int vec;                 // rows of out start on 16 bytes
@@ -182,7 +189,7 @@ __device__ __forceinline__ void tmem_ld_wait8(uint32_t (&r)[8])
                    "+r"(r[7]));
 }
 
-template <int DT, int CG, bool KN, bool OUT_F32>
+template <int DT, int CG, bool KN, bool OUT_F32, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
 grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_a,
                     const GemmParams p)
@@ -192,8 +199,13 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = CG == 2 ? (int)cluster_ctarank() : 0;
     const bool leader = rank == 0;
-    const int unit0 = (int)blockIdx.x / CG, unit_step = (int)gridDim.x / CG;
-    const int num_kb = (p.K + BK - 1) / BK;
+    static_assert(!SPLIT || CG == 1, "a split unit runs on single CTAs");
+    const int ways = SPLIT ? p.split : CG;           // CTAs per unit
+    const int unit0 = (int)blockIdx.x / ways, unit_step = (int)gridDim.x / ways;
+    // this CTA's k-blocks
+    const int all_kb = (p.K + BK - 1) / BK, slice = SPLIT ? (int)cluster_ctarank() : 0;
+    const int kb_begin = SPLIT ? all_kb * slice / ways : 0;
+    const int kb_end = SPLIT ? all_kb * (slice + 1) / ways : all_kb;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) { mbar_init(&S.full[s], 1); mbar_init(&S.empty[s], 1); }
@@ -235,7 +247,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             // barrier, which expects them all; they may land before it is
             // armed (the phase cannot complete while the arrival is pending)
             const uint32_t bytes = CG * (W_BYTES + u.mma_n / CG * BK * 2);
-            for (int kb = 0; kb < num_kb; ++kb) {
+            for (int kb = kb_begin; kb < kb_end; ++kb) {
                 ok = warp_wait<CG>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns);
                 if (!ok) break;
                 const uint32_t sw = ring + stage * p.slot_bytes, here = smem_u32(&S.full[stage]);
@@ -261,7 +273,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             const Unit u = walk.at(unit);
             const int mine = u.mma_n / CG;               // rows this CTA loads
             const int row0 = u.row0 + rank * mine;
-            for (int kb = 0; kb < num_kb; ++kb) {
+            for (int kb = kb_begin; kb < kb_end; ++kb) {
                 ok = warp_wait<CG>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns);
                 if (!ok) break;
                 const uint32_t sa = ring + stage * p.slot_bytes + W_BYTES, here = smem_u32(&S.full[stage]);
@@ -294,7 +306,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             ok = warp_wait<CG>(&S.acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_ns);
             if (!ok) break;
             const uint32_t d = tmem_base + (uint32_t)(acc * ACC_COLS);
-            for (int kb = 0; kb < num_kb; ++kb) {
+            for (int kb = kb_begin; kb < kb_end; ++kb) {
                 ok = warp_wait<CG>(&S.full[stage], phase, abort_flag, p.status, p.wait_ns);
                 if (!ok) break;
                 tc_fence_after();
@@ -302,7 +314,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
 #pragma unroll
                 for (int k = 0; k < BK / UK; ++k)
                     umma_on<CG>(on, d, KN ? sdesc_mn_sw128(w + k * UK * 128, W_BYTES / 2) : sdesc_k_sw128(w + k * UK * 2),
-                                sdesc_k_sw128(a + k * UK * 2), idesc, (kb | k) != 0 ? 1u : 0u);
+                                sdesc_k_sw128(a + k * UK * 2), idesc, (kb - kb_begin) | k ? 1u : 0u);
                 commit_on<CG>(on, &S.empty[stage]);
                 if (++stage == p.stages) { stage = 0; phase ^= 1u; }
             }
@@ -337,7 +349,18 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             const int piece = tid % PIECES, col = u.w0 + piece * (16 / ESZ);
             uint8_t *out0 = p.out + (int64_t)u.row0 * p.out_row_bytes + (int64_t)col * ESZ;
             const bool whole = p.vec && col + 16 / ESZ <= p.N;
-            for (int t0 = group * CH; t0 < u.rows; t0 += 2 * CH, buf ^= 1) {
+            if constexpr (SPLIT) {
+                // the partial sums stay here, [row][n] in FP32
+                float *mine = reinterpret_cast<float *>(S.ring + RING_BYTES - PARTIAL_BYTES) + q * 32 + lane;
+                for (int t0 = group * 16; t0 < u.rows; t0 += 32) {
+                    uint32_t v[16];
+                    tmem_ld16(tbase + t0, v);
+                    tmem_ld_wait16(v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) mine[(t0 + i) * BM] = __uint_as_float(v[i]);
+                }
+            }
+            for (int t0 = group * CH; !SPLIT && t0 < u.rows; t0 += 2 * CH, buf ^= 1) {
                 uint8_t *stg = S.stg[group][buf], *mine = stg + (q * 32 + lane) * ESZ;
                 if constexpr (OUT_F32) {
                     uint32_t v[8];
@@ -387,6 +410,31 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         }
     }
 
+    if constexpr (SPLIT) {
+        // every CTA's partial sums are written; each adds its rows
+        __syncwarp();
+        cluster_sync();
+        if (unit0 < total) {
+            const Unit u = UnitWalk<CG>(S.seg, p, rank).at(unit0);
+            const uint32_t partial = smem_u32(S.ring + RING_BYTES - PARTIAL_BYTES);
+            for (int i = threadIdx.x; ; i += THREADS) {
+                const int t = i / BM * ways + slice, n = i % BM;
+                if (t >= u.rows) break;
+                float sum = 0.0f;
+                for (int r = 0; r < ways; ++r) {
+                    float v;
+                    asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                 : "=f"(v) : "r"(mapa_shared(partial + (t * BM + n) * 4, r)) : "memory");
+                    sum += v;
+                }
+                if (u.w0 + n >= p.N) continue;
+                uint8_t *dst = p.out + (int64_t)(u.row0 + t) * p.out_row_bytes;
+                if constexpr (OUT_F32) reinterpret_cast<float *>(dst)[u.w0 + n] = sum;
+                else reinterpret_cast<typename Elem<DT>::T *>(dst)[u.w0 + n] = Elem<DT>::from_f(sum);
+            }
+        }
+        cluster_sync();             // nobody leaves while its sums are read
+    }
     // ------------------------------------------------------------ teardown
     __syncthreads();
     if (*abort_flag) let_copies_land();
@@ -441,16 +489,18 @@ cudaError_t prepare_kernel(Kernel kernel, int cg, std::atomic<int> *cache, int *
     return cudaSuccess;
 }
 
-template <int DT, int CG, bool KN, bool OUT_F32>
+template <int DT, int CG, bool KN, bool OUT_F32, bool SPLIT>
 cudaError_t launch_kernel(int64_t units, const CUtensorMap &mw, const RowMaps &ma, const GemmParams &p,
                           cudaStream_t s)
 {
     static std::atomic<int> cache[kCachedDevices];
+    auto kernel = grouped_gemm_kernel<DT, CG, KN, OUT_F32, SPLIT>;
     int ctas = 0;
-    cudaError_t err = prepare_kernel(grouped_gemm_kernel<DT, CG, KN, OUT_F32>, CG, cache, &ctas);
+    cudaError_t err = prepare_kernel(kernel, CG, cache, &ctas);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(CG * units < ctas ? CG * units : ctas));
+    const int ways = SPLIT ? p.split : CG;
+    cfg.gridDim = dim3((unsigned)(SPLIT || ways * units < ctas ? ways * units : ctas));
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = s;
@@ -458,18 +508,18 @@ cudaError_t launch_kernel(int64_t units, const CUtensorMap &mw, const RowMaps &m
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = CG;
+    attr[1].val.clusterDim.x = (unsigned)ways;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = CG == 2 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, grouped_gemm_kernel<DT, CG, KN, OUT_F32>, mw, ma, p);
+    cfg.numAttrs = ways > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, mw, ma, p);
 }
 
-template <int DT, int CG>
+template <int DT, int CG, bool SPLIT>
 cudaError_t launch_cg(const void *a, int64_t lda, const int32_t *offsets, int64_t rows, const void *w,
                       int E, int64_t N, int64_t K, bool kn, void *out, int64_t ldo, bool out_f32,
-                      int tok_cap, unsigned *status, cudaStream_t s)
+                      int tok_cap, int split, unsigned *status, cudaStream_t s)
 {
     const CUtensorMapDataType tdt =
         DT == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
@@ -491,19 +541,22 @@ cudaError_t launch_cg(const void *a, int64_t lda, const int32_t *offsets, int64_
     const int64_t block = kRowBlockBytes / (tok_cap * K * 2), most = (rows + tok_cap - 1) / tok_cap;
     p.row_block = (int)(block < 1 ? 1 : block > most ? most : block);
     p.slot_bytes = W_BYTES + tok_cap / CG * BK * 2;
-    p.stages = RING_BYTES / p.slot_bytes < MAX_STAGES ? RING_BYTES / p.slot_bytes : MAX_STAGES;
+    const int slots = (RING_BYTES - (SPLIT ? PARTIAL_BYTES : 0)) / p.slot_bytes;
+    p.stages = slots < MAX_STAGES ? slots : MAX_STAGES;
+    p.split = split;
     p.out = static_cast<uint8_t *>(out);
     p.out_row_bytes = ldo * (out_f32 ? 4 : 2);
     p.vec = p.out_row_bytes % 16 == 0;
     p.status = status;
-    p.wait_ns = wait_limit_ns();
+    // a wait may last one unit's whole reduction: a microsecond per stage on top
+    p.wait_ns = wait_limit_ns() + 1000ull * (uint64_t)((K + BK - 1) / BK);
     // an upper bound: every expert adds at most one unit that is not full
     const int64_t units = (rows / tok_cap + (rows < E ? rows : E)) * p.w_tiles;
     if (out_f32)
-        return kn ? launch_kernel<DT, CG, true, true>(units, mw, ma, p, s)
-                  : launch_kernel<DT, CG, false, true>(units, mw, ma, p, s);
-    return kn ? launch_kernel<DT, CG, true, false>(units, mw, ma, p, s)
-              : launch_kernel<DT, CG, false, false>(units, mw, ma, p, s);
+        return kn ? launch_kernel<DT, CG, true, true, SPLIT>(units, mw, ma, p, s)
+                  : launch_kernel<DT, CG, false, true, SPLIT>(units, mw, ma, p, s);
+    return kn ? launch_kernel<DT, CG, true, false, SPLIT>(units, mw, ma, p, s)
+              : launch_kernel<DT, CG, false, false, SPLIT>(units, mw, ma, p, s);
 }
 
 template <int DT>
@@ -511,9 +564,23 @@ cudaError_t launch_dt(const void *a, int64_t lda, const int32_t *offsets, int64_
                       int E, int64_t N, int64_t K, bool kn, void *out, int64_t ldo, bool out_f32,
                       unsigned *status, cudaStream_t s)
 {
+    // Few units (of the single form's 64 rows by 128 columns): split k over as
+    // many CTAs, 2 to 8, as the GPU has room for and as leave each four k-blocks.
+    const int64_t units = (rows / SPLIT_CAP + (rows < E ? rows : E)) * ((N + BM - 1) / BM);
+    const int64_t num_kb = (K + BK - 1) / BK, sms = device_sm_count();
+    int split = 1;
+    while (split < 8 && units * split * 2 <= sms && num_kb >= split * 2 * 4) split *= 2;
+    if (split > 1)
+        return launch_cg<DT, 1, true>(a, lda, offsets, rows, w, E, N, K, kn, out, ldo, out_f32, SPLIT_CAP,
+                                      split, status, s);
+    // Pairs or single CTAs, by the average rows of an expert. 64 experts, N = K =
+    // 2048 (16 experts, N = K = 4096), us at 4, 32, 48, 64, 96 rows on average:
+    // singles 82.7 87.0 89.4 93.7 113 (87.1 89.9 91.5 101 106),
+    // pairs   87.9 92.9 93.5 95.2 98.1 (91.9 95.2 95.1 97.0 98.6).
     if (rows >= 64 * (int64_t)E)
-        return launch_cg<DT, 2>(a, lda, offsets, rows, w, E, N, K, kn, out, ldo, out_f32, 256, status, s);
-    return launch_cg<DT, 1>(a, lda, offsets, rows, w, E, N, K, kn, out, ldo, out_f32, 64, status, s);
+        return launch_cg<DT, 2, false>(a, lda, offsets, rows, w, E, N, K, kn, out, ldo, out_f32, 256, 1,
+                                       status, s);
+    return launch_cg<DT, 1, false>(a, lda, offsets, rows, w, E, N, K, kn, out, ldo, out_f32, 64, 1, status, s);
 }
 
 }  // namespace

@@ -519,7 +519,12 @@ cudaError_t launch_dt(const void *grad, int64_t ldg, const void *a, int64_t lda,
     p.out_row_bytes = K * (out_f32 ? 4 : 2);
     p.accumulate = accumulate;
     p.status = status;
-    p.wait_ns = wait_limit_ns();
+    // a wait may last one unit's whole reduction: a microsecond per stage on top
+    p.wait_ns = wait_limit_ns() + 1000ull * (uint64_t)((rows + BK - 1) / BK);
+    // Pairs or single CTAs, by the average rows of an expert: us at 256, 384, 512,
+    // 768, 1024, 4096 rows, 64 experts of 2048 x 1408 (16 of 4096 x 4096):
+    // singles 109 144 170 219 273 948 (153 205 236 307 376 1233),
+    // pairs   130 153 176 218 260 868 (177 205 232 284 343 1149).
     if (rows >= 512 * (int64_t)E)
         return out_f32 ? launch_kernel<DT, 2, true>(mg, ma, mo, p, s) : launch_kernel<DT, 2, false>(mg, ma, mo, p, s);
     return out_f32 ? launch_kernel<DT, 1, true>(mg, ma, mo, p, s) : launch_kernel<DT, 1, false>(mg, ma, mo, p, s);

@@ -132,6 +132,45 @@ def test_product(dtype, counts, N, K, transposed):
             check(out[s], ref[s], size[s] * (K + 1) * 2.0 ** -23, out_dtype, f"{out_dtype} pad {pad}")
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("counts", [[1], [0, 3, 0], [64], [65], [16, 1, 0, 40], [130]])
+@pytest.mark.parametrize("N,K,transposed", [(8, 520, False), (8, 4104, True), (130, 2048, False),
+                                            (250, 4096, False), (256, 1032, True), (1000, 1024, False),
+                                            (1, 7168, False), (1032, 2056, True)])
+def test_product_of_few_rows_over_a_long_k(dtype, counts, N, K, transposed):
+    """Few units of work: their k is shared by 2, 4 or 8 CTAs whose sums are joined."""
+    g = gen(N + K)
+    first, rows, E = 2, sum(counts) + 5, len(counts)
+    off = offsets_of(counts, first)
+    a = strided(rows, K, dtype, g, 8)
+    a[:first], a[first + sum(counts):] = float("nan"), float("inf")
+    w = torch.randn((E, K, N) if transposed else (E, N, K), generator=g, device="cuda").to(dtype)
+    ref, size = ref_product(a, off, w, transposed)
+    s = slice(first, first + sum(counts))
+    for out_dtype in {dtype, F32}:
+        whole = torch.full((rows, N + 3), -7.0, dtype=out_dtype, device="cuda")
+        out = moe.moe_grouped_gemm(a, off, w, transposed=transposed, out=whole[:, :N])
+        assert torch.all(whole[:first] == -7) and torch.all(whole[s.stop:] == -7) and torch.all(whole[:, N:] == -7)
+        check(out[s], ref[s], size[s] * (K + 1) * 2.0 ** -23, out_dtype, f"{out_dtype}")
+        again = moe.moe_grouped_gemm(a, off, w, transposed=transposed, out_dtype=out_dtype)
+        assert torch.equal(again[s], out[s])
+
+
+def test_product_of_few_rows_with_bad_offsets():
+    """The joined form also serves what is sound and touches nothing else."""
+    g = gen(30)
+    a = torch.randn((20, 2048), generator=g, device="cuda").to(BF16)
+    w = torch.randn((3, 64, 2048), generator=g, device="cuda").to(BF16)
+    out = torch.full((20, 64), -7.0, dtype=BF16, device="cuda")
+    moe.moe_device_status(clear=True)
+    moe.moe_grouped_gemm(a, torch.tensor([0, 5, 30, 20], dtype=torch.int32, device="cuda"), w, out=out)
+    assert moe.moe_device_status(clear=True) == BAD_INDEX
+    ref = a[:5].double() @ w[0].double().T
+    size = a[:5].double().abs() @ w[0].double().abs().T
+    check(out[:5], ref, size * 2049 * 2.0 ** -23, BF16, "the sound expert")
+    assert torch.all(out[5:] == -7)
+
+
 def test_product_many_experts():
     """1024 experts, most of them idle, and the last one busy."""
     g = gen(5)
