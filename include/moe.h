@@ -655,8 +655,8 @@ int moe_experts_backward(const void *x_disp, const int32_t *offsets, int64_t row
  *
  * Common to these calls: a matrix of dispatched rows has unit column stride
  * and its rows lie `ld` elements apart (ld >= its columns; a half of a
- * stacked [rows, 2I] matrix is one). No output may overlap an input. No call
- * needs a workspace, and every result is bit-reproducible.
+ * stacked [rows, 2I] matrix is one). No output may overlap an input or another
+ * output. No call needs a workspace, and every result is bit-reproducible.
  * `offsets` [E + 1] int32 (device) is that of moe_dispatch: expert e has the
  * rows [offsets[e], offsets[e + 1]). An expert whose offsets fall, are
  * negative or pass `rows` is taken as one without rows and the status word
@@ -682,9 +682,10 @@ typedef enum moe_weight_layout {
  *        for the rows of every expert: out[r, n] = sum_k a[r, k] w[e][n, k]
  *        (or w[e][k, n]), accumulated in FP32, rounded once.
  *   BF16 / F16 run on tcgen05 tensor cores, F32 in true FP32 on CUDA cores.
- *   rows >= 0, 1 <= E <= 1024, N and K >= 1. K, lda and, with MOE_WEIGHT_KN,
- *   N take whole multiples of 16 bytes (8 elements of BF16 / F16, 4 of F32);
- *   other N, and any ldo >= N, are fine.
+ *   0 <= rows <= 2^31 - 1024, 1 <= E <= 1024, 1 <= N, K <= 2^24, strides up to
+ *   2^32 elements. K, lda and, with MOE_WEIGHT_KN, N take whole multiples of
+ *   16 bytes (8 elements of BF16 / F16, 4 of F32); other N, and any ldo >= N,
+ *   are fine.
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_VALUE (layout),
  * MOE_ERR_ALIGN, MOE_ERR_CUDA.
  */
@@ -733,7 +734,7 @@ int moe_grouped_gemm_weight_grad(const void *grad, int64_t ldg, const void *a, i
  *   offsets  NULL (every row), or [E + 1] int32: rows from offsets[E] on are
  *         left alone, in h and in ckpt (E is unused without offsets).
  *   2.06 bytes per value instead of moe_experts_forward_training's 8.
- *   rows >= 0, I >= 1. g, u and h need only their elements' alignment; rows
+ *   rows and I bounded as rows and N above. g, u and h need only their elements' alignment; rows
  *   that all start on 16 bytes are read and written in vectors.
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_ALIGN,
  * MOE_ERR_WORKSPACE (ckpt too small or not aligned), MOE_ERR_CUDA.
@@ -800,7 +801,8 @@ int moe_device_status(void *stream, int clear);
  * gives up (the error convention of the ruDNN user guide, section 3: a
  * MoeError instead of a hang). Every spin-wait inside the tcgen05 expert
  * GEMMs (pipeline barriers, and the per-expert readiness counters of the
- * one-call forward) stops after this many nanoseconds, records
+ * one-call forward) stops after this many nanoseconds (in the grouped
+ * products, plus a microsecond per 64 elements of the reduction), records
  * MOE_ERR_DEVICE_TIMEOUT in the status word, drains its own copies and MMAs
  * and lets the kernel exit. Process-wide; read when a kernel is launched
  * (a captured graph keeps the value of its capture). 0 restores the

@@ -21,9 +21,9 @@ struct Segments {
 // Fills the table: the first THREADS threads of the CTA take part, all of
 // them call; a __syncthreads() by the caller publishes it. units_of(rows)
 // gives an expert's number of units. An expert whose offsets fall, are
-// negative or pass `rows` gets no rows, and the status word records
-// ST_BAD_INDEX: whatever the offsets hold, every row that a unit names lies
-// in [0, rows).
+// negative or pass `rows`, or whose rows an earlier one has, gets no rows, and
+// the status word records ST_BAD_INDEX: whatever the offsets hold, every row
+// that a unit names lies in [0, rows), and no row belongs to two experts.
 template <int THREADS, typename UnitsOf>
 __device__ __forceinline__ void load_segments(Segments &S, int *warp_sum,
                                               const int32_t *__restrict__ offsets, int E,
@@ -38,7 +38,20 @@ __device__ __forceinline__ void load_segments(Segments &S, int *warp_sum,
         S.first[e] = ok ? a : 0;
         S.count[e] = ok ? b - a : 0;
     }
-    if (__syncthreads_or(bad) && threadIdx.x == 0 && blockIdx.x == 0) atomicOr(status, ST_BAD_INDEX);
+    if (__syncthreads_or(bad)) {
+        // offsets that fall somewhere may also name rows twice: the later
+        // expert yields, so that there are never more units than the launch
+        // was sized for and no two experts write one row
+        if (threadIdx.x == 0) {
+            if (blockIdx.x == 0) atomicOr(status, ST_BAD_INDEX);
+            int end = 0;
+            for (int e = 0; e < E; ++e) {
+                if (S.first[e] < end) S.count[e] = 0;
+                if (S.count[e] > 0) end = S.first[e] + S.count[e];
+            }
+        }
+        __syncthreads();
+    }
     // exclusive prefix over the experts' units: a run of experts per thread,
     // then the warps' totals
     const int per = (E + THREADS - 1) / THREADS, e0 = threadIdx.x * per;

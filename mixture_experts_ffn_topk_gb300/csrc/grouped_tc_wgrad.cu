@@ -22,6 +22,10 @@
 //   warp 6     zeroes foreign rows of a segment's last stage.
 // CTA pairs (CG = 2): M = 256, each CTA holds 128 columns of grad and half of
 // a's; the even CTA issues the MMAs.
+// Few units (narrow matrices) and long segments: a cluster of 2, 4 or 8 single
+// CTAs shares each unit's rows (SPLIT); the FP32 partial sums meet through
+// distributed shared memory, in the ring's place, each CTA adding its share of
+// the columns in rank order.
 // Units run over (expert, tile of the wider matrix, tile of the narrower one),
 // the last fastest: the narrower operand's segment stays in L2 while the wider
 // one passes once.
@@ -81,7 +85,8 @@ struct WgradParams {
     int E, rows, N, K;
     int n_tiles, k_tiles;
     int n_fast;              // the n tile runs fastest (grad is the narrower operand)
-    const uint8_t *out;      // read where the gradient is added to
+    int split;               // SPLIT: CTAs that share a unit's rows
+    uint8_t *out;            // read where the gradient is added to, written where split
     int64_t out_row_bytes;
     int accumulate;
     unsigned *status;
@@ -89,7 +94,8 @@ struct WgradParams {
 };
 
 struct Unit {
-    int e, row0, cnt;        // expert, its first row and number of rows
+    int e, row0, cnt;        // expert, first row and number of rows (of this CTA's slice)
+    bool idle;               // the expert has no rows
     int nkb;                 // stages: blocks of 64 rows
     int tail;                // rows of the last block that are the expert's
     int n0;                  // this CTA's first row of grad_w
@@ -98,7 +104,7 @@ struct Unit {
 
 // Walks a CTA's units, first and then every step-th, as (expert, outer tile,
 // inner tile) without dividing between units.
-template <int CG>
+template <int CG, bool SPLIT>
 struct UnitWalk {
     const Segments &S;
     const WgradParams &p;
@@ -128,6 +134,14 @@ struct UnitWalk {
         u.e = e;
         u.row0 = S.first[e];
         u.cnt = S.count[e];
+        u.idle = u.cnt == 0;
+        if constexpr (SPLIT) {
+            const int all = (u.cnt + BK - 1) / BK, slice = (int)cluster_ctarank();
+            const int from = (int)((int64_t)all * slice / p.split) * BK;
+            const int64_t to = (int64_t)all * (slice + 1) / p.split * BK;
+            u.row0 += from;
+            u.cnt = (to < u.cnt ? (int)to : u.cnt) - from;
+        }
         u.nkb = (u.cnt + BK - 1) / BK;
         u.tail = u.cnt - (u.nkb - 1) * BK;
         u.n0 = (nt * CG + rank) * BM;
@@ -144,7 +158,7 @@ struct UnitWalk {
     }
 };
 
-template <int DT, int CG, bool OUT_F32>
+template <int DT, int CG, bool OUT_F32, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
 grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_a,
                      const __grid_constant__ CUtensorMap map_out, const WgradParams p)
@@ -155,7 +169,9 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = CG == 2 ? (int)cluster_ctarank() : 0;
     const bool leader = rank == 0;
-    const int unit0 = (int)blockIdx.x / CG, unit_step = (int)gridDim.x / CG;
+    static_assert(!SPLIT || CG == 1, "a split unit runs on single CTAs");
+    const int ways = SPLIT ? p.split : CG;           // CTAs per unit
+    const int unit0 = (int)blockIdx.x / ways, unit_step = (int)gridDim.x / ways;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < NS; ++s) {
@@ -187,7 +203,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
     const uint32_t tmem_base = S.tmem_base;
     const int total = p.E * p.n_tiles * p.k_tiles;
     volatile int *abort_flag = &S.abort;
-    UnitWalk<CG> walk(S.seg, p, rank, unit0, unit_step);
+    UnitWalk<CG, SPLIT> walk(S.seg, p, rank, unit0, unit_step);
 
     // A producer's loop: loads(dst, bar, u, row) issues its copies of one
     // stage; with ARM it also expects both producers' bytes.
@@ -341,6 +357,18 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
             const int row0 = u.n0 + q * 32;            // this warp's first row of grad_w[e]
             const bool empty = u.cnt == 0;
             int width = p.K - u.k0 < BN ? p.K - u.k0 : BN;
+            if constexpr (SPLIT) {
+                // the partial sums stay here, [column][row] in FP32
+                float *mine = reinterpret_cast<float *>(S.ring[0]) + q * 32 + lane;
+                for (int c0 = 0; c0 < width; c0 += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(tbase + c0, v);
+                    tmem_ld_wait(v);
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) mine[(c0 + i) * BM] = empty ? 0.0f : __uint_as_float(v[i]);
+                }
+                width = 0;
+            }
             if (row0 >= p.N || (empty && p.accumulate)) width = 0;
             for (int c0 = 0; c0 < width; c0 += 32) {
                 uint32_t v[32];
@@ -416,6 +444,57 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
         __syncwarp();
     }
 
+    if constexpr (SPLIT) {
+        static_assert(BN * BM * 4 <= sizeof(S.ring), "the partial sums take the ring's place");
+        // every CTA's partial sums are written; each adds its columns, eight
+        // of a row at a time
+        __syncwarp();
+        cluster_sync();
+        if (unit0 < total) {
+            const int slice = (int)cluster_ctarank();
+            const Unit u = UnitWalk<CG, SPLIT>(S.seg, p, rank, unit0, unit_step).next();
+            const int width = p.K - u.k0 < BN ? p.K - u.k0 : BN;
+            const uint32_t partial = smem_u32(S.ring[0]);
+            for (int i = threadIdx.x; !(u.idle && p.accumulate); i += THREADS) {
+                const int c = (i / BM * ways + slice) * 8, n = i % BM;
+                if (c >= width) break;
+                if (u.n0 + n >= p.N) continue;
+                float sum[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                for (int r = 0; r < ways; ++r) {
+                    const uint32_t from = mapa_shared(partial + (c * BM + n) * 4, r);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        float v;
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(from + j * BM * 4) : "memory");
+                        sum[j] += v;
+                    }
+                }
+                uint4 *dst = reinterpret_cast<uint4 *>(p.out + ((int64_t)u.e * p.N + u.n0 + n) * p.out_row_bytes +
+                                                       (int64_t)(u.k0 + c) * (OUT_F32 ? 4 : 2));
+#pragma unroll
+                for (int h = 0; h < (OUT_F32 ? 2 : 1); ++h) {
+                    Vec16 o;
+                    o.u = p.accumulate ? dst[h] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if constexpr (OUT_F32) {
+                            o.f[j] = p.accumulate ? sum[h * 4 + j] + o.f[j] : sum[h * 4 + j];
+                        } else {
+                            float2 f = make_float2(sum[2 * j], sum[2 * j + 1]);
+                            if (p.accumulate) {
+                                const float2 old = DT == DT_BF16 ? bf16x2_to_float2(o.w[j]) : f16x2_to_float2(o.w[j]);
+                                f.x += old.x;
+                                f.y += old.y;
+                            }
+                            o.w[j] = pack2<DT>(f.x, f.y);
+                        }
+                    }
+                    dst[h] = o.u;
+                }
+            }
+        }
+        cluster_sync();             // nobody leaves while its sums are read
+    }
     // ------------------------------------------------------------ teardown
     __syncthreads();
     if (*abort_flag) let_copies_land();
@@ -447,14 +526,15 @@ bool encode_out(CUtensorMap *m, CUtensorMapDataType dt, void *base, uint64_t K, 
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int DT, int CG, bool OUT_F32>
+template <int DT, int CG, bool OUT_F32, bool SPLIT>
 cudaError_t launch_kernel(const CUtensorMap &mg, const CUtensorMap &ma, const CUtensorMap &mo, WgradParams p,
                           cudaStream_t s)
 {
     // CTAs the GPU holds at once, per device; 0: the kernel is not yet opted
     // in to its shared memory there
     static std::atomic<int> cache[kCachedDevices];
-    auto kernel = grouped_wgrad_kernel<DT, CG, OUT_F32>;
+    auto kernel = grouped_wgrad_kernel<DT, CG, OUT_F32, SPLIT>;
+    const int ways = SPLIT ? p.split : CG;
     p.n_tiles = (p.N + BM * CG - 1) / (BM * CG);
     p.k_tiles = (p.K + BN - 1) / BN;
     p.n_fast = p.N <= p.K;
@@ -464,7 +544,7 @@ cudaError_t launch_kernel(const CUtensorMap &mg, const CUtensorMap &ma, const CU
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.x = (unsigned)ways;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -491,7 +571,7 @@ cudaError_t launch_kernel(const CUtensorMap &mg, const CUtensorMap &ma, const CU
         if (cached) cache[dev].store(ctas);
     }
     const int64_t units = (int64_t)p.E * p.n_tiles * p.k_tiles;
-    cfg.gridDim = dim3((unsigned)(CG * units < ctas ? CG * units : ctas));
+    cfg.gridDim = dim3((unsigned)(SPLIT || ways * units < ctas ? ways * units : ctas));
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, mg, ma, mo, p);
 }
@@ -515,19 +595,30 @@ cudaError_t launch_dt(const void *grad, int64_t ldg, const void *a, int64_t lda,
     p.rows = (int)rows;
     p.N = (int)N;
     p.K = (int)K;
-    p.out = static_cast<const uint8_t *>(grad_w);
+    p.out = static_cast<uint8_t *>(grad_w);
     p.out_row_bytes = K * (out_f32 ? 4 : 2);
     p.accumulate = accumulate;
     p.status = status;
     // a wait may last one unit's whole reduction: a microsecond per stage on top
     p.wait_ns = wait_limit_ns() + 1000ull * (uint64_t)((rows + BK - 1) / BK);
+    // Few units: split an expert's rows over as many CTAs, 2 to 8, as the GPU has
+    // room for and as leave each four blocks of rows on average.
+    const int64_t units = (int64_t)E * ((N + BM - 1) / BM) * ((K + BN - 1) / BN);
+    const int64_t blocks = rows / E / BK, sms = device_sm_count();
+    p.split = 1;
+    while (p.split < 8 && units * p.split * 2 <= sms && blocks >= p.split * 2 * 4) p.split *= 2;
+    if (p.split > 1)
+        return out_f32 ? launch_kernel<DT, 1, true, true>(mg, ma, mo, p, s)
+                       : launch_kernel<DT, 1, false, true>(mg, ma, mo, p, s);
     // Pairs or single CTAs, by the average rows of an expert: us at 256, 384, 512,
     // 768, 1024, 4096 rows, 64 experts of 2048 x 1408 (16 of 4096 x 4096):
     // singles 109 144 170 219 273 948 (153 205 236 307 376 1233),
     // pairs   130 153 176 218 260 868 (177 205 232 284 343 1149).
     if (rows >= 512 * (int64_t)E)
-        return out_f32 ? launch_kernel<DT, 2, true>(mg, ma, mo, p, s) : launch_kernel<DT, 2, false>(mg, ma, mo, p, s);
-    return out_f32 ? launch_kernel<DT, 1, true>(mg, ma, mo, p, s) : launch_kernel<DT, 1, false>(mg, ma, mo, p, s);
+        return out_f32 ? launch_kernel<DT, 2, true, false>(mg, ma, mo, p, s)
+                       : launch_kernel<DT, 2, false, false>(mg, ma, mo, p, s);
+    return out_f32 ? launch_kernel<DT, 1, true, false>(mg, ma, mo, p, s)
+                   : launch_kernel<DT, 1, false, false>(mg, ma, mo, p, s);
 }
 
 }  // namespace

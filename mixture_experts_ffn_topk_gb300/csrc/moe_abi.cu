@@ -89,6 +89,7 @@ size_t round_up(size_t v, size_t a) { return (v + a - 1) / a * a; }
 constexpr int64_t kMaxE = 1024;
 constexpr uint64_t kMaxWaitLimitNs = 60ull * 1000000000ull;   // moe_set_wait_limit_ns bound
 constexpr int64_t kMaxRows = 0x7fffffff;   // dispatched rows are int32
+constexpr int64_t kMaxGroupedRows = 0x7fffffff - 1023;   // rows round up to a unit in int32
 constexpr int64_t kMaxGroupedDim = 1 << 24;      // N, K, I of the grouped products and checkpoints
 constexpr int64_t kMaxStride = int64_t(1) << 32; // their row strides (a TMA stride is below 2^40 bytes)
 
@@ -958,8 +959,8 @@ static int check_grouped_args(int64_t rows, int64_t E, int64_t N, int64_t K, int
     if (!valid_dtype(dt)) return fail(MOE_ERR_DTYPE, "dtype must be F32, BF16 or F16");
     if (odt != dt && odt != MOE_F32)
         return fail(MOE_ERR_DTYPE, "the output dtype must be the operands' or F32");
-    if (rows < 0 || rows > kMaxRows || E < 1 || E > kMaxE)
-        return fail(MOE_ERR_SHAPE, "need 0 <= rows < 2^31 and 1 <= E <= 1024");
+    if (rows < 0 || rows > kMaxGroupedRows || E < 1 || E > kMaxE)
+        return fail(MOE_ERR_SHAPE, "need 0 <= rows <= 2^31 - 1024 and 1 <= E <= 1024");
     if (N < 1 || K < 1 || N > kMaxGroupedDim || K > kMaxGroupedDim)
         return fail(MOE_ERR_SHAPE, "need 1 <= N, K <= 2^24");
     return MOE_OK;
@@ -1042,8 +1043,8 @@ int moe_grouped_gemm_weight_grad(const void *grad, int64_t ldg, const void *a, i
 
 static int check_checkpoint_sizes(int64_t rows, int64_t I)
 {
-    if (rows < 0 || rows > kMaxRows || I < 1 || I > kMaxGroupedDim)
-        return fail(MOE_ERR_SHAPE, "need 0 <= rows < 2^31 and 1 <= I <= 2^24");
+    if (rows < 0 || rows > kMaxGroupedRows || I < 1 || I > kMaxGroupedDim)
+        return fail(MOE_ERR_SHAPE, "need 0 <= rows <= 2^31 - 1024 and 1 <= I <= 2^24");
     return MOE_OK;
 }
 
@@ -1075,7 +1076,7 @@ static int check_checkpoint_ptrs(const char *name, int dt, const int32_t *offset
 
 size_t moe_swiglu_checkpoint_size(int64_t rows, int64_t I)
 {
-    if (rows < 0 || rows > kMaxRows || I < 1 || I > kMaxGroupedDim) return 0;
+    if (rows < 0 || rows > kMaxGroupedRows || I < 1 || I > kMaxGroupedDim) return 0;
     return swiglu_checkpoint_planes(rows, I).total;
 }
 

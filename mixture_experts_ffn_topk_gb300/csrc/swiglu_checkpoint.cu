@@ -18,7 +18,9 @@
 // per value, the backward reads 4.06 and writes 6. Four lanes share a block, 8
 // columns each (16-byte loads of 16-bit rows, 8-byte stores of codes, two
 // shuffles for the block's maximum), so a warp touches whole 32-byte sectors
-// of every plane and no shared memory is needed.
+// of every plane and no shared memory is needed. A thread keeps two blocks in
+// flight. At 32768 x 14336 in BF16 the forward takes 0.64 ms (89 % of the
+// measured copy bandwidth), the backward 0.74 ms (95 %).
 #include <cuda_fp8.h>
 
 #include "common.cuh"
@@ -332,7 +334,9 @@ swiglu_checkpoint_backward_kernel(const void *__restrict__ grad_h, int64_t ld_by
     }
 }
 
-// Enough CTAs to fill every SM with 2048 threads, no more than there are items.
+// At least 8 CTAs per SM (the whole work, if less), more where each thread
+// would walk over 16 blocks: on 32768 x 14336 values 8, 16 and 64 per SM took
+// 645, 637 and 634 us (backward 769, 760, 743), on 24576 x 1408 53, 57, 60.
 Walk make_walk(int64_t rows, int64_t I, const int32_t *end, unsigned *grid)
 {
     Walk w;
@@ -340,9 +344,11 @@ Walk make_walk(int64_t rows, int64_t I, const int32_t *end, unsigned *grid)
     w.S = (int)((I + kBlock - 1) / kBlock);
     w.end = end;
     const int64_t per = kThreads / 4, items = rows * w.S;
-    const int64_t want = (items + per - 1) / per, most = (int64_t)device_sm_count() * 8;
-    *grid = (unsigned)(want < most ? want : most);
-    const int64_t step = (int64_t)*grid * per;
+    const int64_t want = (items + per - 1) / per, fill = (int64_t)device_sm_count() * 8;
+    int64_t n = want / 16 > fill ? want / 16 : want < fill ? want : fill;
+    if (n > 0x7fffffff) n = 0x7fffffff;
+    *grid = (unsigned)n;
+    const int64_t step = n * per;
     w.step_row = step / w.S;
     w.step_blk = (int)(step % w.S);
     return w;

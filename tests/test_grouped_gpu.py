@@ -267,6 +267,59 @@ def test_bad_offsets(bad):
                 assert torch.all(gw[e] == 0)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("E,rows,K", [(64, 60, 2048), (1000, 100, 64), (6, 700, 128)])
+def test_bad_offsets_that_name_rows_again_and_again(dtype, E, rows, K):
+    """0, rows, 0, rows, ...: only the first expert has rows; the others neither write them a second
+    time nor make more units than the launch was sized for."""
+    g = gen(E)
+    off = torch.tensor([0 if e % 2 == 0 else rows - 10 for e in range(E + 1)], dtype=torch.int32, device="cuda")
+    a = torch.randn((rows, K), generator=g, device="cuda").to(dtype)
+    w = torch.randn((E, 40, K), generator=g, device="cuda").to(dtype)
+    out = torch.full((rows, 40), -7.0, dtype=dtype, device="cuda")
+    moe.moe_device_status(clear=True)
+    moe.moe_grouped_gemm(a, off, w, out=out)
+    gw = moe.moe_grouped_gemm_weight_grad(a, a, off) if K <= 128 else None
+    assert moe.moe_device_status(clear=True) == BAD_INDEX
+    n = rows - 10
+    ref = a[:n].double() @ w[0].double().T
+    size = a[:n].double().abs() @ w[0].double().abs().T
+    check(out[:n], ref, size * (K + 1) * 2.0 ** -23, dtype, "the first expert")
+    assert torch.all(out[n:] == -7)
+    if gw is not None:
+        assert torch.all(gw[1:] == 0) and torch.any(gw[0] != 0)
+
+
+def test_few_rows_captured_and_replayed():
+    """The form that joins sums over a cluster, in two graphs on two streams."""
+    g = gen(31)
+    a = torch.randn((3, 4096), generator=g, device="cuda").to(BF16)
+    w = torch.randn((2, 256, 4096), generator=g, device="cuda").to(BF16)
+    off = offsets_of([1, 2])
+    outs = [torch.zeros((3, 256), dtype=BF16, device="cuda") for _ in range(2)]
+    moe.moe_grouped_gemm(a, off, w, out=outs[0])
+    torch.cuda.synchronize()
+    graphs = []
+    for o in outs:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            moe.moe_grouped_gemm(a, off, w, out=o)
+            moe.moe_grouped_gemm(a, off, w, out=o)
+        graphs.append(graph)
+    for counts in ([2, 1], [0, 3], [3, 0]):
+        off.copy_(offsets_of(counts))
+        a.copy_(torch.randn((3, 4096), generator=g, device="cuda"))
+        want = moe.moe_grouped_gemm(a, off, w)
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        for _ in range(3):
+            graphs[0].replay()
+            with torch.cuda.stream(side):
+                graphs[1].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+
+
 GRAD_SHAPES = [(8, 8), (72, 40), (136, 264), (256, 320), (520, 72)]
 
 
@@ -296,6 +349,34 @@ def test_weight_grad(dtype, counts, N, K):
         sum_ = ref + old.double()
         slack = size * terms * 2.0 ** -23 + (ref.abs() + old.double().abs()) * 2.0 ** -24
         check(got, sum_, slack, out_dtype, f"accumulated {out_dtype}")
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("counts", [[1000], [0, 3000, 5], [513, 512, 4097, 0], [40, 9000]])
+@pytest.mark.parametrize("N,K", [(8, 8), (72, 264), (136, 40), (256, 520)])
+def test_weight_grad_of_narrow_matrices_over_long_segments(dtype, counts, N, K):
+    """Few units of work: an expert's rows are shared by 2, 4 or 8 CTAs whose sums are joined."""
+    g = gen(N + K + len(counts))
+    first, rows, E = 3, sum(counts) + 8, len(counts)
+    off = offsets_of(counts, first)
+    a, d = strided(rows, K, dtype, g, 8), strided(rows, N, dtype, g, 8)
+    for m in (a, d):
+        m[:first], m[first + sum(counts):] = float("nan"), float("inf")
+    at = off.tolist()
+    ref = torch.stack([d[at[e]:at[e + 1]].double().T @ a[at[e]:at[e + 1]].double() for e in range(E)])
+    size = torch.stack([d[at[e]:at[e + 1]].double().abs().T @ a[at[e]:at[e + 1]].double().abs()
+                        for e in range(E)])
+    terms = torch.tensor(counts, device="cuda").view(E, 1, 1).double() + 1
+    for out_dtype in {dtype, F32}:
+        room = torch.full((E + 2, N, K), -7.0, dtype=out_dtype, device="cuda")
+        got = moe.moe_grouped_gemm_weight_grad(d, a, off, grad_w=room[1:E + 1])
+        assert torch.all(room[0] == -7) and torch.all(room[-1] == -7)
+        check(got, ref, size * terms * 2.0 ** -23, out_dtype, f"{out_dtype}")
+        assert torch.equal(moe.moe_grouped_gemm_weight_grad(d, a, off, grad_dtype=out_dtype), got)
+        old = torch.randn((E, N, K), generator=g, device="cuda").to(out_dtype)
+        got = moe.moe_grouped_gemm_weight_grad(d, a, off, grad_w=old.clone(), accumulate=True)
+        slack = size * terms * 2.0 ** -23 + (ref.abs() + old.double().abs()) * 2.0 ** -24
+        check(got, ref + old.double(), slack, out_dtype, f"accumulated {out_dtype}")
 
 
 def test_weight_grad_no_rows():
