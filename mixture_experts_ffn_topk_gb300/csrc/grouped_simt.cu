@@ -97,7 +97,7 @@ struct SimtShape {
 };
 
 template <bool WG, bool Y_MAJOR, int BM, int BN, int TM, int TN, int BK, int STAGES>
-__global__ void __launch_bounds__(BM / TM * (BN / TN))
+__global__ void __launch_bounds__(BM / TM * (BN / TN), 2)
 grouped_simt_kernel(SimtOperand x, SimtOperand y, const int32_t *__restrict__ offsets, int E,
                     int rows, int M, int N, int K, float *__restrict__ out, int64_t ldo,
                     int accumulate, unsigned *status)
@@ -213,15 +213,14 @@ cudaError_t launch_tile(const SimtOperand &x, const SimtOperand &y, const int32_
 }
 
 // Tile by the extent of C's rows: the average number of an expert's rows, or
-// grad_w's N. Measured on 64 experts, N = K = 1024 (us; average rows 8, 32, 48,
-// 96, 256, 1024):
+// grad_w's N. Measured on 64 experts, N = K = 1024 (us at 8, 32, 48, 96, 256,
+// 1024 rows on average; [E, K, N] weights are alike):
 //   16 x 128   86.7   206   248   450   1133   4396
-//   64 x 64     227   225   225   439    963   3464
-//   128 x 128   395   397   401   412    917   2952   ([E, K, N]: 425 .. 989 3175,
-//                                                      where 64 x 64 takes 917 3304)
-// so the tall tile is for k-contiguous weights only. Weight gradient, N = 16,
-// 32, 64: 17.7 22.2 33.1 flat, 22.8 22.8 23.7 square; tall 290 to 250 at 1024.
-constexpr int64_t kFlatTile = 40, kTallTile = 80;
+//   64 x 128   -      -     217   387    854   2976
+//   64 x 64    227   225    214   414    903   3243
+// (128 x 64 and 128 x 128: 381 to 412 at 96 rows, 2952 to 3156 at 1024). Weight
+// gradient, N = 16, 32, 64: 17.7 22.2 33.1 us flat, 22.8 22.8 23.7 square.
+constexpr int64_t kFlatTile = 40;
 
 template <bool WG, bool Y_MAJOR>
 cudaError_t launch_sizes(const SimtOperand &x, const SimtOperand &y, const int32_t *offsets, int E,
@@ -232,12 +231,10 @@ cudaError_t launch_sizes(const SimtOperand &x, const SimtOperand &y, const int32
     if (height < kFlatTile)
         return launch_tile<WG, Y_MAJOR, 16, 128, 4, 4, 32, 4>(x, y, offsets, E, rows, M, N, K, out, ldo,
                                                               accumulate, status, s);
-    if constexpr (!WG && !Y_MAJOR) {
-        if (height >= kTallTile && N >= 96)
-            return launch_tile<WG, Y_MAJOR, 128, 128, 8, 8, 16, 3>(x, y, offsets, E, rows, M, N, K, out,
-                                                                   ldo, accumulate, status, s);
-    }
-    return launch_tile<WG, Y_MAJOR, 64, 64, 4, 4, 16, 4>(x, y, offsets, E, rows, M, N, K, out, ldo,
+    if (N > 64)
+        return launch_tile<WG, Y_MAJOR, 64, 128, 4, 8, 16, 3>(x, y, offsets, E, rows, M, N, K, out, ldo,
+                                                              accumulate, status, s);
+    return launch_tile<WG, Y_MAJOR, 64, 64, 4, 4, 32, 3>(x, y, offsets, E, rows, M, N, K, out, ldo,
                                                          accumulate, status, s);
 }
 
