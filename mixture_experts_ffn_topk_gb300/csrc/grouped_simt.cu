@@ -86,6 +86,14 @@ __device__ __forceinline__ void frag(const float *tile, int k, int t, float (&f)
     }
 }
 
+// Two FP32 multiply-adds in one instruction: each half of d += that of a * b.
+__device__ __forceinline__ void fma2(float2 &d, float2 a, float2 b)
+{
+    asm("fma.rn.f32x2 %0, %1, %2, %0;"
+        : "+l"(reinterpret_cast<unsigned long long &>(d))
+        : "l"(reinterpret_cast<const unsigned long long &>(a)), "l"(reinterpret_cast<const unsigned long long &>(b)));
+}
+
 // WG: the reduction runs over the expert's rows (X = grad, Y = a, both stored
 // with the output index contiguous). Otherwise X = a (k contiguous), Y = w,
 // k contiguous unless Y_MAJOR.
@@ -133,11 +141,16 @@ grouped_simt_kernel(SimtOperand x, SimtOperand y, const int32_t *__restrict__ of
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
-        float acc[TM][TN];
+        // where a thread's columns are neighbours, two of them share an
+        // instruction (6 % faster there; sums over even and odd k of one
+        // output, the pairing that k-contiguous operands offer, cost registers
+        // and were 11 % slower than single multiply-adds)
+        constexpr bool PAIRED = WG || Y_MAJOR;
+        float2 acc[TM][TN / 2];
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
-            for (int j = 0; j < TN; ++j) acc[i][j] = 0.0f;
+            for (int j = 0; j < TN / 2; ++j) acc[i][j] = make_float2(0.0f, 0.0f);
         for (int t = 0; t < STAGES - 1; ++t) fetch(t);
         for (int t = 0; t < steps; ++t) {
             asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
@@ -154,7 +167,15 @@ grouped_simt_kernel(SimtOperand x, SimtOperand y, const int32_t *__restrict__ of
 #pragma unroll
                     for (int i = 0; i < TM; ++i)
 #pragma unroll
-                        for (int j = 0; j < TN; ++j) acc[i][j] = fmaf(a[i][kk], b[j][kk], acc[i][j]);
+                        for (int j = 0; j < TN / 2; ++j) {
+                            const float2 y2 = make_float2(b[2 * j][kk], b[2 * j + 1][kk]);
+                            if constexpr (PAIRED) {
+                                fma2(acc[i][j], make_float2(a[i][kk], a[i][kk]), y2);
+                            } else {
+                                acc[i][j].x = fmaf(a[i][kk], y2.x, acc[i][j].x);
+                                acc[i][j].y = fmaf(a[i][kk], y2.y, acc[i][j].y);
+                            }
+                        }
             }
         }
         __syncthreads();                // the ring is free for the next unit
@@ -170,7 +191,7 @@ grouped_simt_kernel(SimtOperand x, SimtOperand y, const int32_t *__restrict__ of
                 for (int j = 0; j < TN; j += 4) {
                     const int n = n0 + index_of<TN, GN, true>(j, tn);
                     if (n >= N) continue;
-                    float4 v = make_float4(acc[i][j], acc[i][j + 1], acc[i][j + 2], acc[i][j + 3]);
+                    float4 v = make_float4(acc[i][j / 2].x, acc[i][j / 2].y, acc[i][j / 2 + 1].x, acc[i][j / 2 + 1].y);
                     if (accumulate) {
                         const float4 old = *reinterpret_cast<const float4 *>(row + n);
                         v = make_float4(old.x + v.x, old.y + v.y, old.z + v.z, old.w + v.w);
@@ -181,7 +202,7 @@ grouped_simt_kernel(SimtOperand x, SimtOperand y, const int32_t *__restrict__ of
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
                     const int n = n0 + index_of<TN, GN, Y_MAJOR>(j, tn);
-                    if (n < N) row[n] = acc[i][j];
+                    if (n < N) row[n] = j & 1 ? acc[i][j / 2].y : acc[i][j / 2].x;
                 }
             }
         }
@@ -214,9 +235,9 @@ cudaError_t launch_tile(const SimtOperand &x, const SimtOperand &y, const int32_
 
 // Tile by the extent of C's rows: the average number of an expert's rows, or
 // grad_w's N. Measured on 64 experts, N = K = 1024 (us at 8, 32, 48, 96, 256,
-// 1024 rows on average; [E, K, N] weights are alike):
-//   16 x 128   86.7   206   248   450   1133   4396
-//   64 x 128   -      -     217   387    854   2976
+// 1024 rows on average; 2.98 ms are 46 TFLOP/s, [E, K, N] weights take 2.80):
+//   16 x 128   76.2   181   248   450   1133   4396
+//   64 x 128   -      -     216   387    854   2975
 //   64 x 64    227   225    214   414    903   3243
 // (128 x 64 and 128 x 128: 381 to 412 at 96 rows, 2952 to 3156 at 1024). Weight
 // gradient, N = 16, 32, 64: 17.7 22.2 33.1 us flat, 22.8 22.8 23.7 square.
