@@ -32,6 +32,9 @@
 // fastest, so that CTAs at work share a weight tile in L2; a block's rows are
 // held to what stays in L2 while all weight tiles pass.
 //
+// FP32 outputs are summed in parts of kPartStages stages, each in the next
+// accumulator; the epilogue adds a later part to what it stored of the earlier.
+//
 // Every wait is bounded (wait_ns); on expiry the kernel records ST_TIMEOUT,
 // stops issuing work, drains its own copies and MMAs, frees TMEM and exits.
 #include <atomic>
@@ -88,6 +91,7 @@ struct GemmParams {
     int slot_bytes;          // ring slot: W_BYTES + this CTA's rows of a full unit
     int stages;
     int split;               // SPLIT: CTAs that share a unit's k
+    int part_kb;             // k-blocks summed in one accumulator (see kPartStages)
     uint8_t *out;
     int64_t out_row_bytes;
     int vec;                 // rows of out start on 16 bytes
@@ -187,6 +191,27 @@ __device__ __forceinline__ void tmem_ld_wait8(uint32_t (&r)[8])
     asm volatile(""
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]),
                    "+r"(r[7]));
+}
+
+// 16 TMEM lanes x 16 consecutive fp32 columns as four 8 x 8 blocks: thread T
+// holds lanes T / 4 (r[0], r[1], r[4], r[5]) and T / 4 + 8 (the others), columns
+// 2 (T % 4) and the next, of columns 0-7 (r[0..3]) and 8-15 (r[4..7]).
+__device__ __forceinline__ void tmem_ld_blocks(uint32_t taddr, uint32_t (&r)[8])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+        : "r"(taddr));
+}
+
+// Stores four 8 x 8 blocks of 16-bit values, one register each, transposed; the
+// lanes 8 m .. 8 m + 7 give the addresses of block m's eight rows of 16 bytes.
+__device__ __forceinline__ void store_blocks_transposed(uint32_t saddr, uint32_t r0, uint32_t r1, uint32_t r2,
+                                                        uint32_t r3)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(r0),
+                 "r"(r1), "r"(r2), "r"(r3)
+                 : "memory");
 }
 
 template <int DT, int CG, bool KN, bool OUT_F32, bool SPLIT>
@@ -298,27 +323,30 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         uint32_t phase = 0;
         int it = 0;
         bool ok = true;
-        for (int unit = unit0; unit < total && ok; unit += unit_step, ++it) {
+        for (int unit = unit0; unit < total && ok; unit += unit_step) {
             const Unit u = walk.at(unit);
             const uint32_t idesc = idesc0 | ((uint32_t)(u.mma_n >> 3) << 17);
-            const int acc = it & 1;
-            const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
-            ok = warp_wait<CG>(&S.acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_ns);
-            if (!ok) break;
-            const uint32_t d = tmem_base + (uint32_t)(acc * ACC_COLS);
-            for (int kb = kb_begin; kb < kb_end; ++kb) {
-                ok = warp_wait<CG>(&S.full[stage], phase, abort_flag, p.status, p.wait_ns);
+            for (int kb0 = kb_begin; kb0 < kb_end && ok; kb0 += p.part_kb, ++it) {
+                const int kb1 = kb_end - kb0 < p.part_kb ? kb_end : kb0 + p.part_kb;
+                const int acc = it & 1;
+                const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
+                ok = warp_wait<CG>(&S.acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_ns);
                 if (!ok) break;
-                tc_fence_after();
-                const uint32_t w = ring + stage * p.slot_bytes, a = w + W_BYTES;
+                const uint32_t d = tmem_base + (uint32_t)(acc * ACC_COLS);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = warp_wait<CG>(&S.full[stage], phase, abort_flag, p.status, p.wait_ns);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t w = ring + stage * p.slot_bytes, a = w + W_BYTES;
 #pragma unroll
-                for (int k = 0; k < BK / UK; ++k)
-                    umma_on<CG>(on, d, KN ? sdesc_mn_sw128(w + k * UK * 128, W_BYTES / 2) : sdesc_k_sw128(w + k * UK * 2),
-                                sdesc_k_sw128(a + k * UK * 2), idesc, (kb - kb_begin) | k ? 1u : 0u);
-                commit_on<CG>(on, &S.empty[stage]);
-                if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+                    for (int k = 0; k < BK / UK; ++k)
+                        umma_on<CG>(on, d, KN ? sdesc_mn_sw128(w + k * UK * 128, W_BYTES / 2) : sdesc_k_sw128(w + k * UK * 2),
+                                    sdesc_k_sw128(a + k * UK * 2), idesc, (kb - kb0) | k ? 1u : 0u);
+                    commit_on<CG>(on, &S.empty[stage]);
+                    if (++stage == p.stages) { stage = 0; phase ^= 1u; }
+                }
+                if (ok) commit_on<CG>(on, &S.acc_full[acc]);
             }
-            if (ok) commit_on<CG>(on, &S.acc_full[acc]);
         }
         // every MMA issued must finish before TMEM is released, also where
         // another role has given up
@@ -336,9 +364,17 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         constexpr int ESZ = OUT_F32 ? 4 : 2;
         constexpr int ROW_BYTES = BM * ESZ;              // staged bytes per row: 512 / 256
         constexpr int PIECES = ROW_BYTES / 16, PER_IT = 128 / PIECES;
-        int it = 0, buf = 0;
-        for (int unit = unit0; unit < total; unit += unit_step, ++it) {
-            const Unit u = walk.at(unit);
+        int it = 0, buf = 0, unit = unit0, kb0 = kb_begin;
+        Unit u = {};
+        // unit by unit, part by part (kb0: the part's first k-block)
+        for (; unit < total; ++it, kb0 += p.part_kb) {
+            if (kb0 >= kb_end) {
+                kb0 = kb_begin;
+                unit += unit_step;
+                if (unit >= total) break;
+            }
+            if (kb0 == kb_begin) u = walk.at(unit);
+            const bool more = OUT_F32 && kb0 != kb_begin;     // adds to what the earlier parts left
             const int acc = it & 1;
             const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
             // a group's warps leave together: none may wait at a barrier for
@@ -357,26 +393,36 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     tmem_ld16(tbase + t0, v);
                     tmem_ld_wait16(v);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) mine[(t0 + i) * BM] = __uint_as_float(v[i]);
+                    for (int i = 0; i < 16; ++i)
+                        mine[(t0 + i) * BM] = more ? mine[(t0 + i) * BM] + __uint_as_float(v[i]) : __uint_as_float(v[i]);
                 }
             }
             for (int t0 = group * CH; !SPLIT && t0 < u.rows; t0 += 2 * CH, buf ^= 1) {
-                uint8_t *stg = S.stg[group][buf], *mine = stg + (q * 32 + lane) * ESZ;
+                uint8_t *stg = S.stg[group][buf];
                 if constexpr (OUT_F32) {
+                    uint8_t *mine = stg + (q * 32 + lane) * ESZ;
                     uint32_t v[8];
                     tmem_ld8(tbase + t0, v);
                     tmem_ld_wait8(v);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) *reinterpret_cast<uint32_t *>(mine + i * ROW_BYTES) = v[i];
                 } else {
-                    uint32_t v[16];
-                    tmem_ld16(tbase + t0, v);
-                    tmem_ld_wait16(v);
+                    // blocks of 8 n by 8 rows, rounded, leave transposed; the 16-byte
+                    // pieces of row t are permuted by t % 8, so that a block's eight
+                    // rows (256 bytes apart) meet no bank twice
+                    uint32_t lo[8], hi[8];               // lanes 0-15, 16-31 of the quadrant
+                    tmem_ld_blocks(tbase + t0, lo);
+                    tmem_ld_blocks(tbase + (16u << 16) + t0, hi);
+                    tmem_ld_wait8(lo);
+                    tmem_ld_wait8(hi);
+                    const int t = lane & 7, at = q * 4 + (lane >> 3);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const uint32_t w = pack2<DT>(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-                        *reinterpret_cast<uint16_t *>(mine + 2 * i * ROW_BYTES) = (uint16_t)w;
-                        *reinterpret_cast<uint16_t *>(mine + (2 * i + 1) * ROW_BYTES) = (uint16_t)(w >> 16);
+                    for (int c = 0; c < 2; ++c) {
+                        auto block = [&](const uint32_t (&v)[8], int i) {
+                            return pack2<DT>(__uint_as_float(v[c * 4 + i]), __uint_as_float(v[c * 4 + i + 1]));
+                        };
+                        store_blocks_transposed(smem_u32(stg + (c * 8 + t) * ROW_BYTES + ((at ^ t) << 4)),
+                                                block(lo, 0), block(lo, 2), block(hi, 0), block(hi, 2));
                     }
                 }
                 // one barrier per buffer: who passes it has read the other one
@@ -384,9 +430,24 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
 #pragma unroll
                 for (int i = 0; i < CH / PER_IT; ++i) {
                     const int t = i * PER_IT + tid / PIECES;
-                    const uint4 v = *reinterpret_cast<const uint4 *>(stg + t * ROW_BYTES + piece * 16);
+                    uint4 v = *reinterpret_cast<const uint4 *>(
+                        stg + t * ROW_BYTES + (OUT_F32 ? piece : piece ^ (t & 7)) * 16);
                     if (t0 + t >= u.rows) continue;
                     uint8_t *dst = out0 + (int64_t)(t0 + t) * p.out_row_bytes;
+                    if (more) {
+                        // this thread stored these sums itself
+                        Vec16 x;
+                        x.u = v;
+                        if (whole) {
+                            const float4 y = *reinterpret_cast<const float4 *>(dst);
+                            x.f[0] += y.x; x.f[1] += y.y; x.f[2] += y.z; x.f[3] += y.w;
+                        } else {
+#pragma unroll
+                            for (int c = 0; c < 4; ++c)
+                                if (col + c < p.N) x.f[c] += reinterpret_cast<const float *>(dst)[c];
+                        }
+                        v = x.u;
+                    }
                     if (whole) {
                         *reinterpret_cast<uint4 *>(dst) = v;
                     } else {
@@ -548,6 +609,7 @@ cudaError_t launch_cg(const void *a, int64_t lda, const int32_t *offsets, int64_
     p.out_row_bytes = ldo * (out_f32 ? 4 : 2);
     p.vec = p.out_row_bytes % 16 == 0;
     p.status = status;
+    p.part_kb = out_f32 ? kPartStages : (1 << 20);
     // a wait may last one unit's whole reduction: a microsecond per stage on top
     p.wait_ns = wait_limit_ns() + 1000ull * (uint64_t)((K + BK - 1) / BK);
     // an upper bound: every expert adds at most one unit that is not full

@@ -23,9 +23,12 @@
 // CTA pairs (CG = 2): M = 256, each CTA holds 128 columns of grad and half of
 // a's; the even CTA issues the MMAs.
 // Few units (narrow matrices) and long segments: a cluster of 2, 4 or 8 single
-// CTAs shares each unit's rows (SPLIT); the FP32 partial sums meet through
-// distributed shared memory, in the ring's place, each CTA adding its share of
+// CTAs shares each unit's rows (SPLIT, units of 128 columns); the FP32 partial
+// sums meet through distributed shared memory, each CTA adding its share of
 // the columns in rank order.
+// FP32 gradients are summed in parts of kPartStages stages, each in the next
+// accumulator; the epilogue adds a later part to what the earlier ones left, in
+// grad_w (which L2 holds meanwhile) or, SPLIT, in shared memory.
 // Units run over (expert, tile of the wider matrix, tile of the narrower one),
 // the last fastest: the narrower operand's segment stays in L2 while the wider
 // one passes once.
@@ -44,15 +47,22 @@ namespace moe {
 namespace {
 
 constexpr int BM = 128;                  // rows of grad_w per CTA
-constexpr int BN = 256;                  // columns of grad_w per unit
+// columns of grad_w per unit; half as many where sums are joined, which leaves
+// the ring's last 64 KiB to them
+template <bool SPLIT>
+constexpr int BN = SPLIT ? 128 : 256;
 constexpr int BK = 64;                   // rows reduced per stage
 constexpr int UK = 16;                   // rows reduced per tcgen05.mma
 constexpr int BOX_BYTES = 64 * BK * 2;   // 64 columns x 64 rows
 constexpr int G_BYTES = 2 * BOX_BYTES;
-template <int CG>
-constexpr int SLOT_BYTES = G_BYTES + 4 / CG * BOX_BYTES;
+template <int CG, bool SPLIT>
+constexpr int SLOT_BYTES = G_BYTES + BN<SPLIT> / 64 / CG * BOX_BYTES;
 template <int CG>
 constexpr int STAGES = CG == 2 ? 6 : 4;
+constexpr int RING_BYTES = 192 << 10;
+constexpr int PARTIAL_AT = STAGES<1> * SLOT_BYTES<1, true>;       // SPLIT: the sums, [column][row]
+static_assert(STAGES<1> * SLOT_BYTES<1, false> <= RING_BYTES && STAGES<2> * SLOT_BYTES<2, false> <= RING_BYTES &&
+              PARTIAL_AT + BN<true> * BM * 4 <= RING_BYTES, "the ring");
 constexpr int ACC_COLS = 256;
 constexpr int TMEM_COLS = 2 * ACC_COLS;
 constexpr int THREADS = 256;
@@ -62,7 +72,7 @@ constexpr uint64_t kDrainLimitNs = 100000000ull;
 
 template <int CG>
 struct __align__(1024) Smem {
-    uint8_t ring[STAGES<CG>][SLOT_BYTES<CG>];
+    uint8_t ring[RING_BYTES];
     uint8_t stg[4][2][STG_BYTES];
     uint64_t full[STAGES<CG>];
     uint64_t empty[STAGES<CG>];
@@ -86,6 +96,7 @@ struct WgradParams {
     int n_tiles, k_tiles;
     int n_fast;              // the n tile runs fastest (grad is the narrower operand)
     int split;               // SPLIT: CTAs that share a unit's rows
+    int part_kb;             // blocks of rows summed in one accumulator (see kPartStages)
     uint8_t *out;            // read where the gradient is added to, written where split
     int64_t out_row_bytes;
     int accumulate;
@@ -145,10 +156,10 @@ struct UnitWalk {
         u.nkb = (u.cnt + BK - 1) / BK;
         u.tail = u.cnt - (u.nkb - 1) * BK;
         u.n0 = (nt * CG + rank) * BM;
-        u.k0 = kt * BN;
+        u.k0 = kt * BN<SPLIT>;
         // whole 64-column boxes for each CTA: an MN-major operand's 128-byte rows
         const int left = p.K - u.k0;
-        u.mma_n = left >= BN ? BN : (left + 64 * CG - 1) / (64 * CG) * (64 * CG);
+        u.mma_n = left >= BN<SPLIT> ? BN<SPLIT> : (left + 64 * CG - 1) / (64 * CG) * (64 * CG);
         e += de;
         outer += douter;
         inner += dinner;
@@ -237,7 +248,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
                     bar = CG == 2 ? mapa_shared(here, 0) : here;
                     if (ARM && leader) expect_tx_on(on, &S.full[stage], CG * bytes);
                 }
-                loads(ring + stage * SLOT_BYTES<CG>, bar, u, u.row0 + kb * BK);
+                loads(ring + stage * SLOT_BYTES<CG, SPLIT>, bar, u, u.row0 + kb * BK);
                 if (++stage == NS) { stage = 0; phase ^= 1u; }
             }
         }
@@ -255,7 +266,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
         produce(on, std::false_type{}, [&](uint32_t dst, uint32_t bar, const Unit &u, int row) {
             const int mine = u.mma_n / CG, col0 = u.k0 + rank * mine;     // columns this CTA loads
 #pragma unroll
-            for (int j = 0; j < 4 / CG; ++j)
+            for (int j = 0; j < BN<SPLIT> / 64 / CG; ++j)
                 load_2d_on<CG>(j * 64 < mine ? on : 0u, dst + G_BYTES + j * BOX_BYTES, &map_a, bar, col0 + j * 64, row);
         });
     } else if (warp == 1 && leader) {
@@ -267,40 +278,47 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
         uint32_t phase = 0, tails = 0;
         int it = 0;
         bool ok = true;
-        for (int unit = unit0; unit < total && ok; unit += unit_step, ++it) {
+        for (int unit = unit0; unit < total && ok; unit += unit_step) {
             const Unit u = walk.next();
             const uint32_t idesc = idesc0 | ((uint32_t)(u.mma_n >> 3) << 17);
-            const int acc = it & 1;
-            const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
-            ok = warp_wait<CG>(&S.acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_ns);
-            if (!ok) break;
-            const uint32_t d = tmem_base + (uint32_t)(acc * ACC_COLS);
-            for (int kb = 0; kb < u.nkb; ++kb) {
-                ok = warp_wait<CG>(&S.full[stage], phase, abort_flag, p.status, p.wait_ns);
+            // (an expert without rows commits one part with no MMA: its epilogue writes zeros)
+            int kb0 = 0;
+            do {
+                const int kb1 = u.nkb - kb0 < p.part_kb ? u.nkb : kb0 + p.part_kb;
+                const int acc = it & 1;
+                const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
+                ok = warp_wait<CG>(&S.acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_ns);
                 if (!ok) break;
-                const int valid = kb == u.nkb - 1 ? u.tail : BK;
-                if (valid % UK != 0) {
-                    ok = warp_wait<CG>(&S.tail_out[stage], tails >> stage & 1u, abort_flag, p.status, p.wait_ns);
+                const uint32_t d = tmem_base + (uint32_t)(acc * ACC_COLS);
+                for (int kb = kb0; kb < kb1; ++kb) {
+                    ok = warp_wait<CG>(&S.full[stage], phase, abort_flag, p.status, p.wait_ns);
                     if (!ok) break;
-                    tails ^= 1u << stage;
-                }
-                tc_fence_after();
-                const uint32_t g = ring + stage * SLOT_BYTES<CG>, a = g + G_BYTES;
-                auto mma = [&](int k) {
-                    umma_on<CG>(on, d, sdesc_mn_sw128(g + k * UK * 128, BOX_BYTES),
-                                sdesc_mn_sw128(a + k * UK * 128, BOX_BYTES), idesc, (kb | k) != 0 ? 1u : 0u);
-                };
-                if (valid == BK) {
+                    const int valid = kb == u.nkb - 1 ? u.tail : BK;
+                    if (valid % UK != 0) {
+                        ok = warp_wait<CG>(&S.tail_out[stage], tails >> stage & 1u, abort_flag, p.status, p.wait_ns);
+                        if (!ok) break;
+                        tails ^= 1u << stage;
+                    }
+                    tc_fence_after();
+                    const uint32_t g = ring + stage * SLOT_BYTES<CG, SPLIT>, a = g + G_BYTES;
+                    auto mma = [&](int k) {
+                        umma_on<CG>(on, d, sdesc_mn_sw128(g + k * UK * 128, BOX_BYTES),
+                                    sdesc_mn_sw128(a + k * UK * 128, BOX_BYTES), idesc, (kb - kb0) | k ? 1u : 0u);
+                    };
+                    if (valid == BK) {
 #pragma unroll
-                    for (int k = 0; k < BK / UK; ++k) mma(k);
-                } else {
-                    for (int k = 0; k * UK < valid; ++k) mma(k);
+                        for (int k = 0; k < BK / UK; ++k) mma(k);
+                    } else {
+                        for (int k = 0; k * UK < valid; ++k) mma(k);
+                    }
+                    commit_on<CG>(on, &S.empty[stage]);
+                    if (++stage == NS) { stage = 0; phase ^= 1u; }
                 }
-                commit_on<CG>(on, &S.empty[stage]);
-                if (++stage == NS) { stage = 0; phase ^= 1u; }
-            }
-            // (an expert without rows commits with no MMA: its epilogue writes zeros)
-            if (ok) commit_on<CG>(on, &S.acc_full[acc]);
+                if (!ok) break;
+                commit_on<CG>(on, &S.acc_full[acc]);
+                ++it;
+                kb0 = kb1;
+            } while (kb0 < u.nkb);
         }
         // every MMA issued must finish before TMEM is released, also where
         // another role has given up
@@ -326,7 +344,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
                 const int boxes = 2 + u.mma_n / CG / 64;
                 for (int i = lane; i < boxes * nrows * 8; i += 32) {
                     const int box = i / (nrows * 8), c = i - box * (nrows * 8);
-                    *reinterpret_cast<uint4 *>(S.ring[stage] + box * BOX_BYTES + u.tail * 128 + c * 16) =
+                    *reinterpret_cast<uint4 *>(S.ring + stage * SLOT_BYTES<CG, SPLIT> + box * BOX_BYTES + u.tail * 128 + c * 16) =
                         make_uint4(0u, 0u, 0u, 0u);
                 }
                 // the MMA reads shared memory through the async proxy
@@ -345,9 +363,17 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
         constexpr int ESZ = OUT_F32 ? 4 : 2;
         constexpr int COLS = STG_ROW_BYTES / ESZ;  // columns per staging buffer: 16 / 32
         const uint32_t on = elect_lane();
-        int it = 0, buf = 0;
-        for (int unit = unit0; unit < total; unit += unit_step, ++it) {
-            const Unit u = walk.next();
+        int it = 0, buf = 0, unit = unit0, kb0 = 0;
+        Unit u = {};
+        // unit by unit, part by part (kb0: the part's first block of rows)
+        for (; unit < total; ++it, kb0 += p.part_kb) {
+            if (kb0 != 0 && kb0 >= u.nkb) {
+                kb0 = 0;
+                unit += unit_step;
+                if (unit >= total) break;
+            }
+            if (kb0 == 0) u = walk.next();
+            const bool more = kb0 != 0;                // adds to what the earlier parts left
             const int acc = it & 1;
             const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
             const bool ready = mbar_wait<CG>(&S.acc_full[acc], acc_phase, abort_flag, p.status, p.wait_ns);
@@ -356,20 +382,29 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
             const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
             const int row0 = u.n0 + q * 32;            // this warp's first row of grad_w[e]
             const bool empty = u.cnt == 0;
-            int width = p.K - u.k0 < BN ? p.K - u.k0 : BN;
+            int width = p.K - u.k0 < BN<SPLIT> ? p.K - u.k0 : BN<SPLIT>;
             if constexpr (SPLIT) {
                 // the partial sums stay here, [column][row] in FP32
-                float *mine = reinterpret_cast<float *>(S.ring[0]) + q * 32 + lane;
+                float *mine = reinterpret_cast<float *>(S.ring + PARTIAL_AT) + q * 32 + lane;
                 for (int c0 = 0; c0 < width; c0 += 32) {
                     uint32_t v[32];
                     tmem_ld32(tbase + c0, v);
                     tmem_ld_wait(v);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) mine[(c0 + i) * BM] = empty ? 0.0f : __uint_as_float(v[i]);
+                    for (int i = 0; i < 32; ++i) {
+                        const float x = empty ? 0.0f : __uint_as_float(v[i]);
+                        mine[(c0 + i) * BM] = more ? mine[(c0 + i) * BM] + x : x;
+                    }
                 }
                 width = 0;
             }
             if (row0 >= p.N || (empty && p.accumulate)) width = 0;
+            if (more && width > 0) {
+                // the earlier part's stores are complete before they are read
+                if (on) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                __syncwarp();
+                asm volatile("fence.proxy.async.global;" ::: "memory");
+            }
             for (int c0 = 0; c0 < width; c0 += 32) {
                 uint32_t v[32];
                 tmem_ld32(tbase + c0, v);
@@ -378,14 +413,18 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0u;
                 }
-                if (p.accumulate && row0 + lane < p.N) {
+                if ((p.accumulate || more) && row0 + lane < p.N) {
                     const int64_t col_byte = (int64_t)(u.k0 + c0) * ESZ;
                     const uint8_t *old = p.out + ((int64_t)u.e * p.N + row0 + lane) * p.out_row_bytes + col_byte;
 #pragma unroll
                     for (int c = 0; c < 32 * ESZ / 16; ++c) {
                         if (col_byte + c * 16 >= p.out_row_bytes) continue;
                         Vec16 o;
-                        o.u = *reinterpret_cast<const uint4 *>(old + c * 16);
+                        // past L1, which TMA stores do not update
+                        asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(o.w[0]), "=r"(o.w[1]), "=r"(o.w[2]), "=r"(o.w[3])
+                                     : "l"(old + c * 16)
+                                     : "memory");
                         if constexpr (OUT_F32) {
 #pragma unroll
                             for (int i = 0; i < 4; ++i)
@@ -445,7 +484,6 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
     }
 
     if constexpr (SPLIT) {
-        static_assert(BN * BM * 4 <= sizeof(S.ring), "the partial sums take the ring's place");
         // every CTA's partial sums are written; each adds its columns, eight
         // of a row at a time
         __syncwarp();
@@ -453,8 +491,8 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
         if (unit0 < total) {
             const int slice = (int)cluster_ctarank();
             const Unit u = UnitWalk<CG, SPLIT>(S.seg, p, rank, unit0, unit_step).next();
-            const int width = p.K - u.k0 < BN ? p.K - u.k0 : BN;
-            const uint32_t partial = smem_u32(S.ring[0]);
+            const int width = p.K - u.k0 < BN<SPLIT> ? p.K - u.k0 : BN<SPLIT>;
+            const uint32_t partial = smem_u32(S.ring + PARTIAL_AT);
             for (int i = threadIdx.x; !(u.idle && p.accumulate); i += THREADS) {
                 const int c = (i / BM * ways + slice) * 8, n = i % BM;
                 if (c >= width) break;
@@ -536,7 +574,7 @@ cudaError_t launch_kernel(const CUtensorMap &mg, const CUtensorMap &ma, const CU
     auto kernel = grouped_wgrad_kernel<DT, CG, OUT_F32, SPLIT>;
     const int ways = SPLIT ? p.split : CG;
     p.n_tiles = (p.N + BM * CG - 1) / (BM * CG);
-    p.k_tiles = (p.K + BN - 1) / BN;
+    p.k_tiles = (p.K + BN<SPLIT> - 1) / BN<SPLIT>;
     p.n_fast = p.N <= p.K;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(THREADS);
@@ -599,11 +637,12 @@ cudaError_t launch_dt(const void *grad, int64_t ldg, const void *a, int64_t lda,
     p.out_row_bytes = K * (out_f32 ? 4 : 2);
     p.accumulate = accumulate;
     p.status = status;
+    p.part_kb = out_f32 ? kPartStages : (1 << 30);
     // a wait may last one unit's whole reduction: a microsecond per stage on top
     p.wait_ns = wait_limit_ns() + 1000ull * (uint64_t)((rows + BK - 1) / BK);
     // Few units: split an expert's rows over as many CTAs, 2 to 8, as the GPU has
     // room for and as leave each four blocks of rows on average.
-    const int64_t units = (int64_t)E * ((N + BM - 1) / BM) * ((K + BN - 1) / BN);
+    const int64_t units = (int64_t)E * ((N + BM - 1) / BM) * ((K + BN<true> - 1) / BN<true>);
     const int64_t blocks = rows / E / BK, sms = device_sm_count();
     p.split = 1;
     while (p.split < 8 && units * p.split * 2 <= sms && blocks >= p.split * 2 * 4) p.split *= 2;

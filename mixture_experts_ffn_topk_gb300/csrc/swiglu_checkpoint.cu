@@ -321,7 +321,7 @@ swiglu_checkpoint_backward_kernel(const void *__restrict__ grad_h, int64_t ld_by
                 float t, not_t;
                 sigmoid_of<DT>(g[i], t, not_t);
                 const float gt = g[i] * t, x = d[k].at(i);
-                dg[i] = x * u[i] * (t * (1.0f + g[i] * not_t));
+                dg[i] = x * (u[i] * (t * (1.0f + g[i] * not_t)));
                 du[i] = x * gt;
                 o[i] = gt * u[i];
             }

@@ -171,6 +171,37 @@ def test_product_of_few_rows_with_bad_offsets():
     assert torch.all(out[5:] == -7)
 
 
+def test_fp32_outputs_do_not_drift_over_long_sums():
+    """Positive terms, so that a sum that loses a little at each step loses it always. FP32 outputs of
+    16-bit operands are summed in parts of 768 terms: at most 48 truncating steps of 16 and 17 roundings
+    within a step, then one rounding per part, each of at most 2^-23 of the (positive) sum."""
+    g = gen(40)
+    pos = lambda *s: (torch.rand(s, generator=g, device="cuda") + 0.5).to(BF16)
+    K = 14336
+    tol = (48 + 17 + (K + 767) // 768) * 2.0 ** -23
+    for E, rows, N in ((1, 3, 40), (2, 300, 264), (8, 48, 2100)):      # joined, pairs, single CTAs
+        off = offsets_of([rows // E] * E)
+        a, w = pos(rows, K), pos(E, N, K)
+        ref, _ = ref_product(a, off, w, False)
+        for got in (moe.moe_grouped_gemm(a, off, w, out_dtype=F32),
+                    moe.moe_grouped_gemm(a, off, w.transpose(1, 2).contiguous(), transposed=True, out_dtype=F32)
+                    if N % 8 == 0 else ref):
+            assert float(((got.double() - ref).abs() / ref).max()) <= tol, (E, rows, N)
+    for E, rows, N, K in ((1, 20000, 40, 72), (2, 12000, 264, 2048), (16, 16 * 500 + 3000, 1024, 1032)):
+        c = [3500] + [500] * (E - 1) if E == 16 else [rows // E] * E   # joined, pairs, single CTAs
+        off = offsets_of(c)
+        a, d = pos(rows, K), pos(rows, N)
+        at = off.tolist()
+        got = moe.moe_grouped_gemm_weight_grad(d, a, off)
+        old = moe.moe_grouped_gemm_weight_grad(d, a, off, grad_w=got.clone(), accumulate=True)
+        for e in range(E):
+            s = slice(at[e], at[e + 1])
+            ref = d[s].double().T @ a[s].double()
+            tol = (48 + 17 + (c[e] + 767) // 768 + 8) * 2.0 ** -23     # and up to 8 joined CTAs
+            assert float(((got[e].double() - ref).abs() / ref).max()) <= tol, (E, e)
+            assert float(((old[e].double() - 2 * ref).abs() / ref).max()) <= 2 * tol, (E, e)
+
+
 def test_product_many_experts():
     """1024 experts, most of them idle, and the last one busy."""
     g = gen(5)
