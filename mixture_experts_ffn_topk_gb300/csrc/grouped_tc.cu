@@ -33,7 +33,8 @@
 // held to what stays in L2 while all weight tiles pass.
 //
 // FP32 outputs are summed in parts of kPartStages stages, each in the next
-// accumulator; the epilogue adds a later part to what it stored of the earlier.
+// accumulator; the epilogue adds them in registers (PARTS, units of 128 rows at
+// most) or, SPLIT, in shared memory.
 //
 // Every wait is bounded (wait_ns); on expiry the kernel records ST_TIMEOUT,
 // stops issuing work, drains its own copies and MMAs, frees TMEM and exits.
@@ -60,6 +61,7 @@ constexpr int THREADS = 352;
 constexpr int EPI_WARPS = 8;             // two groups of four: 2-5 and 7-10
 constexpr int STG_BYTES = 4096;          // one epilogue staging buffer
 constexpr int SPLIT_CAP = 64;            // rows of a split unit at most
+constexpr int PARTS_CAP = 128;           // rows of a unit whose parts are added in registers
 constexpr int PARTIAL_BYTES = SPLIT_CAP * BM * 4;
 constexpr uint64_t kDrainLimitNs = 100000000ull;
 // Bytes of rows a block of row units may cover, well inside the 129 MB L2
@@ -214,7 +216,7 @@ __device__ __forceinline__ void store_blocks_transposed(uint32_t saddr, uint32_t
                  : "memory");
 }
 
-template <int DT, int CG, bool KN, bool OUT_F32, bool SPLIT>
+template <int DT, int CG, bool KN, bool OUT_F32, bool SPLIT, bool PARTS>
 __global__ void __launch_bounds__(THREADS, 1)
 grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_a,
                     const GemmParams p)
@@ -225,6 +227,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     const int rank = CG == 2 ? (int)cluster_ctarank() : 0;
     const bool leader = rank == 0;
     static_assert(!SPLIT || CG == 1, "a split unit runs on single CTAs");
+    static_assert(!PARTS || (OUT_F32 && !SPLIT), "sums of parts in registers");
     const int ways = SPLIT ? p.split : CG;           // CTAs per unit
     const int unit0 = (int)blockIdx.x / ways, unit_step = (int)gridDim.x / ways;
     // this CTA's k-blocks
@@ -366,6 +369,17 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         constexpr int PIECES = ROW_BYTES / 16, PER_IT = 128 / PIECES;
         int it = 0, buf = 0, unit = unit0, kb0 = kb_begin;
         Unit u = {};
+        // an accumulator is read: the next part but one may have it
+        auto release = [&](int acc) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2 && !leader) mbar_arrive_cluster(mapa_shared(smem_u32(&S.acc_empty[acc]), 0));
+                else mbar_arrive(&S.acc_empty[acc]);
+            }
+        };
+        float sums[PARTS ? PARTS_CAP / 32 : 1][16];        // PARTS: of this lane's n and the group's rows
+        (void)sums;
         // unit by unit, part by part (kb0: the part's first k-block)
         for (; unit < total; ++it, kb0 += p.part_kb) {
             if (kb0 >= kb_end) {
@@ -397,57 +411,18 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                         mine[(t0 + i) * BM] = more ? mine[(t0 + i) * BM] + __uint_as_float(v[i]) : __uint_as_float(v[i]);
                 }
             }
-            for (int t0 = group * CH; !SPLIT && t0 < u.rows; t0 += 2 * CH, buf ^= 1) {
-                uint8_t *stg = S.stg[group][buf];
-                if constexpr (OUT_F32) {
-                    uint8_t *mine = stg + (q * 32 + lane) * ESZ;
-                    uint32_t v[8];
-                    tmem_ld8(tbase + t0, v);
-                    tmem_ld_wait8(v);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) *reinterpret_cast<uint32_t *>(mine + i * ROW_BYTES) = v[i];
-                } else {
-                    // blocks of 8 n by 8 rows, rounded, leave transposed; the 16-byte
-                    // pieces of row t are permuted by t % 8, so that a block's eight
-                    // rows (256 bytes apart) meet no bank twice
-                    uint32_t lo[8], hi[8];               // lanes 0-15, 16-31 of the quadrant
-                    tmem_ld_blocks(tbase + t0, lo);
-                    tmem_ld_blocks(tbase + (16u << 16) + t0, hi);
-                    tmem_ld_wait8(lo);
-                    tmem_ld_wait8(hi);
-                    const int t = lane & 7, at = q * 4 + (lane >> 3);
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        auto block = [&](const uint32_t (&v)[8], int i) {
-                            return pack2<DT>(__uint_as_float(v[c * 4 + i]), __uint_as_float(v[c * 4 + i + 1]));
-                        };
-                        store_blocks_transposed(smem_u32(stg + (c * 8 + t) * ROW_BYTES + ((at ^ t) << 4)),
-                                                block(lo, 0), block(lo, 2), block(hi, 0), block(hi, 2));
-                    }
-                }
+            // Stores CH staged rows from row t0 of the unit on; all four warps
+            // of the group call, with their part of the rows in the buffer.
+            auto store_rows = [&](const uint8_t *stg, int t0) {
                 // one barrier per buffer: who passes it has read the other one
                 epi_sync(1 + group);
 #pragma unroll
                 for (int i = 0; i < CH / PER_IT; ++i) {
                     const int t = i * PER_IT + tid / PIECES;
-                    uint4 v = *reinterpret_cast<const uint4 *>(
+                    const uint4 v = *reinterpret_cast<const uint4 *>(
                         stg + t * ROW_BYTES + (OUT_F32 ? piece : piece ^ (t & 7)) * 16);
                     if (t0 + t >= u.rows) continue;
                     uint8_t *dst = out0 + (int64_t)(t0 + t) * p.out_row_bytes;
-                    if (more) {
-                        // this thread stored these sums itself
-                        Vec16 x;
-                        x.u = v;
-                        if (whole) {
-                            const float4 y = *reinterpret_cast<const float4 *>(dst);
-                            x.f[0] += y.x; x.f[1] += y.y; x.f[2] += y.z; x.f[3] += y.w;
-                        } else {
-#pragma unroll
-                            for (int c = 0; c < 4; ++c)
-                                if (col + c < p.N) x.f[c] += reinterpret_cast<const float *>(dst)[c];
-                        }
-                        v = x.u;
-                    }
                     if (whole) {
                         *reinterpret_cast<uint4 *>(dst) = v;
                     } else {
@@ -460,13 +435,71 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                         }
                     }
                 }
-            }
-            // the accumulator is read: the next unit but one may have it
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (CG == 2 && !leader) mbar_arrive_cluster(mapa_shared(smem_u32(&S.acc_empty[acc]), 0));
-                else mbar_arrive(&S.acc_empty[acc]);
+            };
+            auto stage_fp32 = [&](const float *v, int t0) {
+                uint8_t *stg = S.stg[group][buf], *mine = stg + (q * 32 + lane) * ESZ;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) *reinterpret_cast<float *>(mine + i * ROW_BYTES) = v[i];
+                store_rows(stg, t0);
+                buf ^= 1;
+            };
+            if constexpr (PARTS) {
+                // this group's rows: 16 of every 32, at most 64
+#pragma unroll
+                for (int j = 0; j < PARTS_CAP / 32; ++j) {
+                    const int t0 = j * 32 + group * 16;
+                    if (t0 >= u.rows) continue;
+                    uint32_t v[16];
+                    tmem_ld16(tbase + t0, v);
+                    tmem_ld_wait16(v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        sums[j][i] = more ? sums[j][i] + __uint_as_float(v[i]) : __uint_as_float(v[i]);
+                }
+                release(acc);
+                if (kb_end - kb0 > p.part_kb) continue;
+#pragma unroll
+                for (int j = 0; j < PARTS_CAP / 32; ++j) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int t0 = j * 32 + group * 16 + h * 8;
+                        if (t0 < u.rows) stage_fp32(&sums[j][h * 8], t0);
+                    }
+                }
+            } else {
+                for (int t0 = group * CH; !SPLIT && t0 < u.rows; t0 += 2 * CH) {
+                    if constexpr (OUT_F32) {
+                        uint32_t v[8];
+                        tmem_ld8(tbase + t0, v);
+                        tmem_ld_wait8(v);
+                        float f[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(v[i]);
+                        stage_fp32(f, t0);
+                    } else {
+                        // blocks of 8 n by 8 rows, rounded, leave transposed; the 16-byte
+                        // pieces of row t are permuted by t % 8, so that a block's eight
+                        // rows (256 bytes apart) meet no bank twice
+                        const uint8_t *stg = S.stg[group][buf];
+                        uint32_t lo[8], hi[8];               // lanes 0-15, 16-31 of the quadrant
+                        tmem_ld_blocks(tbase + t0, lo);
+                        tmem_ld_blocks(tbase + (16u << 16) + t0, hi);
+                        tmem_ld_wait8(lo);
+                        tmem_ld_wait8(hi);
+                        const int t = lane & 7, at = q * 4 + (lane >> 3);
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            auto block = [&](const uint32_t (&v)[8], int i) {
+                                return pack2<DT>(__uint_as_float(v[c * 4 + i]), __uint_as_float(v[c * 4 + i + 1]));
+                            };
+                            store_blocks_transposed(smem_u32(stg + (c * 8 + t) * ROW_BYTES + ((at ^ t) << 4)),
+                                                    block(lo, 0), block(lo, 2), block(hi, 0), block(hi, 2));
+                        }
+                        store_rows(stg, t0);
+                        buf ^= 1;
+                    }
+                }
+                release(acc);
             }
         }
     }
@@ -550,12 +583,12 @@ cudaError_t prepare_kernel(Kernel kernel, int cg, std::atomic<int> *cache, int *
     return cudaSuccess;
 }
 
-template <int DT, int CG, bool KN, bool OUT_F32, bool SPLIT>
+template <int DT, int CG, bool KN, bool OUT_F32, bool SPLIT, bool PARTS>
 cudaError_t launch_kernel(int64_t units, const CUtensorMap &mw, const RowMaps &ma, const GemmParams &p,
                           cudaStream_t s)
 {
     static std::atomic<int> cache[kCachedDevices];
-    auto kernel = grouped_gemm_kernel<DT, CG, KN, OUT_F32, SPLIT>;
+    auto kernel = grouped_gemm_kernel<DT, CG, KN, OUT_F32, SPLIT, PARTS>;
     int ctas = 0;
     cudaError_t err = prepare_kernel(kernel, CG, cache, &ctas);
     if (err != cudaSuccess) return err;
@@ -614,11 +647,16 @@ cudaError_t launch_cg(const void *a, int64_t lda, const int32_t *offsets, int64_
     p.wait_ns = wait_limit_ns() + 1000ull * (uint64_t)((K + BK - 1) / BK);
     // an upper bound: every expert adds at most one unit that is not full
     const int64_t units = (rows / tok_cap + (rows < E ? rows : E)) * p.w_tiles;
+    if constexpr (!SPLIT) {
+        if (out_f32 && (K + BK - 1) / BK > kPartStages)
+            return kn ? launch_kernel<DT, CG, true, true, false, true>(units, mw, ma, p, s)
+                      : launch_kernel<DT, CG, false, true, false, true>(units, mw, ma, p, s);
+    }
     if (out_f32)
-        return kn ? launch_kernel<DT, CG, true, true, SPLIT>(units, mw, ma, p, s)
-                  : launch_kernel<DT, CG, false, true, SPLIT>(units, mw, ma, p, s);
-    return kn ? launch_kernel<DT, CG, true, false, SPLIT>(units, mw, ma, p, s)
-              : launch_kernel<DT, CG, false, false, SPLIT>(units, mw, ma, p, s);
+        return kn ? launch_kernel<DT, CG, true, true, SPLIT, false>(units, mw, ma, p, s)
+                  : launch_kernel<DT, CG, false, true, SPLIT, false>(units, mw, ma, p, s);
+    return kn ? launch_kernel<DT, CG, true, false, SPLIT, false>(units, mw, ma, p, s)
+              : launch_kernel<DT, CG, false, false, SPLIT, false>(units, mw, ma, p, s);
 }
 
 template <int DT>
@@ -640,8 +678,8 @@ cudaError_t launch_dt(const void *a, int64_t lda, const int32_t *offsets, int64_
     // singles 82.7 87.0 89.4 93.7 113 (87.1 89.9 91.5 101 106),
     // pairs   87.9 92.9 93.5 95.2 98.1 (91.9 95.2 95.1 97.0 98.6).
     if (rows >= 64 * (int64_t)E)
-        return launch_cg<DT, 2, false>(a, lda, offsets, rows, w, E, N, K, kn, out, ldo, out_f32, 256, 1,
-                                       status, s);
+        return launch_cg<DT, 2, false>(a, lda, offsets, rows, w, E, N, K, kn, out, ldo, out_f32,
+                                       out_f32 && num_kb > kPartStages ? PARTS_CAP : 256, 1, status, s);
     return launch_cg<DT, 1, false>(a, lda, offsets, rows, w, E, N, K, kn, out, ldo, out_f32, 64, 1, status, s);
 }
 

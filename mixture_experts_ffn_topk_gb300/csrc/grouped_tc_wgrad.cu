@@ -27,8 +27,9 @@
 // sums meet through distributed shared memory, each CTA adding its share of
 // the columns in rank order.
 // FP32 gradients are summed in parts of kPartStages stages, each in the next
-// accumulator; the epilogue adds a later part to what the earlier ones left, in
-// grad_w (which L2 holds meanwhile) or, SPLIT, in shared memory.
+// accumulator; the epilogue adds them in registers (pairs, units of 128
+// columns), in shared memory (SPLIT) or, on single CTAs, where few experts
+// have that many rows, in grad_w, which L2 holds meanwhile.
 // Units run over (expert, tile of the wider matrix, tile of the narrower one),
 // the last fastest: the narrower operand's segment stays in L2 while the wider
 // one passes once.
@@ -47,22 +48,26 @@ namespace moe {
 namespace {
 
 constexpr int BM = 128;                  // rows of grad_w per CTA
-// columns of grad_w per unit; half as many where sums are joined, which leaves
-// the ring's last 64 KiB to them
-template <bool SPLIT>
-constexpr int BN = SPLIT ? 128 : 256;
 constexpr int BK = 64;                   // rows reduced per stage
 constexpr int UK = 16;                   // rows reduced per tcgen05.mma
 constexpr int BOX_BYTES = 64 * BK * 2;   // 64 columns x 64 rows
 constexpr int G_BYTES = 2 * BOX_BYTES;
-template <int CG, bool SPLIT>
-constexpr int SLOT_BYTES = G_BYTES + BN<SPLIT> / 64 / CG * BOX_BYTES;
-template <int CG>
-constexpr int STAGES = CG == 2 ? 6 : 4;
+// Columns of grad_w per unit; half as many for FP32 sums of parts that are
+// added in registers (pairs) or shared memory (SPLIT).
+template <bool HALF>
+constexpr int BN = HALF ? 128 : 256;
+template <int CG, bool HALF>
+constexpr int SLOT_BYTES = G_BYTES + BN<HALF> / 64 / CG * BOX_BYTES;
 constexpr int RING_BYTES = 192 << 10;
-constexpr int PARTIAL_AT = STAGES<1> * SLOT_BYTES<1, true>;       // SPLIT: the sums, [column][row]
-static_assert(STAGES<1> * SLOT_BYTES<1, false> <= RING_BYTES && STAGES<2> * SLOT_BYTES<2, false> <= RING_BYTES &&
-              PARTIAL_AT + BN<true> * BM * 4 <= RING_BYTES, "the ring");
+template <int CG, bool HALF>
+constexpr int STAGES = CG == 2 ? (HALF ? 8 : 6) : 4;
+template <bool HALF>
+constexpr int PARTIAL_AT = HALF ? STAGES<1, true> * SLOT_BYTES<1, true> : 0;  // SPLIT: the sums, [column][row]
+static_assert(STAGES<1, false> * SLOT_BYTES<1, false> <= RING_BYTES &&
+              STAGES<2, false> * SLOT_BYTES<2, false> <= RING_BYTES &&
+              STAGES<2, true> * SLOT_BYTES<2, true> <= RING_BYTES &&
+              PARTIAL_AT<true> + BN<true> * BM * 4 <= RING_BYTES && BN<false> * BM * 4 <= RING_BYTES, "the ring");
+constexpr int MAX_STAGES = 8;
 constexpr int ACC_COLS = 256;
 constexpr int TMEM_COLS = 2 * ACC_COLS;
 constexpr int THREADS = 256;
@@ -70,14 +75,13 @@ constexpr int STG_ROW_BYTES = 64;        // staged bytes per row of grad_w
 constexpr int STG_BYTES = 32 * STG_ROW_BYTES;
 constexpr uint64_t kDrainLimitNs = 100000000ull;
 
-template <int CG>
 struct __align__(1024) Smem {
     uint8_t ring[RING_BYTES];
     uint8_t stg[4][2][STG_BYTES];
-    uint64_t full[STAGES<CG>];
-    uint64_t empty[STAGES<CG>];
-    uint64_t tail_in[STAGES<CG>];        // this CTA's copies of a stage with foreign rows
-    uint64_t tail_out[STAGES<CG>];       // (leader) the rows of both CTAs are zeroed
+    uint64_t full[MAX_STAGES];
+    uint64_t empty[MAX_STAGES];
+    uint64_t tail_in[MAX_STAGES];        // this CTA's copies of a stage with foreign rows
+    uint64_t tail_out[MAX_STAGES];       // (leader) the rows of both CTAs are zeroed
     uint64_t acc_full[2];
     uint64_t acc_empty[2];
     uint64_t drain;
@@ -86,9 +90,8 @@ struct __align__(1024) Smem {
     int warp_sum[THREADS / 32];
     Segments seg;
 };
-template <int CG>
-constexpr size_t kSmemBytes = sizeof(Smem<CG>) + 1024;   // + alignment slack
-static_assert(kSmemBytes<1> <= 232448 && kSmemBytes<2> <= 232448, "one CTA's shared memory");
+constexpr size_t kSmemBytes = sizeof(Smem) + 1024;       // + alignment slack
+static_assert(kSmemBytes <= 232448, "one CTA's shared memory");
 
 struct WgradParams {
     const int32_t *offsets;
@@ -115,7 +118,7 @@ struct Unit {
 
 // Walks a CTA's units, first and then every step-th, as (expert, outer tile,
 // inner tile) without dividing between units.
-template <int CG, bool SPLIT>
+template <int CG, bool SPLIT, bool HALF>
 struct UnitWalk {
     const Segments &S;
     const WgradParams &p;
@@ -156,10 +159,10 @@ struct UnitWalk {
         u.nkb = (u.cnt + BK - 1) / BK;
         u.tail = u.cnt - (u.nkb - 1) * BK;
         u.n0 = (nt * CG + rank) * BM;
-        u.k0 = kt * BN<SPLIT>;
+        u.k0 = kt * BN<HALF>;
         // whole 64-column boxes for each CTA: an MN-major operand's 128-byte rows
         const int left = p.K - u.k0;
-        u.mma_n = left >= BN<SPLIT> ? BN<SPLIT> : (left + 64 * CG - 1) / (64 * CG) * (64 * CG);
+        u.mma_n = left >= BN<HALF> ? BN<HALF> : (left + 64 * CG - 1) / (64 * CG) * (64 * CG);
         e += de;
         outer += douter;
         inner += dinner;
@@ -174,9 +177,10 @@ __global__ void __launch_bounds__(THREADS, 1)
 grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_a,
                      const __grid_constant__ CUtensorMap map_out, const WgradParams p)
 {
-    constexpr int NS = STAGES<CG>;
+    constexpr bool HALF = OUT_F32 && (SPLIT || CG == 2), PARTS = OUT_F32 && CG == 2;
+    constexpr int NS = STAGES<CG, HALF>;
     extern __shared__ uint8_t smem_raw[];
-    Smem<CG> &S = *reinterpret_cast<Smem<CG> *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    Smem &S = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int rank = CG == 2 ? (int)cluster_ctarank() : 0;
     const bool leader = rank == 0;
@@ -214,7 +218,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
     const uint32_t tmem_base = S.tmem_base;
     const int total = p.E * p.n_tiles * p.k_tiles;
     volatile int *abort_flag = &S.abort;
-    UnitWalk<CG, SPLIT> walk(S.seg, p, rank, unit0, unit_step);
+    UnitWalk<CG, SPLIT, HALF> walk(S.seg, p, rank, unit0, unit_step);
 
     // A producer's loop: loads(dst, bar, u, row) issues its copies of one
     // stage; with ARM it also expects both producers' bytes.
@@ -248,7 +252,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
                     bar = CG == 2 ? mapa_shared(here, 0) : here;
                     if (ARM && leader) expect_tx_on(on, &S.full[stage], CG * bytes);
                 }
-                loads(ring + stage * SLOT_BYTES<CG, SPLIT>, bar, u, u.row0 + kb * BK);
+                loads(ring + stage * SLOT_BYTES<CG, HALF>, bar, u, u.row0 + kb * BK);
                 if (++stage == NS) { stage = 0; phase ^= 1u; }
             }
         }
@@ -266,7 +270,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
         produce(on, std::false_type{}, [&](uint32_t dst, uint32_t bar, const Unit &u, int row) {
             const int mine = u.mma_n / CG, col0 = u.k0 + rank * mine;     // columns this CTA loads
 #pragma unroll
-            for (int j = 0; j < BN<SPLIT> / 64 / CG; ++j)
+            for (int j = 0; j < BN<HALF> / 64 / CG; ++j)
                 load_2d_on<CG>(j * 64 < mine ? on : 0u, dst + G_BYTES + j * BOX_BYTES, &map_a, bar, col0 + j * 64, row);
         });
     } else if (warp == 1 && leader) {
@@ -300,7 +304,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
                         tails ^= 1u << stage;
                     }
                     tc_fence_after();
-                    const uint32_t g = ring + stage * SLOT_BYTES<CG, SPLIT>, a = g + G_BYTES;
+                    const uint32_t g = ring + stage * SLOT_BYTES<CG, HALF>, a = g + G_BYTES;
                     auto mma = [&](int k) {
                         umma_on<CG>(on, d, sdesc_mn_sw128(g + k * UK * 128, BOX_BYTES),
                                     sdesc_mn_sw128(a + k * UK * 128, BOX_BYTES), idesc, (kb - kb0) | k ? 1u : 0u);
@@ -344,7 +348,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
                 const int boxes = 2 + u.mma_n / CG / 64;
                 for (int i = lane; i < boxes * nrows * 8; i += 32) {
                     const int box = i / (nrows * 8), c = i - box * (nrows * 8);
-                    *reinterpret_cast<uint4 *>(S.ring + stage * SLOT_BYTES<CG, SPLIT> + box * BOX_BYTES + u.tail * 128 + c * 16) =
+                    *reinterpret_cast<uint4 *>(S.ring + stage * SLOT_BYTES<CG, HALF> + box * BOX_BYTES + u.tail * 128 + c * 16) =
                         make_uint4(0u, 0u, 0u, 0u);
                 }
                 // the MMA reads shared memory through the async proxy
@@ -365,6 +369,17 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
         const uint32_t on = elect_lane();
         int it = 0, buf = 0, unit = unit0, kb0 = 0;
         Unit u = {};
+        // an accumulator is read: the next part but one may have it
+        auto release = [&](int acc) {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (CG == 2 && !leader) mbar_arrive_cluster(mapa_shared(smem_u32(&S.acc_empty[acc]), 0));
+                else mbar_arrive(&S.acc_empty[acc]);
+            }
+        };
+        float sums[PARTS ? 4 : 1][32];         // PARTS: of this lane's row
+        (void)sums;
         // unit by unit, part by part (kb0: the part's first block of rows)
         for (; unit < total; ++it, kb0 += p.part_kb) {
             if (kb0 != 0 && kb0 >= u.nkb) {
@@ -382,10 +397,10 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
             const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
             const int row0 = u.n0 + q * 32;            // this warp's first row of grad_w[e]
             const bool empty = u.cnt == 0;
-            int width = p.K - u.k0 < BN<SPLIT> ? p.K - u.k0 : BN<SPLIT>;
+            int width = p.K - u.k0 < BN<HALF> ? p.K - u.k0 : BN<HALF>;
             if constexpr (SPLIT) {
                 // the partial sums stay here, [column][row] in FP32
-                float *mine = reinterpret_cast<float *>(S.ring + PARTIAL_AT) + q * 32 + lane;
+                float *mine = reinterpret_cast<float *>(S.ring + PARTIAL_AT<HALF>) + q * 32 + lane;
                 for (int c0 = 0; c0 < width; c0 += 32) {
                     uint32_t v[32];
                     tmem_ld32(tbase + c0, v);
@@ -399,21 +414,9 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
                 width = 0;
             }
             if (row0 >= p.N || (empty && p.accumulate)) width = 0;
-            if (more && width > 0) {
-                // the earlier part's stores are complete before they are read
-                if (on) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-                __syncwarp();
-                asm volatile("fence.proxy.async.global;" ::: "memory");
-            }
-            for (int c0 = 0; c0 < width; c0 += 32) {
-                uint32_t v[32];
-                tmem_ld32(tbase + c0, v);
-                tmem_ld_wait(v);
-                if (empty) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = 0u;
-                }
-                if ((p.accumulate || more) && row0 + lane < p.N) {
+            // adds what grad_w holds to 32 columns from c0 on (`add`) and stores them
+            auto emit = [&](uint32_t (&v)[32], int c0, bool add) {
+                if (add && row0 + lane < p.N) {
                     const int64_t col_byte = (int64_t)(u.k0 + c0) * ESZ;
                     const uint8_t *old = p.out + ((int64_t)u.e * p.N + row0 + lane) * p.out_row_bytes + col_byte;
 #pragma unroll
@@ -470,12 +473,49 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     }
                 }
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) {
-                if (CG == 2 && !leader) mbar_arrive_cluster(mapa_shared(smem_u32(&S.acc_empty[acc]), 0));
-                else mbar_arrive(&S.acc_empty[acc]);
+            };
+            if constexpr (PARTS) {
+#pragma unroll
+                for (int b = 0; b < 8; ++b) {
+                    if (b * 16 >= width) continue;
+                    uint32_t v[16];
+                    tmem_ld16(tbase + b * 16, v);
+                    tmem_ld_wait16(v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float x = empty ? 0.0f : __uint_as_float(v[i]);
+                        float &sum = sums[b / 2][b % 2 * 16 + i];
+                        sum = more ? sum + x : x;
+                    }
+                }
+                release(acc);
+                if (u.nkb - kb0 > p.part_kb) continue;
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                    if (b * 32 >= width) continue;
+                    uint32_t v[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sums[b][i]);
+                    emit(v, b * 32, p.accumulate);
+                }
+            } else {
+                if (more && width > 0) {
+                    // the earlier part's stores are complete before they are read
+                    if (on) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+                    __syncwarp();
+                    asm volatile("fence.proxy.async.global;" ::: "memory");
+                }
+                for (int c0 = 0; c0 < width; c0 += 32) {
+                    uint32_t v[32];
+                    tmem_ld32(tbase + c0, v);
+                    tmem_ld_wait(v);
+                    if (empty) {
+    #pragma unroll
+                        for (int i = 0; i < 32; ++i) v[i] = 0u;
+                    }
+                    emit(v, c0, p.accumulate || more);
+                }
+                release(acc);
             }
         }
         // the stores have read their buffers and written what they carried
@@ -490,9 +530,9 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
         cluster_sync();
         if (unit0 < total) {
             const int slice = (int)cluster_ctarank();
-            const Unit u = UnitWalk<CG, SPLIT>(S.seg, p, rank, unit0, unit_step).next();
-            const int width = p.K - u.k0 < BN<SPLIT> ? p.K - u.k0 : BN<SPLIT>;
-            const uint32_t partial = smem_u32(S.ring + PARTIAL_AT);
+            const Unit u = UnitWalk<CG, SPLIT, HALF>(S.seg, p, rank, unit0, unit_step).next();
+            const int width = p.K - u.k0 < BN<HALF> ? p.K - u.k0 : BN<HALF>;
+            const uint32_t partial = smem_u32(S.ring + PARTIAL_AT<HALF>);
             for (int i = threadIdx.x; !(u.idle && p.accumulate); i += THREADS) {
                 const int c = (i / BM * ways + slice) * 8, n = i % BM;
                 if (c >= width) break;
@@ -574,11 +614,12 @@ cudaError_t launch_kernel(const CUtensorMap &mg, const CUtensorMap &ma, const CU
     auto kernel = grouped_wgrad_kernel<DT, CG, OUT_F32, SPLIT>;
     const int ways = SPLIT ? p.split : CG;
     p.n_tiles = (p.N + BM * CG - 1) / (BM * CG);
-    p.k_tiles = (p.K + BN<SPLIT> - 1) / BN<SPLIT>;
+    constexpr int COLS = BN<(OUT_F32 && (SPLIT || CG == 2))>;
+    p.k_tiles = (p.K + COLS - 1) / COLS;
     p.n_fast = p.N <= p.K;
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(THREADS);
-    cfg.dynamicSmemBytes = kSmemBytes<CG>;
+    cfg.dynamicSmemBytes = kSmemBytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -594,7 +635,7 @@ cudaError_t launch_kernel(const CUtensorMap &mg, const CUtensorMap &ma, const CU
     const bool cached = dev >= 0 && dev < kCachedDevices;
     int ctas = cached ? cache[dev].load() : 0;
     if (ctas == 0) {
-        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes<CG>);
+        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
         if (err != cudaSuccess) return err;
         ctas = device_sm_count();
         if (CG == 2) {
@@ -642,7 +683,8 @@ cudaError_t launch_dt(const void *grad, int64_t ldg, const void *a, int64_t lda,
     p.wait_ns = wait_limit_ns() + 1000ull * (uint64_t)((rows + BK - 1) / BK);
     // Few units: split an expert's rows over as many CTAs, 2 to 8, as the GPU has
     // room for and as leave each four blocks of rows on average.
-    const int64_t units = (int64_t)E * ((N + BM - 1) / BM) * ((K + BN<true> - 1) / BN<true>);
+    const int cols = out_f32 ? BN<true> : BN<false>;
+    const int64_t units = (int64_t)E * ((N + BM - 1) / BM) * ((K + cols - 1) / cols);
     const int64_t blocks = rows / E / BK, sms = device_sm_count();
     p.split = 1;
     while (p.split < 8 && units * p.split * 2 <= sms && blocks >= p.split * 2 * 4) p.split *= 2;
