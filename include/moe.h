@@ -680,7 +680,9 @@ typedef enum moe_weight_layout {
  *        dense, read only.
  *   out  [rows, N] in out_dtype (dtype or MOE_F32), row stride ldo, written
  *        for the rows of every expert: out[r, n] = sum_k a[r, k] w[e][n, k]
- *        (or w[e][k, n]), accumulated in FP32, rounded once.
+ *        (or w[e][k, n]), accumulated in FP32, rounded once. With F32 out,
+ *        sums of BF16 / F16 products are formed in parts of 768 terms, so that
+ *        the tensor cores' truncating accumulator does not drift over long K.
  *   BF16 / F16 run on tcgen05 tensor cores, F32 in true FP32 on CUDA cores.
  *   0 <= rows <= 2^31 - 1024, 1 <= E <= 1024, 1 <= N, K <= 2^24, strides up to
  *   2^32 elements. K, lda and, with MOE_WEIGHT_KN, N take whole multiples of
@@ -700,8 +702,9 @@ int moe_grouped_gemm(const void *a, int64_t lda, const int32_t *offsets, int64_t
  *   a       [rows, K] in dtype, row stride lda, read only.
  *   grad_w  [E, N, K] in grad_dtype (dtype or MOE_F32), dense, written in
  *           full: grad_w[e][n, k] = sum over the expert's rows of
- *           grad[r, n] a[r, k], accumulated in FP32, rounded once; zeros for an
- *           expert without rows. With accumulate != 0 the sum is added, in
+ *           grad[r, n] a[r, k], accumulated in FP32 (F32 gradients in parts of
+ *           768 terms, as above), rounded once; zeros for an expert without
+ *           rows. With accumulate != 0 the sum is added, in
  *           FP32, to what grad_w holds and the result rounded once. A NaN in
  *           one expert's rows stays in that expert's gradient.
  *   For weights stored [E, K, N] the gradient is the same call with grad and a

@@ -14,7 +14,7 @@
 //
 // Per CTA (one per SM, 256 threads, persistent over the units):
 //   warps 0, 7 TMA producers: 128 columns of grad (16 KiB), 256 / CG of a;
-//   warp 1     tcgen05.mma issuer, M = 128 * CG by N = up to 256;
+//   warp 1     tcgen05.mma issuer, M = 128 * CG by N up to 256;
 //   warps 2-5  epilogue: 32 rows x 64 bytes at a time into a swizzled staging
 //              buffer that a TMA store carries off, two buffers per warp, so
 //              that the warp only reads tensor memory and fills buffers; the
@@ -23,8 +23,8 @@
 // CTA pairs (CG = 2): M = 256, each CTA holds 128 columns of grad and half of
 // a's; the even CTA issues the MMAs.
 // Few units (narrow matrices) and long segments: a cluster of 2, 4 or 8 single
-// CTAs shares each unit's rows (SPLIT, units of 128 columns); the FP32 partial
-// sums meet through distributed shared memory, each CTA adding its share of
+// CTAs shares each unit's rows (SPLIT; FP32 gradients in units of 128 columns);
+// the FP32 partial sums meet through distributed shared memory, each CTA adding its share of
 // the columns in rank order.
 // FP32 gradients are summed in parts of kPartStages stages, each in the next
 // accumulator; the epilogue adds them in registers (pairs, units of 128
