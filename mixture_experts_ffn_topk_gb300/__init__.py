@@ -787,33 +787,34 @@ def moe_experts_backward(x_disp: torch.Tensor, offsets: torch.Tensor, gate: torc
 # attribute reads and integer comparisons: 5 to 9 us of host time per call.
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 
 
-def _enqueue(name: str, dev: torch.device, stream, *args):
-    """Calls the C entry point with ``dev`` current and its stream last."""
+def _enqueue(name: str, index: int, stream, *args):
+    """Calls the C entry point with CUDA device ``index`` current and its stream last."""
     fn = getattr(_lib or load_library(), name)
-    if stream is not None and isinstance(stream, torch.cuda.Stream) and stream.device != dev:
-        raise ValueError(f"the stream belongs to {stream.device}, the tensors to {dev}")
-    index = dev.index
-    if index == torch.cuda.current_device():
+    if stream is not None and isinstance(stream, torch.cuda.Stream) and stream.device.index != index:
+        raise ValueError(f"the stream belongs to {stream.device}, the tensors to cuda:{index}")
+    if index == _current_device():
         rc = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
     else:
-        with torch.cuda.device(dev):
+        with torch.cuda.device(index):
             rc = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
     if rc != 0:
         _check(rc, name)
 
 
-def _cuda(t: torch.Tensor) -> torch.device:
+def _cuda(t: torch.Tensor) -> int:
+    """The index of the tensor's CUDA device."""
     if not t.is_cuda:
         raise ValueError("tensors passed to the C ABI must live on a CUDA device")
-    return t.device
+    return t.get_device()
 
 
-def _ld(name: str, t: torch.Tensor, rows: int, cols: int, dtype, dev) -> int:
+def _ld(name: str, t: torch.Tensor, rows: int, cols: int, dtype, index: int) -> int:
     """Checks a matrix of dispatched rows; returns its row stride."""
-    if t.dim() != 2 or t.size(0) != rows or t.size(1) != cols or t.dtype != dtype or t.device != dev:
-        raise ValueError(f"{name} must be {dtype} of shape {(rows, cols)} on {dev}, not "
+    if t.shape != (rows, cols) or t.dtype is not dtype or not t.is_cuda or t.get_device() != index:
+        raise ValueError(f"{name} must be {dtype} of shape {(rows, cols)} on cuda:{index}, not "
                          f"{t.dtype} {tuple(t.shape)} on {t.device}")
     ld, unit = t.stride()
     if unit != 1 and cols > 1 and rows > 0:
@@ -821,12 +822,12 @@ def _ld(name: str, t: torch.Tensor, rows: int, cols: int, dtype, dev) -> int:
     return ld if rows > 1 else cols
 
 
-def _experts(offsets: torch.Tensor, dev) -> int:
+def _experts(offsets: torch.Tensor, index: int) -> int:
     """Checks expert offsets; returns the number of experts."""
     n = offsets.numel()
-    if (offsets.dtype != torch.int32 or offsets.dim() != 1 or n < 2 or offsets.device != dev or
-            not offsets.is_contiguous()):
-        raise ValueError(f"offsets must be contiguous int32 of shape [E + 1] on {dev}")
+    if (offsets.dtype is not torch.int32 or offsets.dim() != 1 or n < 2 or not offsets.is_cuda or
+            offsets.get_device() != index or not offsets.is_contiguous()):
+        raise ValueError(f"offsets must be contiguous int32 of shape [E + 1] on cuda:{index}")
     return n - 1
 
 
@@ -841,8 +842,8 @@ def moe_grouped_gemm(a: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
     dev, dt = _cuda(a), a.dtype
     rows, K = a.shape
     E = _experts(offsets, dev)
-    if w.dim() != 3 or w.dtype != dt or w.device != dev or not w.is_contiguous():
-        raise ValueError(f"w must be a contiguous {dt} tensor of three dimensions on {dev}")
+    if w.dim() != 3 or w.dtype is not dt or not w.is_cuda or w.get_device() != dev or not w.is_contiguous():
+        raise ValueError(f"w must be a contiguous {dt} tensor of three dimensions on cuda:{dev}")
     e, N, k = w.shape
     if transposed:
         N, k = k, N
@@ -851,7 +852,7 @@ def moe_grouped_gemm(a: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
                          f"K = {K}, not {tuple(w.shape)}")
     lda = _ld("a", a, rows, K, dt, dev)
     if out is None:
-        out = torch.empty((rows, N), dtype=out_dtype or dt, device=dev)
+        out = torch.empty((rows, N), dtype=out_dtype or dt, device=a.device)
         ldo = N
     else:
         ldo = _ld("out", out, rows, N, out_dtype or out.dtype, dev)
@@ -878,10 +879,11 @@ def moe_grouped_gemm_weight_grad(grad: torch.Tensor, a: torch.Tensor, offsets: t
     if grad_w is None:
         if accumulate:
             raise ValueError("accumulate needs the grad_w to add to")
-        grad_w = torch.empty((E, N, K), dtype=grad_dtype or torch.float32, device=dev)
-    elif (grad_w.shape != (E, N, K) or grad_w.device != dev or not grad_w.is_contiguous() or
+        grad_w = torch.empty((E, N, K), dtype=grad_dtype or torch.float32, device=grad.device)
+    elif (grad_w.shape != (E, N, K) or not grad_w.is_cuda or grad_w.get_device() != dev or
+          not grad_w.is_contiguous() or
           (grad_dtype is not None and grad_w.dtype != grad_dtype)):
-        raise ValueError(f"grad_w must be contiguous, of shape {(E, N, K)}, on {dev} and in grad_dtype")
+        raise ValueError(f"grad_w must be contiguous, of shape {(E, N, K)}, on cuda:{dev} and in grad_dtype")
     _enqueue("moe_grouped_gemm_weight_grad", dev, stream, grad.data_ptr(), ldg, a.data_ptr(), lda,
              offsets.data_ptr(), rows, E, N, K, _code(dt), grad_w.data_ptr(), _code(grad_w.dtype),
              int(bool(accumulate)))
@@ -924,8 +926,8 @@ def swiglu_checkpoint_views(ckpt: torch.Tensor, rows: int, I: int) -> dict:
 
 def _checkpoint(ckpt: torch.Tensor, dev) -> int:
     """Checks a checkpoint buffer (its size is the C entry point's to check); returns its bytes."""
-    if ckpt.device != dev or not ckpt.is_contiguous():
-        raise ValueError(f"ckpt must be contiguous on {dev}")
+    if not ckpt.is_cuda or ckpt.get_device() != dev or not ckpt.is_contiguous():
+        raise ValueError(f"ckpt must be contiguous on cuda:{dev}")
     return ckpt.numel() * ckpt.element_size()
 
 
@@ -943,11 +945,11 @@ def moe_swiglu_checkpoint(g: torch.Tensor, u: torch.Tensor, offsets=None, h=None
     if _ld("u", u, rows, I, dt, dev) != ld:
         raise ValueError("g and u must have the same row stride")
     if h is None:
-        h, ldh = torch.empty((rows, I), dtype=dt, device=dev), I
+        h, ldh = torch.empty((rows, I), dtype=dt, device=g.device), I
     else:
         ldh = _ld("h", h, rows, I, dt, dev)
     if ckpt is None:
-        ckpt = torch.empty(_checkpoint_planes(rows, I)[5], dtype=torch.uint8, device=dev)
+        ckpt = torch.empty(_checkpoint_planes(rows, I)[5], dtype=torch.uint8, device=g.device)
     _enqueue("moe_swiglu_checkpoint", dev, stream, g.data_ptr(), u.data_ptr(), ld,
              None if offsets is None else offsets.data_ptr(), E, rows, I, _code(dt), h.data_ptr(),
              ldh, ckpt.data_ptr(), _checkpoint(ckpt, dev))
@@ -966,7 +968,7 @@ def moe_swiglu_checkpoint_backward(grad_h: torch.Tensor, ckpt: torch.Tensor, off
     E = 0 if offsets is None else _experts(offsets, dev)
     ld = _ld("grad_h", grad_h, rows, I, dt, dev)
     if grad_g is None and grad_u is None:
-        both = torch.empty((rows, 2 * I), dtype=dt, device=dev)
+        both = torch.empty((rows, 2 * I), dtype=dt, device=grad_h.device)
         grad_g, grad_u, ldg = both[:, :I], both[:, I:], 2 * I
     elif grad_g is None or grad_u is None:
         raise ValueError("give both grad_g and grad_u, or neither")
@@ -978,7 +980,7 @@ def moe_swiglu_checkpoint_backward(grad_h: torch.Tensor, ckpt: torch.Tensor, off
     if h is not None:
         ldh = _ld("h", h, rows, I, dt, dev)
     elif need_h:
-        h = torch.empty((rows, I), dtype=dt, device=dev)
+        h = torch.empty((rows, I), dtype=dt, device=grad_h.device)
     _enqueue("moe_swiglu_checkpoint_backward", dev, stream, grad_h.data_ptr(), ld, ckpt.data_ptr(),
              _checkpoint(ckpt, dev), None if offsets is None else offsets.data_ptr(), E, rows, I,
              _code(dt), grad_g.data_ptr(), grad_u.data_ptr(), ldg,
