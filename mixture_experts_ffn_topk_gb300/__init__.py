@@ -782,7 +782,8 @@ def moe_experts_backward(x_disp: torch.Tensor, offsets: torch.Tensor, gate: torc
 
 # ---- grouped products and the 8-bit SwiGLU checkpoint -----------------------
 # These calls run on the device of their tensors, whatever the current device
-# is; stream (default: that device's current stream) must belong to it. A call
+# is; stream (default: that device's current stream) must belong to it, and the
+# caller orders it after whatever made the inputs. A call
 # on a few rows lasts a few microseconds on the GPU, so the checks are kept to
 # attribute reads and integer comparisons: 5 to 9 us of host time per call.
 
@@ -802,6 +803,17 @@ def _enqueue(name: str, index: int, stream, *args):
             rc = fn(*args, _raw_stream(index) if stream is None else _stream(stream))
     if rc != 0:
         _check(rc, name)
+
+
+def _empty(shape, dtype, like: torch.Tensor, stream) -> torch.Tensor:
+    """An output on ``like``'s device, from the allocator's pool of the stream
+    that writes it: a block freed on another stream may still be in use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
 
 
 def _cuda(t: torch.Tensor) -> int:
@@ -852,7 +864,7 @@ def moe_grouped_gemm(a: torch.Tensor, offsets: torch.Tensor, w: torch.Tensor,
                          f"K = {K}, not {tuple(w.shape)}")
     lda = _ld("a", a, rows, K, dt, dev)
     if out is None:
-        out = torch.empty((rows, N), dtype=out_dtype or dt, device=a.device)
+        out = _empty((rows, N), out_dtype or dt, a, stream)
         ldo = N
     else:
         ldo = _ld("out", out, rows, N, out_dtype or out.dtype, dev)
@@ -879,7 +891,7 @@ def moe_grouped_gemm_weight_grad(grad: torch.Tensor, a: torch.Tensor, offsets: t
     if grad_w is None:
         if accumulate:
             raise ValueError("accumulate needs the grad_w to add to")
-        grad_w = torch.empty((E, N, K), dtype=grad_dtype or torch.float32, device=grad.device)
+        grad_w = _empty((E, N, K), grad_dtype or torch.float32, grad, stream)
     elif (grad_w.shape != (E, N, K) or not grad_w.is_cuda or grad_w.get_device() != dev or
           not grad_w.is_contiguous() or
           (grad_dtype is not None and grad_w.dtype != grad_dtype)):
@@ -945,11 +957,11 @@ def moe_swiglu_checkpoint(g: torch.Tensor, u: torch.Tensor, offsets=None, h=None
     if _ld("u", u, rows, I, dt, dev) != ld:
         raise ValueError("g and u must have the same row stride")
     if h is None:
-        h, ldh = torch.empty((rows, I), dtype=dt, device=g.device), I
+        h, ldh = _empty((rows, I), dt, g, stream), I
     else:
         ldh = _ld("h", h, rows, I, dt, dev)
     if ckpt is None:
-        ckpt = torch.empty(_checkpoint_planes(rows, I)[5], dtype=torch.uint8, device=g.device)
+        ckpt = _empty(_checkpoint_planes(rows, I)[5], torch.uint8, g, stream)
     _enqueue("moe_swiglu_checkpoint", dev, stream, g.data_ptr(), u.data_ptr(), ld,
              None if offsets is None else offsets.data_ptr(), E, rows, I, _code(dt), h.data_ptr(),
              ldh, ckpt.data_ptr(), _checkpoint(ckpt, dev))
@@ -968,7 +980,7 @@ def moe_swiglu_checkpoint_backward(grad_h: torch.Tensor, ckpt: torch.Tensor, off
     E = 0 if offsets is None else _experts(offsets, dev)
     ld = _ld("grad_h", grad_h, rows, I, dt, dev)
     if grad_g is None and grad_u is None:
-        both = torch.empty((rows, 2 * I), dtype=dt, device=grad_h.device)
+        both = _empty((rows, 2 * I), dt, grad_h, stream)
         grad_g, grad_u, ldg = both[:, :I], both[:, I:], 2 * I
     elif grad_g is None or grad_u is None:
         raise ValueError("give both grad_g and grad_u, or neither")
@@ -980,7 +992,7 @@ def moe_swiglu_checkpoint_backward(grad_h: torch.Tensor, ckpt: torch.Tensor, off
     if h is not None:
         ldh = _ld("h", h, rows, I, dt, dev)
     elif need_h:
-        h = torch.empty((rows, I), dtype=dt, device=grad_h.device)
+        h = _empty((rows, I), dt, grad_h, stream)
     _enqueue("moe_swiglu_checkpoint_backward", dev, stream, grad_h.data_ptr(), ld, ckpt.data_ptr(),
              _checkpoint(ckpt, dev), None if offsets is None else offsets.data_ptr(), E, rows, I,
              _code(dt), grad_g.data_ptr(), grad_u.data_ptr(), ldg,

@@ -479,6 +479,31 @@ def test_products_repeat_bit_for_bit_on_any_stream():
         assert all(torch.equal(x, y) for x, y in zip(got, want))
 
 
+def test_outputs_on_another_stream_take_that_streams_memory():
+    """A block that the current stream has freed but still works on is not handed to a call on another
+    stream: the output made there comes out right, and the pending work keeps its own values."""
+    g = gen(50)
+    rows, N, K = 4096, 2048, 256
+    off = offsets_of([rows])
+    a = torch.randn((rows, K), generator=g, device="cuda").to(BF16)
+    w = torch.randn((1, N, K), generator=g, device="cuda").to(BF16)
+    want = moe.moe_grouped_gemm(a, off, w)
+    total = torch.zeros((), dtype=torch.float64, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for handle in (side, side.cuda_stream):
+        busy = torch.ones((rows, N), dtype=BF16, device="cuda")
+        for _ in range(30):                               # pending work on `busy`
+            busy.mul_(1.0)
+        total.add_(busy.sum(dtype=torch.float64))
+        del busy                                          # free for the current stream's next tensor
+        out = moe.moe_grouped_gemm(a, off, w, stream=handle)
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+        del out
+    assert float(total) == 2.0 * rows * N
+
+
 def test_captured_and_replayed():
     """Offsets, rows and weights may change between replays; two graphs run side by side."""
     g = gen(12)
