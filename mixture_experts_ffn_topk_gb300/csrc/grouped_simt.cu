@@ -249,7 +249,8 @@ cudaError_t launch_sizes(const SimtOperand &x, const SimtOperand &y, const int32
                          int accumulate, unsigned *status, cudaStream_t s)
 {
     const int64_t height = WG ? M : rows / E;
-    if (height < kFlatTile)
+    const int64_t tiles = (WG ? (int64_t)E * ((M + 63) / 64) : rows / 64 + (rows < E ? rows : E)) * ((N + 127) / 128);
+    if (height < kFlatTile || tiles < device_sm_count())
         return launch_tile<WG, Y_MAJOR, 16, 128, 4, 4, 32, 4>(x, y, offsets, E, rows, M, N, K, out, ldo,
                                                               accumulate, status, s);
     if (N > 64)
