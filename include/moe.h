@@ -680,9 +680,11 @@ typedef enum moe_weight_layout {
  *        dense, read only.
  *   out  [rows, N] in out_dtype (dtype or MOE_F32), row stride ldo, written
  *        for the rows of every expert: out[r, n] = sum_k a[r, k] w[e][n, k]
- *        (or w[e][k, n]), accumulated in FP32, rounded once. With F32 out,
- *        sums of BF16 / F16 products are formed in parts of 768 terms, so that
- *        the tensor cores' truncating accumulator does not drift over long K.
+ *        (or w[e][k, n]), accumulated in FP32, rounded once. The tensor
+ *        cores' FP32 accumulator truncates, so sums of BF16 / F16 products are
+ *        formed in parts that FP32 additions join: of 768 terms with F32 out,
+ *        16384 with F16 out, 32768 with BF16 out. A part of positive terms, the
+ *        worst, comes out about 6.4e-9 of itself per term low.
  *   BF16 / F16 run on tcgen05 tensor cores, F32 in true FP32 on CUDA cores.
  *   0 <= rows <= 2^31 - 1024, 1 <= E <= 1024, 1 <= N, K <= 2^24, strides up to
  *   2^32 elements. K, lda and, with MOE_WEIGHT_KN, N take whole multiples of

@@ -11,13 +11,27 @@ namespace {
 constexpr int kGroupedMaxE = 1024;
 
 // The tensor cores add into their FP32 accumulator by truncation, so a long
-// reduction drifts towards zero: relative errors measured against 64 bits were
-// 3.5e-7 over 384 terms, 1.0e-6 over 1048, 3.2e-6 over 3000 and 7.8e-6 over
-// 7032, where FP32 sums in torch stay at 1e-7 to 8e-7. FP32 outputs are
-// therefore summed in parts of this many stages of 64, each in an accumulator
-// of its own, added up by ordinary FP32 additions. 16-bit outputs, whose
-// rounding is 2^-9 or 2^-12 of a value, take one accumulator.
+// reduction drifts towards zero. Normal operands of either sign: relative errors
+// against 64 bits of 3.5e-7 over 384 terms, 1.0e-6 over 1048, 3.2e-6 over 3000 and
+// 7.8e-6 over 7032, where FP32 sums in torch stay at 1e-7 to 8e-7. Positive terms,
+// the worst: 6.4e-9 of the sum per term, 3.3e-3 over 2^19. Sums are therefore formed in parts of so many stages of 64, each in
+// an accumulator of its own, added up by ordinary FP32 additions: FP32 outputs in
+// parts of 768 terms (positive ones 4.3e-6 low); 16-bit ones, rounded by half a
+// step (2^-12 to 2^-11 of an F16 value, 2^-9 to 2^-8 of a BF16 one), in parts of
+// 16384 and 32768, over which positive terms drift by 2^-13.2 and 2^-12.2. Parts of
+// 4096 cost F16 5 to 7 % over K = 7168 and 14336 (8 experts of 4096 rows, N = 4096:
+// 2.30 against 2.18 ms), where these are one part.
 constexpr int kPartStages = 12;
+template <int DT>
+constexpr int kLongPartStages = DT == DT_F16 ? 256 : 512;
+
+// sum[i] += v[i] of FP32 values held as their bits.
+template <int N>
+__device__ __forceinline__ void add_to(uint32_t (&sum)[N], const uint32_t (&v)[N])
+{
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum[i] = __float_as_uint(__uint_as_float(sum[i]) + __uint_as_float(v[i]));
+}
 
 // Expert e has rows [first[e], first[e] + count[e]) and the work units
 // [unit[e], unit[e + 1]).

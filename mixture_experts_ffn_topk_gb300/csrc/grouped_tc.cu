@@ -32,9 +32,12 @@
 // fastest, so that CTAs at work share a weight tile in L2; a block's rows are
 // held to what stays in L2 while all weight tiles pass.
 //
-// FP32 outputs are summed in parts of kPartStages stages, each in the next
-// accumulator; the epilogue adds them in registers (PARTS, units of 128 rows at
-// most) or, SPLIT, in shared memory.
+// Outputs are summed in parts, of kPartStages stages (FP32 outputs) or
+// kLongPartStages (16-bit ones), each in an accumulator of its own. The epilogue
+// adds the parts of FP32 outputs in registers (PARTS, units of 128 rows at most)
+// while the next one is summed, and, SPLIT, all parts in shared memory. Otherwise
+// (TOTAL) the total stays in the accumulator of the first part, and the later
+// ones, all in the other accumulator, wait until the part before is added.
 //
 // Every wait is bounded (wait_ns); on expiry the kernel records ST_TIMEOUT,
 // stops issuing work, drains its own copies and MMAs, frees TMEM and exits.
@@ -93,7 +96,7 @@ struct GemmParams {
     int slot_bytes;          // ring slot: W_BYTES + this CTA's rows of a full unit
     int stages;
     int split;               // SPLIT: CTAs that share a unit's k
-    int part_kb;             // k-blocks summed in one accumulator (see kPartStages)
+    int part_kb;             // k-blocks summed in one accumulator: kPartStages or kLongPartStages
     uint8_t *out;
     int64_t out_row_bytes;
     int vec;                 // rows of out start on 16 bytes
@@ -178,6 +181,15 @@ __device__ __forceinline__ bool epi_all(int id, bool ok)
     return r != 0;
 }
 
+// Accumulators take turns; where a sum's total stays in its first part's
+// accumulator (TOTAL), the later parts of that sum all have the other one.
+// more: the part adds to earlier ones; last: no other part follows.
+template <bool TOTAL>
+__device__ __forceinline__ int next_acc(int acc, bool more, bool last)
+{
+    return TOTAL && more && !last ? acc : acc ^ 1;
+}
+
 // 32 TMEM lanes x 8 consecutive fp32 columns.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
 {
@@ -228,6 +240,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     const bool leader = rank == 0;
     static_assert(!SPLIT || CG == 1, "a split unit runs on single CTAs");
     static_assert(!PARTS || (OUT_F32 && !SPLIT), "sums of parts in registers");
+    constexpr bool TOTAL = !OUT_F32 && !SPLIT;       // an FP32 sum of several parts is PARTS or SPLIT
     const int ways = SPLIT ? p.split : CG;           // CTAs per unit
     const int unit0 = (int)blockIdx.x / ways, unit_step = (int)gridDim.x / ways;
     // this CTA's k-blocks
@@ -324,17 +337,17 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         const uint32_t ring = smem_u32(S.ring);
         int stage = 0;
         uint32_t phase = 0;
-        int it = 0;
+        int acc = 0;
+        uint32_t used = 0;                               // parity of each accumulator's uses so far
         bool ok = true;
         for (int unit = unit0; unit < total && ok; unit += unit_step) {
             const Unit u = walk.at(unit);
             const uint32_t idesc = idesc0 | ((uint32_t)(u.mma_n >> 3) << 17);
-            for (int kb0 = kb_begin; kb0 < kb_end && ok; kb0 += p.part_kb, ++it) {
+            for (int kb0 = kb_begin; kb0 < kb_end && ok; kb0 += p.part_kb) {
                 const int kb1 = kb_end - kb0 < p.part_kb ? kb_end : kb0 + p.part_kb;
-                const int acc = it & 1;
-                const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
-                ok = warp_wait<CG>(&S.acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_ns);
+                ok = warp_wait<CG>(&S.acc_empty[acc], (used >> acc & 1u) ^ 1u, abort_flag, p.status, p.wait_ns);
                 if (!ok) break;
+                used ^= 1u << acc;
                 const uint32_t d = tmem_base + (uint32_t)(acc * ACC_COLS);
                 for (int kb = kb0; kb < kb1; ++kb) {
                     ok = warp_wait<CG>(&S.full[stage], phase, abort_flag, p.status, p.wait_ns);
@@ -349,6 +362,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     if (++stage == p.stages) { stage = 0; phase ^= 1u; }
                 }
                 if (ok) commit_on<CG>(on, &S.acc_full[acc]);
+                acc = next_acc<TOTAL>(acc, kb0 != kb_begin, kb1 == kb_end);
             }
         }
         // every MMA issued must finish before TMEM is released, also where
@@ -367,9 +381,10 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         constexpr int ESZ = OUT_F32 ? 4 : 2;
         constexpr int ROW_BYTES = BM * ESZ;              // staged bytes per row: 512 / 256
         constexpr int PIECES = ROW_BYTES / 16, PER_IT = 128 / PIECES;
-        int it = 0, buf = 0, unit = unit0, kb0 = kb_begin;
+        int next = 0, buf = 0, unit = unit0, kb0 = kb_begin;
+        uint32_t used = 0;
         Unit u = {};
-        // an accumulator is read: the next part but one may have it
+        // an accumulator is read: another part may have it
         auto release = [&](int acc) {
             tc_fence_before();
             __syncwarp();
@@ -381,20 +396,25 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         float sums[PARTS ? PARTS_CAP / 32 : 1][16];        // PARTS: of this lane's n and the group's rows
         (void)sums;
         // unit by unit, part by part (kb0: the part's first k-block)
-        for (; unit < total; ++it, kb0 += p.part_kb) {
+        for (; unit < total; kb0 += p.part_kb) {
             if (kb0 >= kb_end) {
                 kb0 = kb_begin;
                 unit += unit_step;
                 if (unit >= total) break;
             }
             if (kb0 == kb_begin) u = walk.at(unit);
-            const bool more = OUT_F32 && kb0 != kb_begin;     // adds to what the earlier parts left
-            const int acc = it & 1;
-            const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
+            const bool more = kb0 != kb_begin, last = kb_end - kb0 <= p.part_kb;  // adds to the earlier parts; ends the sum
+            const int acc = next;
+            const uint32_t acc_phase = used >> acc & 1u;
+            used ^= 1u << acc;
+            next = next_acc<TOTAL>(acc, more, last);
             // a group's warps leave together: none may wait at a barrier for
             // one that has given up
             if (!epi_all(1 + group, mbar_wait<CG>(&S.acc_full[acc], acc_phase, abort_flag, p.status, p.wait_ns))) break;
             tc_fence_after();
+            // (TOTAL) the accumulator that holds the sum of the earlier parts
+            const uint32_t ttotal = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)((acc ^ 1) * ACC_COLS);
+            (void)ttotal;
             const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
             const int piece = tid % PIECES, col = u.w0 + piece * (16 / ESZ);
             uint8_t *out0 = p.out + (int64_t)u.row0 * p.out_row_bytes + (int64_t)col * ESZ;
@@ -457,7 +477,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                         sums[j][i] = more ? sums[j][i] + __uint_as_float(v[i]) : __uint_as_float(v[i]);
                 }
                 release(acc);
-                if (kb_end - kb0 > p.part_kb) continue;
+                if (!last) continue;
 #pragma unroll
                 for (int j = 0; j < PARTS_CAP / 32; ++j) {
 #pragma unroll
@@ -467,6 +487,25 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     }
                 }
             } else {
+                if constexpr (TOTAL) {
+                    // a sum that goes on: the first part stays where it is, a
+                    // later one is added to it
+                    if (!last && !more) continue;
+                    if (!last) {
+                        for (int t0 = group * CH; t0 < u.rows; t0 += 2 * CH) {
+                            uint32_t v[16], sum[16];
+                            tmem_ld16(tbase + t0, v);
+                            tmem_ld16(ttotal + t0, sum);
+                            tmem_ld_wait16(v);
+                            tmem_ld_wait16(sum);
+                            add_to(sum, v);
+                            tmem_st16(ttotal + t0, sum);
+                        }
+                        tmem_st_wait();
+                        release(acc);
+                        continue;
+                    }
+                }
                 for (int t0 = group * CH; !SPLIT && t0 < u.rows; t0 += 2 * CH) {
                     if constexpr (OUT_F32) {
                         uint32_t v[8];
@@ -486,6 +525,15 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                         tmem_ld_blocks(tbase + (16u << 16) + t0, hi);
                         tmem_ld_wait8(lo);
                         tmem_ld_wait8(hi);
+                        if (TOTAL && more) {
+                            uint32_t sum[8];
+                            tmem_ld_blocks(ttotal + t0, sum);
+                            tmem_ld_wait8(sum);
+                            add_to(lo, sum);
+                            tmem_ld_blocks(ttotal + (16u << 16) + t0, sum);
+                            tmem_ld_wait8(sum);
+                            add_to(hi, sum);
+                        }
                         const int t = lane & 7, at = q * 4 + (lane >> 3);
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
@@ -500,6 +548,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     }
                 }
                 release(acc);
+                if (TOTAL && more) release(acc ^ 1);
             }
         }
     }
@@ -642,7 +691,7 @@ cudaError_t launch_cg(const void *a, int64_t lda, const int32_t *offsets, int64_
     p.out_row_bytes = ldo * (out_f32 ? 4 : 2);
     p.vec = p.out_row_bytes % 16 == 0;
     p.status = status;
-    p.part_kb = out_f32 ? kPartStages : (1 << 20);
+    p.part_kb = out_f32 ? kPartStages : kLongPartStages<DT>;
     // a wait may last one unit's whole reduction: a microsecond per stage on top
     p.wait_ns = wait_limit_ns() + 1000ull * (uint64_t)((K + BK - 1) / BK);
     // an upper bound: every expert adds at most one unit that is not full

@@ -1,0 +1,100 @@
+"""Long sums of the grouped products, against 64 bits at tolerances that do not
+grow with the length.
+
+The tensor cores' accumulator truncates: an instruction adds 16 products to the
+accumulator, 17 values that may each lose a step of the partial sum, 2^-23 of it
+at most. With positive terms of like size the partial sum after j of n
+instructions is within a tenth of j / n of the sum, so n instructions lose at
+most 17 * 0.55 n * 2^-23 of it. 16-bit outputs are summed in parts of 16384 (F16)
+or 32768 (BF16) terms, FP32 outputs in parts of 768, joined by FP32 additions of
+2^-24 each: the length of the sum itself enters by those alone.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+import mixture_experts_ffn_topk_gb300 as moe
+
+pytestmark = pytest.mark.gpu
+
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def ready():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from mixture_experts_ffn_topk_gb300 import build
+    build.build()
+    moe.moe_device_status(clear=True)
+    yield
+    torch.cuda.empty_cache()
+
+
+@pytest.fixture(autouse=True)
+def status_stays_clear():
+    yield
+    torch.cuda.synchronize()
+    assert moe.moe_device_status(clear=True) == 0
+
+
+def offsets_of(counts):
+    return torch.tensor(np.concatenate([[0], np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+
+
+def positive(shape, dtype, g, along=0, mean=0.03):
+    """Values between mean / 2 and 3 mean, drawn slab by slab: of like size but for a factor of 1 to 2
+    for each index of dimension `along`, so that sums over the others meet every place of a binade."""
+    out = torch.empty(shape, dtype=dtype, device="cuda")
+    view = [1] * len(shape)
+    view[along] = shape[along]
+    factor = (torch.rand(view, generator=g, device="cuda") + 1).expand((shape[0],) + tuple(view[1:]))
+    per = max(1, (1 << 27) // out[0].numel())
+    for s in range(0, shape[0], per):
+        v = torch.rand((min(per, shape[0] - s),) + tuple(shape[1:]), generator=g, device="cuda")
+        out[s:s + per] = (v + 0.5) * mean * factor[s:s + per]
+    return out
+
+
+def half_step(ref, dtype):
+    """Half a step of dtype at ref (positive, normal)."""
+    return torch.exp2(torch.floor(torch.log2(ref))) * (torch.finfo(dtype).eps / 2)
+
+
+def part_slack(n, dtype):
+    """Relative error of a sum of n positive terms, before its rounding (8: CTAs joined)."""
+    part = {F16: 16384, BF16: 32768, F32: 768}[dtype]
+    return (17 * 0.55 * min(n, part) / 16 + -(-n // part) + 8) * 2.0 ** -23
+
+
+def check_long_sum(got, ref, n, dtype, what):
+    slack = ref * part_slack(n, dtype)
+    over = (got.double() - ref).abs() - slack - half_step(ref + slack, dtype)
+    assert float(over.max()) <= 0, f"{what}: {float((got.double() / ref - 1).mean()):.2e} off on average"
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("counts,N,K", [([3], 40, 1 << 22),            # joined over a cluster
+                                        ([640], 1000, 1 << 19),        # pairs
+                                        ([40] * 16, 384, 1 << 19)],    # single CTAs
+                         ids=["joined", "pairs", "singles"])
+def test_16_bit_products_do_not_drift_over_long_k(dtype, counts, N, K):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    E, rows, off = len(counts), sum(counts), offsets_of(counts)
+    at = off.tolist()
+    a, w = positive((rows, K), dtype, g), positive((E, N, K), dtype, g, along=1)
+    refs = []
+    for e in range(E):
+        ref = torch.zeros((counts[e], N), dtype=torch.float64, device="cuda")
+        for k in range(0, K, 1 << 16):
+            ref += a[at[e]:at[e + 1], k:k + (1 << 16)].double() @ w[e, :, k:k + (1 << 16)].double().T
+        refs.append(ref)
+    ref = torch.cat(refs)
+    check_long_sum(moe.moe_grouped_gemm(a, off, w), ref, K, dtype, "[E, N, K]")
+    wt = torch.empty((E, K, N), dtype=dtype, device="cuda")
+    for e in range(E):
+        wt[e] = w[e].T
+    del w
+    check_long_sum(moe.moe_grouped_gemm(a, off, wt, transposed=True), ref, K, dtype, "[E, K, N]")
