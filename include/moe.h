@@ -704,8 +704,8 @@ int moe_grouped_gemm(const void *a, int64_t lda, const int32_t *offsets, int64_t
  *   a       [rows, K] in dtype, row stride lda, read only.
  *   grad_w  [E, N, K] in grad_dtype (dtype or MOE_F32), dense, written in
  *           full: grad_w[e][n, k] = sum over the expert's rows of
- *           grad[r, n] a[r, k], accumulated in FP32 (F32 gradients in parts of
- *           768 terms, as above), rounded once; zeros for an expert without
+ *           grad[r, n] a[r, k], accumulated in FP32 (BF16 and F16 rows in parts,
+ *           as above), rounded once; zeros for an expert without
  *           rows. With accumulate != 0 the sum is added, in
  *           FP32, to what grad_w holds and the result rounded once. A NaN in
  *           one expert's rows stays in that expert's gradient.

@@ -33,6 +33,15 @@ __device__ __forceinline__ void add_to(uint32_t (&sum)[N], const uint32_t (&v)[N
     for (int i = 0; i < N; ++i) sum[i] = __float_as_uint(__uint_as_float(sum[i]) + __uint_as_float(v[i]));
 }
 
+// Accumulators take turns; where a sum's total stays in its first part's
+// accumulator (TOTAL), the later parts of that sum all have the other one.
+// more: the part adds to earlier ones; last: no other part follows.
+template <bool TOTAL>
+__device__ __forceinline__ int next_acc(int acc, bool more, bool last)
+{
+    return TOTAL && more && !last ? acc : acc ^ 1;
+}
+
 // Expert e has rows [first[e], first[e] + count[e]) and the work units
 // [unit[e], unit[e + 1]).
 struct Segments {

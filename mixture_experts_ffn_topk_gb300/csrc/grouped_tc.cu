@@ -181,15 +181,6 @@ __device__ __forceinline__ bool epi_all(int id, bool ok)
     return r != 0;
 }
 
-// Accumulators take turns; where a sum's total stays in its first part's
-// accumulator (TOTAL), the later parts of that sum all have the other one.
-// more: the part adds to earlier ones; last: no other part follows.
-template <bool TOTAL>
-__device__ __forceinline__ int next_acc(int acc, bool more, bool last)
-{
-    return TOTAL && more && !last ? acc : acc ^ 1;
-}
-
 // 32 TMEM lanes x 8 consecutive fp32 columns.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
 {

@@ -29,7 +29,10 @@
 // FP32 gradients are summed in parts of kPartStages stages, each in the next
 // accumulator; the epilogue adds them in registers (pairs, units of 128
 // columns), in shared memory (SPLIT) or, on single CTAs, where few experts
-// have that many rows, in grad_w, which L2 holds meanwhile.
+// have that many rows, in grad_w, which L2 holds meanwhile. 16-bit ones are
+// summed in parts of kLongPartStages: the total stays in the first part's
+// accumulator (TOTAL), and the later parts, all in the other one, wait until the
+// part before is added.
 // Units run over (expert, tile of the wider matrix, tile of the narrower one),
 // the last fastest: the narrower operand's segment stays in L2 while the wider
 // one passes once.
@@ -99,7 +102,7 @@ struct WgradParams {
     int n_tiles, k_tiles;
     int n_fast;              // the n tile runs fastest (grad is the narrower operand)
     int split;               // SPLIT: CTAs that share a unit's rows
-    int part_kb;             // blocks of rows summed in one accumulator (see kPartStages)
+    int part_kb;             // blocks of rows summed in one accumulator: kPartStages or kLongPartStages
     uint8_t *out;            // read where the gradient is added to, written where split
     int64_t out_row_bytes;
     int accumulate;
@@ -177,7 +180,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_a,
                      const __grid_constant__ CUtensorMap map_out, const WgradParams p)
 {
-    constexpr bool HALF = OUT_F32 && (SPLIT || CG == 2), PARTS = OUT_F32 && CG == 2;
+    constexpr bool HALF = OUT_F32 && (SPLIT || CG == 2), PARTS = OUT_F32 && CG == 2, TOTAL = !OUT_F32;
     constexpr int NS = STAGES<CG, HALF>;
     extern __shared__ uint8_t smem_raw[];
     Smem &S = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -280,7 +283,8 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
         const uint32_t ring = smem_u32(S.ring);
         int stage = 0;
         uint32_t phase = 0, tails = 0;
-        int it = 0;
+        int acc = 0;
+        uint32_t used = 0;                         // parity of each accumulator's uses so far
         bool ok = true;
         for (int unit = unit0; unit < total && ok; unit += unit_step) {
             const Unit u = walk.next();
@@ -289,10 +293,9 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
             int kb0 = 0;
             do {
                 const int kb1 = u.nkb - kb0 < p.part_kb ? u.nkb : kb0 + p.part_kb;
-                const int acc = it & 1;
-                const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
-                ok = warp_wait<CG>(&S.acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_ns);
+                ok = warp_wait<CG>(&S.acc_empty[acc], (used >> acc & 1u) ^ 1u, abort_flag, p.status, p.wait_ns);
                 if (!ok) break;
+                used ^= 1u << acc;
                 const uint32_t d = tmem_base + (uint32_t)(acc * ACC_COLS);
                 for (int kb = kb0; kb < kb1; ++kb) {
                     ok = warp_wait<CG>(&S.full[stage], phase, abort_flag, p.status, p.wait_ns);
@@ -320,7 +323,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
                 }
                 if (!ok) break;
                 commit_on<CG>(on, &S.acc_full[acc]);
-                ++it;
+                acc = next_acc<TOTAL>(acc, kb0 != 0, kb1 == u.nkb);
                 kb0 = kb1;
             } while (kb0 < u.nkb);
         }
@@ -367,9 +370,10 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
         constexpr int ESZ = OUT_F32 ? 4 : 2;
         constexpr int COLS = STG_ROW_BYTES / ESZ;  // columns per staging buffer: 16 / 32
         const uint32_t on = elect_lane();
-        int it = 0, buf = 0, unit = unit0, kb0 = 0;
+        int next = 0, buf = 0, unit = unit0, kb0 = 0;
+        uint32_t used = 0;
         Unit u = {};
-        // an accumulator is read: the next part but one may have it
+        // an accumulator is read: another part may have it
         auto release = [&](int acc) {
             tc_fence_before();
             __syncwarp();
@@ -381,34 +385,69 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
         float sums[PARTS ? 4 : 1][32];         // PARTS: of this lane's row
         (void)sums;
         // unit by unit, part by part (kb0: the part's first block of rows)
-        for (; unit < total; ++it, kb0 += p.part_kb) {
+        for (; unit < total; kb0 += p.part_kb) {
             if (kb0 != 0 && kb0 >= u.nkb) {
                 kb0 = 0;
                 unit += unit_step;
                 if (unit >= total) break;
             }
             if (kb0 == 0) u = walk.next();
-            const bool more = kb0 != 0;                // adds to what the earlier parts left
-            const int acc = it & 1;
-            const uint32_t acc_phase = (uint32_t)(it >> 1) & 1u;
+            const bool more = kb0 != 0, last = u.nkb - kb0 <= p.part_kb;      // adds to the earlier parts; ends the sum
+            const int acc = next;
+            const uint32_t acc_phase = used >> acc & 1u;
+            used ^= 1u << acc;
+            next = next_acc<TOTAL>(acc, more, last);
             const bool ready = mbar_wait<CG>(&S.acc_full[acc], acc_phase, abort_flag, p.status, p.wait_ns);
             if (!__all_sync(0xffffffffu, ready)) break;
             tc_fence_after();
             const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
+            // (TOTAL) the accumulator that holds the sum of the earlier parts
+            const uint32_t ttotal = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)((acc ^ 1) * ACC_COLS);
+            (void)ttotal;
             const int row0 = u.n0 + q * 32;            // this warp's first row of grad_w[e]
             const bool empty = u.cnt == 0;
             int width = p.K - u.k0 < BN<HALF> ? p.K - u.k0 : BN<HALF>;
+            if constexpr (TOTAL) {
+                // a sum that goes on: the first part stays where it is, a
+                // later one is added to it
+                if (!last) {
+                    if (!more) continue;
+                    for (int c0 = 0; c0 < width; c0 += 32) {
+                        uint32_t v[32], sum[32];
+                        tmem_ld32(tbase + c0, v);
+                        tmem_ld32(ttotal + c0, sum);
+                        tmem_ld_wait(v);
+                        tmem_ld_wait(sum);
+                        add_to(sum, v);
+                        tmem_st32(ttotal + c0, sum);
+                    }
+                    tmem_st_wait();
+                    release(acc);
+                    continue;
+                }
+            }
+            // 32 columns of the sum from c0 on
+            auto read_sum = [&](int c0, uint32_t (&v)[32]) {
+                tmem_ld32(tbase + c0, v);
+                tmem_ld_wait(v);
+                if (TOTAL && more) {
+                    uint32_t sum[32];
+                    tmem_ld32(ttotal + c0, sum);
+                    tmem_ld_wait(sum);
+                    add_to(v, sum);
+                }
+            };
             if constexpr (SPLIT) {
-                // the partial sums stay here, [column][row] in FP32
+                // the partial sums stay here, [column][row] in FP32 (16-bit
+                // gradients: over the ring, whose last MMA is done)
                 float *mine = reinterpret_cast<float *>(S.ring + PARTIAL_AT<HALF>) + q * 32 + lane;
                 for (int c0 = 0; c0 < width; c0 += 32) {
                     uint32_t v[32];
-                    tmem_ld32(tbase + c0, v);
-                    tmem_ld_wait(v);
+                    read_sum(c0, v);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         const float x = empty ? 0.0f : __uint_as_float(v[i]);
-                        mine[(c0 + i) * BM] = more ? mine[(c0 + i) * BM] + x : x;
+                        mine[(c0 + i) * BM] = !TOTAL && more ? mine[(c0 + i) * BM] + x : x;
                     }
                 }
                 width = 0;
@@ -489,7 +528,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
                     }
                 }
                 release(acc);
-                if (u.nkb - kb0 > p.part_kb) continue;
+                if (!last) continue;
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                     if (b * 32 >= width) continue;
@@ -499,7 +538,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
                     emit(v, b * 32, p.accumulate);
                 }
             } else {
-                if (more && width > 0) {
+                if (!TOTAL && more && width > 0) {
                     // the earlier part's stores are complete before they are read
                     if (on) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
                     __syncwarp();
@@ -507,15 +546,15 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
                 }
                 for (int c0 = 0; c0 < width; c0 += 32) {
                     uint32_t v[32];
-                    tmem_ld32(tbase + c0, v);
-                    tmem_ld_wait(v);
+                    read_sum(c0, v);
                     if (empty) {
-    #pragma unroll
+#pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0u;
                     }
-                    emit(v, c0, p.accumulate || more);
+                    emit(v, c0, p.accumulate || (!TOTAL && more));
                 }
                 release(acc);
+                if (TOTAL && more) release(acc ^ 1);
             }
         }
         // the stores have read their buffers and written what they carried
@@ -678,7 +717,7 @@ cudaError_t launch_dt(const void *grad, int64_t ldg, const void *a, int64_t lda,
     p.out_row_bytes = K * (out_f32 ? 4 : 2);
     p.accumulate = accumulate;
     p.status = status;
-    p.part_kb = out_f32 ? kPartStages : (1 << 30);
+    p.part_kb = out_f32 ? kPartStages : kLongPartStages<DT>;
     // a wait may last one unit's whole reduction: a microsecond per stage on top
     p.wait_ns = wait_limit_ns() + 1000ull * (uint64_t)((rows + BK - 1) / BK);
     // Few units: split an expert's rows over as many CTAs, 2 to 8, as the GPU has

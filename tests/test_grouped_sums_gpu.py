@@ -98,3 +98,29 @@ def test_16_bit_products_do_not_drift_over_long_k(dtype, counts, N, K):
         wt[e] = w[e].T
     del w
     check_long_sum(moe.moe_grouped_gemm(a, off, wt, transposed=True), ref, K, dtype, "[E, K, N]")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("E,rows,N,K", [(1, 1 << 22, 72, 264),         # joined over a cluster
+                                        (1, 1 << 19, 1544, 2048),      # pairs
+                                        (1024, 500_000, 72, 72)],      # single CTAs
+                         ids=["joined", "pairs", "singles"])
+def test_16_bit_weight_gradients_do_not_drift_over_long_segments(dtype, E, rows, N, K):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(2)
+    e = E // 3
+    off = offsets_of([0] * e + [rows] + [0] * (E - e - 1))
+    d, a = positive((rows, N), dtype, g, along=1), positive((rows, K), dtype, g, along=1)
+    some = torch.arange(0, N, max(1, N // 64), device="cuda")
+    ref = torch.zeros((some.numel(), K), dtype=torch.float64, device="cuda")
+    for r in range(0, rows, 1 << 16):
+        ref += d[r:r + (1 << 16)][:, some].double().T @ a[r:r + (1 << 16)].double()
+    got = moe.moe_grouped_gemm_weight_grad(d, a, off, grad_dtype=dtype)
+    check_long_sum(got[e][some], ref, rows, dtype, "gradient")
+    assert int(torch.count_nonzero(got[:e])) == 0 and int(torch.count_nonzero(got[e + 1:])) == 0
+    old = positive((E, N, K), dtype, g, mean=2000.0)
+    kept = old[e][some].double()
+    got = moe.moe_grouped_gemm_weight_grad(d, a, off, grad_w=old, accumulate=True)
+    slack = ref * part_slack(rows, dtype) + (ref + kept) * 2.0 ** -24
+    over = (got[e][some].double() - ref - kept).abs() - slack - half_step(ref + kept + slack, dtype)
+    assert float(over.max()) <= 0
