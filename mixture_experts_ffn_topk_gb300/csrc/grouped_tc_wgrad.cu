@@ -26,13 +26,13 @@
 // CTAs shares each unit's rows (SPLIT; FP32 gradients in units of 128 columns);
 // the FP32 partial sums meet through distributed shared memory, each CTA adding its share of
 // the columns in rank order.
-// FP32 gradients are summed in parts of kPartStages stages, each in the next
-// accumulator; the epilogue adds them in registers (pairs, units of 128
-// columns), in shared memory (SPLIT) or, on single CTAs, where few experts
-// have that many rows, in grad_w, which L2 holds meanwhile. 16-bit ones are
-// summed in parts of kLongPartStages: the total stays in the first part's
-// accumulator (TOTAL), and the later parts, all in the other one, wait until the
-// part before is added.
+// Gradients are summed in parts, of kPartStages stages (FP32) or kLongPartStages
+// (16 bits), each in an accumulator of its own. The epilogue adds the parts of
+// FP32 gradients in registers (pairs, units of 128 columns) or in shared memory
+// (SPLIT), while the next one is summed. Otherwise (TOTAL) the total stays in the
+// first part's accumulator, and the later parts, all in the other one, wait until
+// the part before is added: FP32 gradients on single CTAs, where few experts have
+// that many rows, and 16-bit ones.
 // Units run over (expert, tile of the wider matrix, tile of the narrower one),
 // the last fastest: the narrower operand's segment stays in L2 while the wider
 // one passes once.
@@ -180,7 +180,8 @@ __global__ void __launch_bounds__(THREADS, 1)
 grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_a,
                      const __grid_constant__ CUtensorMap map_out, const WgradParams p)
 {
-    constexpr bool HALF = OUT_F32 && (SPLIT || CG == 2), PARTS = OUT_F32 && CG == 2, TOTAL = !OUT_F32;
+    constexpr bool HALF = OUT_F32 && (SPLIT || CG == 2), PARTS = OUT_F32 && CG == 2;
+    constexpr bool TOTAL = !PARTS && !(OUT_F32 && SPLIT);
     constexpr int NS = STAGES<CG, HALF>;
     extern __shared__ uint8_t smem_raw[];
     Smem &S = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -447,22 +448,22 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         const float x = empty ? 0.0f : __uint_as_float(v[i]);
-                        mine[(c0 + i) * BM] = !TOTAL && more ? mine[(c0 + i) * BM] + x : x;
+                        mine[(c0 + i) * BM] = OUT_F32 && more ? mine[(c0 + i) * BM] + x : x;
                     }
                 }
                 width = 0;
             }
             if (row0 >= p.N || (empty && p.accumulate)) width = 0;
-            // adds what grad_w holds to 32 columns from c0 on (`add`) and stores them
-            auto emit = [&](uint32_t (&v)[32], int c0, bool add) {
-                if (add && row0 + lane < p.N) {
+            // stores 32 columns from c0 on, accumulating what grad_w holds
+            auto emit = [&](uint32_t (&v)[32], int c0) {
+                if (p.accumulate && row0 + lane < p.N) {
                     const int64_t col_byte = (int64_t)(u.k0 + c0) * ESZ;
                     const uint8_t *old = p.out + ((int64_t)u.e * p.N + row0 + lane) * p.out_row_bytes + col_byte;
 #pragma unroll
                     for (int c = 0; c < 32 * ESZ / 16; ++c) {
                         if (col_byte + c * 16 >= p.out_row_bytes) continue;
                         Vec16 o;
-                        // past L1, which TMA stores do not update
+                        // past L1: read once
                         asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];"
                                      : "=r"(o.w[0]), "=r"(o.w[1]), "=r"(o.w[2]), "=r"(o.w[3])
                                      : "l"(old + c * 16)
@@ -535,15 +536,9 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
                     uint32_t v[32];
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sums[b][i]);
-                    emit(v, b * 32, p.accumulate);
+                    emit(v, b * 32);
                 }
             } else {
-                if (!TOTAL && more && width > 0) {
-                    // the earlier part's stores are complete before they are read
-                    if (on) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-                    __syncwarp();
-                    asm volatile("fence.proxy.async.global;" ::: "memory");
-                }
                 for (int c0 = 0; c0 < width; c0 += 32) {
                     uint32_t v[32];
                     read_sum(c0, v);
@@ -551,7 +546,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
 #pragma unroll
                         for (int i = 0; i < 32; ++i) v[i] = 0u;
                     }
-                    emit(v, c0, p.accumulate || (!TOTAL && more));
+                    emit(v, c0);
                 }
                 release(acc);
                 if (TOTAL && more) release(acc ^ 1);

@@ -124,3 +124,24 @@ def test_16_bit_weight_gradients_do_not_drift_over_long_segments(dtype, E, rows,
     slack = ref * part_slack(rows, dtype) + (ref + kept) * 2.0 ** -24
     over = (got[e][some].double() - ref - kept).abs() - slack - half_step(ref + kept + slack, dtype)
     assert float(over.max()) <= 0
+
+
+def test_fp32_gradients_of_single_ctas_are_added_to_once():
+    """Integers, so that every sum up to the last addition is exact: with accumulate, old + sum rounded
+    once, for a segment of several parts among short ones (no pairs, nothing joined)."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(3)
+    E, N, K = 16, 1000, 1032
+    counts = [200] * E
+    counts[5] = 3500
+    off = offsets_of(counts)
+    at = off.tolist()
+    ints = lambda *s: torch.randint(-3, 4, s, generator=g, device="cuda").to(BF16)
+    d, a = ints(at[-1], N), ints(at[-1], K)
+    # 2^25 and up: a step of FP32 is 4 there
+    old = torch.randint(1 << 23, 1 << 24, (E, N, K), generator=g, device="cuda").float() * 4
+    ref = torch.stack([d[at[e]:at[e + 1]].double().T @ a[at[e]:at[e + 1]].double() for e in range(E)])
+    assert torch.equal(moe.moe_grouped_gemm_weight_grad(d, a, off).double(), ref)
+    got = moe.moe_grouped_gemm_weight_grad(d, a, off, grad_w=old.clone(), accumulate=True)
+    wrong = got != (old.double() + ref).float()
+    assert not bool(wrong.any()), f"{int(wrong.sum())} of {wrong.numel()} rounded otherwise"
