@@ -807,11 +807,13 @@ int moe_device_status(void *stream, int clear);
  * MoeError instead of a hang). Every spin-wait inside the tcgen05 expert
  * GEMMs (pipeline barriers, and the per-expert readiness counters of the
  * one-call forward) stops after this many nanoseconds (in the grouped
- * products, plus a microsecond per 64 elements of the reduction), records
- * MOE_ERR_DEVICE_TIMEOUT in the status word, drains its own copies and MMAs
- * and lets the kernel exit. Process-wide; read when a kernel is launched
- * (a captured graph keeps the value of its capture). 0 restores the
- * default of 2 s; more than 60 s gives MOE_ERR_VALUE. Meant for tests of the
+ * products and weight gradients, plus an allowance for the launch's own work:
+ * a microsecond per 64 elements of a reduction and 20 per tile of the output
+ * that a wait may stand behind), records MOE_ERR_DEVICE_TIMEOUT in the status
+ * word, drains its own copies and MMAs and lets the kernel exit. Process-wide;
+ * read when a kernel is launched (a captured graph keeps the value of its
+ * capture). 0 restores the default of 2 s; more than 60 s gives
+ * MOE_ERR_VALUE. Meant for tests of the
  * failure path, which shorten it so an expiry costs milliseconds.
  * moe_wait_limit_ns returns the limit in force.
  */

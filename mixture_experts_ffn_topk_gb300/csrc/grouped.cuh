@@ -25,6 +25,11 @@ constexpr int kPartStages = 12;
 template <int DT>
 constexpr int kLongPartStages = DT == DT_F16 ? 256 : 512;
 
+// What a wait may last for the launch's own work, on top of the wait limit: a
+// microsecond per stage and 20 per stored tile it may have to wait for, three
+// times what either takes on all SMs at once.
+inline uint64_t work_ns(uint64_t stages, uint64_t tiles) { return 1000ull * stages + 20000ull * tiles; }
+
 // sum[i] += v[i] of FP32 values held as their bits.
 template <int N>
 __device__ __forceinline__ void add_to(uint32_t (&sum)[N], const uint32_t (&v)[N])

@@ -683,8 +683,9 @@ cudaError_t launch_cg(const void *a, int64_t lda, const int32_t *offsets, int64_
     p.vec = p.out_row_bytes % 16 == 0;
     p.status = status;
     p.part_kb = out_f32 ? kPartStages : kLongPartStages<DT>;
-    // a wait may last one unit's whole reduction: a microsecond per stage on top
-    p.wait_ns = wait_limit_ns() + 1000ull * (uint64_t)((K + BK - 1) / BK);
+    // a wait may last one unit's whole reduction, a producer's as many short units
+    // as the ring has stages
+    p.wait_ns = wait_limit_ns() + work_ns((uint64_t)((K + BK - 1) / BK + p.stages), (uint64_t)p.stages);
     // an upper bound: every expert adds at most one unit that is not full
     const int64_t units = (rows / tok_cap + (rows < E ? rows : E)) * p.w_tiles;
     if constexpr (!SPLIT) {

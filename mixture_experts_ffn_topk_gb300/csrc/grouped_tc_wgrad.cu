@@ -686,6 +686,12 @@ cudaError_t launch_kernel(const CUtensorMap &mg, const CUtensorMap &ma, const CU
     const int64_t units = (int64_t)p.E * p.n_tiles * p.k_tiles;
     cfg.gridDim = dim3((unsigned)(SPLIT || ways * units < ctas ? ways * units : ctas));
     cfg.numAttrs = 2;
+    // The warp that zeroes foreign rows passes over units without any, and the
+    // producers over experts without rows, so their waits may last most of what a
+    // CTA does: per expert, its share of the expert's tiles.
+    const uint64_t groups = cfg.gridDim.x / (unsigned)ways;
+    const uint64_t tiles = ((uint64_t)p.n_tiles * p.k_tiles + groups - 1) / groups;
+    p.wait_ns = wait_limit_ns() + work_ns(tiles * (uint64_t)(p.rows / BK + p.E), tiles * (uint64_t)p.E);
     return cudaLaunchKernelEx(&cfg, kernel, mg, ma, mo, p);
 }
 
@@ -713,8 +719,6 @@ cudaError_t launch_dt(const void *grad, int64_t ldg, const void *a, int64_t lda,
     p.accumulate = accumulate;
     p.status = status;
     p.part_kb = out_f32 ? kPartStages : kLongPartStages<DT>;
-    // a wait may last one unit's whole reduction: a microsecond per stage on top
-    p.wait_ns = wait_limit_ns() + 1000ull * (uint64_t)((rows + BK - 1) / BK);
     // Few units: split an expert's rows over as many CTAs, 2 to 8, as the GPU has
     // room for and as leave each four blocks of rows on average.
     const int cols = out_f32 ? BN<true> : BN<false>;
