@@ -787,8 +787,9 @@ def moe_experts_backward(x_disp: torch.Tensor, offsets: torch.Tensor, gate: torc
 # on a few rows lasts a few microseconds on the GPU, so the checks are kept to
 # attribute reads and integer comparisons: 5 to 9 us of host time per call.
 
-_raw_stream = torch._C._cuda_getCurrentRawStream
-_current_device = torch._C._cuda_getDevice
+# None where torch was built without CUDA; no call gets that far there
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
 def _enqueue(name: str, index: int, stream, *args):
