@@ -660,7 +660,10 @@ int moe_experts_backward(const void *x_disp, const int32_t *offsets, int64_t row
  * `offsets` [E + 1] int32 (device) is that of moe_dispatch: expert e has the
  * rows [offsets[e], offsets[e + 1]). An expert whose offsets fall, are
  * negative or pass `rows` is taken as one without rows and the status word
- * records MOE_ERR_BAD_INDEX; nothing outside the matrices is touched. Rows
+ * records MOE_ERR_BAD_INDEX; nothing outside the matrices is touched. Where
+ * that happens, an expert whose rows begin before the end of an earlier one's
+ * is taken as one without rows too, so that no row has two experts: of
+ * {0, 40, 20, 60} only the first expert has rows. Rows
  * that belong to no expert are not read, and their outputs are left as they
  * were.
  * ====================================================================== */

@@ -84,3 +84,33 @@ def test_waits_allow_for_the_launchs_own_work(counts, N, K, out):
     for e in (0, 1, len(counts) - 1):
         ref = exact_matmul(d[at[e]:at[e + 1]].T, a[at[e]:at[e + 1]])
         assert torch.equal(gw[e], ref.to(out))
+
+
+BAD_INDEX = 9
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16, F32])
+@pytest.mark.parametrize("offsets,served", [([0, 40, 20, 60], [40, 0, 0]),          # falls, then overlaps
+                                            ([0, 40, 20, 60, 70], [40, 0, 0, 10]),  # one behind both is served
+                                            ([10, 30, 5, 25, 60, 61], [20, 0, 0, 0, 1]),
+                                            ([0, 50, -1, 30, 40, 70], [50, 0, 0, 0, 0])])
+def test_offsets_that_name_rows_twice(dtype, offsets, served):
+    """Once offsets fall, an expert whose rows begin before an earlier one's end has none either: its rows
+    keep what they held, and its gradient is zero."""
+    g = generator(2)
+    E, rows, N, K = len(offsets) - 1, 70, 72, 64
+    off = torch.tensor(offsets, dtype=torch.int32, device="cuda")
+    a, d = integers((rows, K), dtype, g), integers((rows, N), dtype, g)
+    w = integers((E, N, K), dtype, g)
+    out = torch.full((rows, N), -7.0, dtype=dtype, device="cuda")
+    want, gw_want = out.clone(), torch.zeros((E, N, K), device="cuda")
+    for e, n in enumerate(served):
+        s = slice(offsets[e], offsets[e] + n) if n else slice(0, 0)
+        want[s] = exact_matmul(a[s], w[e].T).to(dtype)
+        gw_want[e] = exact_matmul(d[s].T, a[s])
+    moe.moe_grouped_gemm(a, off, w, out=out)
+    assert moe.moe_device_status(clear=True) == BAD_INDEX
+    assert torch.equal(out, want)
+    gw = moe.moe_grouped_gemm_weight_grad(d, a, off)
+    assert moe.moe_device_status(clear=True) == BAD_INDEX
+    assert torch.equal(gw, gw_want)
