@@ -740,7 +740,10 @@ int moe_grouped_gemm_weight_grad(const void *grad, int64_t ldg, const void *a, i
  *         448 * 2^119 as 448): within 2^-4 of itself, or 2^(x-10) where the
  *         code is subnormal. NaN and infinities are kept as NaN.
  *   offsets  NULL (every row), or [E + 1] int32: rows from offsets[E] on are
- *         left alone, in h and in ckpt (E is unused without offsets).
+ *        left alone, in h and in ckpt (E is unused without offsets). Only
+ *        offsets[E] is read here and in the backward; a negative one counts as
+ *        0, one past `rows` as rows, and no status is recorded: the products
+ *        around these calls report such offsets.
  *   2.06 bytes per value instead of moe_experts_forward_training's 8.
  *   rows and I bounded as rows and N above. g, u and h need only their elements' alignment; rows
  *   that all start on 16 bytes are read and written in vectors.
