@@ -27,12 +27,12 @@
 // the FP32 partial sums meet through distributed shared memory, each CTA adding its share of
 // the columns in rank order.
 // Gradients are summed in parts, of kPartStages stages (FP32) or kLongPartStages
-// (16 bits), each in an accumulator of its own. The epilogue adds the parts of
-// FP32 gradients in registers (pairs, units of 128 columns) or in shared memory
-// (SPLIT), while the next one is summed. Otherwise (TOTAL) the total stays in the
-// first part's accumulator, and the later parts, all in the other one, wait until
-// the part before is added: FP32 gradients on single CTAs, where few experts have
-// that many rows, and 16-bit ones.
+// (16 bits), each in an accumulator of its own. The total stays in the first
+// part's accumulator (TOTAL), and the later parts, all in the other one, wait
+// until the part before is added; the parts of FP32 gradients that a cluster
+// shares are added in shared memory. (Sums in the epilogue's registers, which let
+// the next part run meanwhile but hold units of 128 columns at most, took 1.10 ms
+// on 8 experts of 4096 rows, N = K = 4096, where this takes 0.76.)
 // Units run over (expert, tile of the wider matrix, tile of the narrower one),
 // the last fastest: the narrower operand's segment stays in L2 while the wider
 // one passes once.
@@ -56,21 +56,20 @@ constexpr int UK = 16;                   // rows reduced per tcgen05.mma
 constexpr int BOX_BYTES = 64 * BK * 2;   // 64 columns x 64 rows
 constexpr int G_BYTES = 2 * BOX_BYTES;
 // Columns of grad_w per unit; half as many for FP32 sums of parts that are
-// added in registers (pairs) or shared memory (SPLIT).
+// added in shared memory (SPLIT).
 template <bool HALF>
 constexpr int BN = HALF ? 128 : 256;
 template <int CG, bool HALF>
 constexpr int SLOT_BYTES = G_BYTES + BN<HALF> / 64 / CG * BOX_BYTES;
 constexpr int RING_BYTES = 192 << 10;
 template <int CG, bool HALF>
-constexpr int STAGES = CG == 2 ? (HALF ? 8 : 6) : 4;
+constexpr int STAGES = CG == 2 ? 6 : 4;
 template <bool HALF>
 constexpr int PARTIAL_AT = HALF ? STAGES<1, true> * SLOT_BYTES<1, true> : 0;  // SPLIT: the sums, [column][row]
 static_assert(STAGES<1, false> * SLOT_BYTES<1, false> <= RING_BYTES &&
               STAGES<2, false> * SLOT_BYTES<2, false> <= RING_BYTES &&
-              STAGES<2, true> * SLOT_BYTES<2, true> <= RING_BYTES &&
               PARTIAL_AT<true> + BN<true> * BM * 4 <= RING_BYTES && BN<false> * BM * 4 <= RING_BYTES, "the ring");
-constexpr int MAX_STAGES = 8;
+constexpr int MAX_STAGES = 6;
 constexpr int ACC_COLS = 256;
 constexpr int TMEM_COLS = 2 * ACC_COLS;
 constexpr int THREADS = 256;
@@ -180,8 +179,7 @@ __global__ void __launch_bounds__(THREADS, 1)
 grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_constant__ CUtensorMap map_a,
                      const __grid_constant__ CUtensorMap map_out, const WgradParams p)
 {
-    constexpr bool HALF = OUT_F32 && (SPLIT || CG == 2), PARTS = OUT_F32 && CG == 2;
-    constexpr bool TOTAL = !PARTS && !(OUT_F32 && SPLIT);
+    constexpr bool HALF = OUT_F32 && SPLIT, TOTAL = !HALF;
     constexpr int NS = STAGES<CG, HALF>;
     extern __shared__ uint8_t smem_raw[];
     Smem &S = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -383,8 +381,6 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
                 else mbar_arrive(&S.acc_empty[acc]);
             }
         };
-        float sums[PARTS ? 4 : 1][32];         // PARTS: of this lane's row
-        (void)sums;
         // unit by unit, part by part (kb0: the part's first block of rows)
         for (; unit < total; kb0 += p.part_kb) {
             if (kb0 != 0 && kb0 >= u.nkb) {
@@ -448,7 +444,7 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         const float x = empty ? 0.0f : __uint_as_float(v[i]);
-                        mine[(c0 + i) * BM] = OUT_F32 && more ? mine[(c0 + i) * BM] + x : x;
+                        mine[(c0 + i) * BM] = HALF && more ? mine[(c0 + i) * BM] + x : x;
                     }
                 }
                 width = 0;
@@ -514,43 +510,17 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
                     }
                 }
             };
-            if constexpr (PARTS) {
+            for (int c0 = 0; c0 < width; c0 += 32) {
+                uint32_t v[32];
+                read_sum(c0, v);
+                if (empty) {
 #pragma unroll
-                for (int b = 0; b < 8; ++b) {
-                    if (b * 16 >= width) continue;
-                    uint32_t v[16];
-                    tmem_ld16(tbase + b * 16, v);
-                    tmem_ld_wait16(v);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float x = empty ? 0.0f : __uint_as_float(v[i]);
-                        float &sum = sums[b / 2][b % 2 * 16 + i];
-                        sum = more ? sum + x : x;
-                    }
+                    for (int i = 0; i < 32; ++i) v[i] = 0u;
                 }
-                release(acc);
-                if (!last) continue;
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                    if (b * 32 >= width) continue;
-                    uint32_t v[32];
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) v[i] = __float_as_uint(sums[b][i]);
-                    emit(v, b * 32);
-                }
-            } else {
-                for (int c0 = 0; c0 < width; c0 += 32) {
-                    uint32_t v[32];
-                    read_sum(c0, v);
-                    if (empty) {
-#pragma unroll
-                        for (int i = 0; i < 32; ++i) v[i] = 0u;
-                    }
-                    emit(v, c0);
-                }
-                release(acc);
-                if (TOTAL && more) release(acc ^ 1);
+                emit(v, c0);
             }
+            release(acc);
+            if (TOTAL && more) release(acc ^ 1);
         }
         // the stores have read their buffers and written what they carried
         if (on) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -648,7 +618,7 @@ cudaError_t launch_kernel(const CUtensorMap &mg, const CUtensorMap &ma, const CU
     auto kernel = grouped_wgrad_kernel<DT, CG, OUT_F32, SPLIT>;
     const int ways = SPLIT ? p.split : CG;
     p.n_tiles = (p.N + BM * CG - 1) / (BM * CG);
-    constexpr int COLS = BN<(OUT_F32 && (SPLIT || CG == 2))>;
+    constexpr int COLS = BN<(OUT_F32 && SPLIT)>;
     p.k_tiles = (p.K + COLS - 1) / COLS;
     p.n_fast = p.N <= p.K;
     cudaLaunchConfig_t cfg = {};
@@ -731,8 +701,10 @@ cudaError_t launch_dt(const void *grad, int64_t ldg, const void *a, int64_t lda,
                        : launch_kernel<DT, 1, false, true>(mg, ma, mo, p, s);
     // Pairs or single CTAs, by the average rows of an expert: us at 256, 384, 512,
     // 768, 1024, 4096 rows, 64 experts of 2048 x 1408 (16 of 4096 x 4096):
-    // singles 109 144 170 219 273 948 (153 205 236 307 376 1233),
-    // pairs   130 153 176 218 260 868 (177 205 232 284 343 1149).
+    // 16 bits, singles 111 125 152 214 278 1028 (143 178 221 301 386 1303),
+    //          pairs   128 140 153 192 239 937 (166 192 208 260 315 1230);
+    // FP32,    singles 155 173 195 245 354 1172 (200 230 275 357 483 1552),
+    //          pairs   171 188 200 229 386 1160 (225 250 279 320 491 1538).
     if (rows >= 512 * (int64_t)E)
         return out_f32 ? launch_kernel<DT, 2, true, false>(mg, ma, mo, p, s)
                        : launch_kernel<DT, 2, false, false>(mg, ma, mo, p, s);
