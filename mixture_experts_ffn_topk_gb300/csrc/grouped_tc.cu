@@ -403,10 +403,27 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
             // one that has given up
             if (!epi_all(1 + group, mbar_wait<CG>(&S.acc_full[acc], acc_phase, abort_flag, p.status, p.wait_ns))) break;
             tc_fence_after();
-            // (TOTAL) the accumulator that holds the sum of the earlier parts
-            const uint32_t ttotal = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)((acc ^ 1) * ACC_COLS);
-            (void)ttotal;
-            const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
+            auto tmem_of = [&](int a) { return tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * ACC_COLS); };
+            int held = acc;                                  // the accumulator that holds the sum
+            if constexpr (TOTAL) {
+                // a later part is added to the first one, which stays where it is
+                if (more) {
+                    held = acc ^ 1;
+                    for (int t0 = group * CH; t0 < u.rows; t0 += 2 * CH) {
+                        uint32_t v[16], sum[16];
+                        tmem_ld16(tmem_of(acc) + t0, v);
+                        tmem_ld16(tmem_of(held) + t0, sum);
+                        tmem_ld_wait16(v);
+                        tmem_ld_wait16(sum);
+                        add_to(sum, v);
+                        tmem_st16(tmem_of(held) + t0, sum);
+                    }
+                    tmem_st_wait();
+                    release(acc);
+                }
+                if (!last) continue;
+            }
+            const uint32_t tbase = tmem_of(held);
             const int piece = tid % PIECES, col = u.w0 + piece * (16 / ESZ);
             uint8_t *out0 = p.out + (int64_t)u.row0 * p.out_row_bytes + (int64_t)col * ESZ;
             const bool whole = p.vec && col + 16 / ESZ <= p.N;
@@ -478,25 +495,6 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                     }
                 }
             } else {
-                if constexpr (TOTAL) {
-                    // a sum that goes on: the first part stays where it is, a
-                    // later one is added to it
-                    if (!last && !more) continue;
-                    if (!last) {
-                        for (int t0 = group * CH; t0 < u.rows; t0 += 2 * CH) {
-                            uint32_t v[16], sum[16];
-                            tmem_ld16(tbase + t0, v);
-                            tmem_ld16(ttotal + t0, sum);
-                            tmem_ld_wait16(v);
-                            tmem_ld_wait16(sum);
-                            add_to(sum, v);
-                            tmem_st16(ttotal + t0, sum);
-                        }
-                        tmem_st_wait();
-                        release(acc);
-                        continue;
-                    }
-                }
                 for (int t0 = group * CH; !SPLIT && t0 < u.rows; t0 += 2 * CH) {
                     if constexpr (OUT_F32) {
                         uint32_t v[8];
@@ -516,15 +514,6 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                         tmem_ld_blocks(tbase + (16u << 16) + t0, hi);
                         tmem_ld_wait8(lo);
                         tmem_ld_wait8(hi);
-                        if (TOTAL && more) {
-                            uint32_t sum[8];
-                            tmem_ld_blocks(ttotal + t0, sum);
-                            tmem_ld_wait8(sum);
-                            add_to(lo, sum);
-                            tmem_ld_blocks(ttotal + (16u << 16) + t0, sum);
-                            tmem_ld_wait8(sum);
-                            add_to(hi, sum);
-                        }
                         const int t = lane & 7, at = q * 4 + (lane >> 3);
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
@@ -538,8 +527,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
                         buf ^= 1;
                     }
                 }
-                release(acc);
-                if (TOTAL && more) release(acc ^ 1);
+                release(held);
             }
         }
     }

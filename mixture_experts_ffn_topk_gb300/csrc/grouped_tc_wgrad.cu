@@ -397,50 +397,38 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
             const bool ready = mbar_wait<CG>(&S.acc_full[acc], acc_phase, abort_flag, p.status, p.wait_ns);
             if (!__all_sync(0xffffffffu, ready)) break;
             tc_fence_after();
-            const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * ACC_COLS);
-            // (TOTAL) the accumulator that holds the sum of the earlier parts
-            const uint32_t ttotal = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)((acc ^ 1) * ACC_COLS);
-            (void)ttotal;
             const int row0 = u.n0 + q * 32;            // this warp's first row of grad_w[e]
             const bool empty = u.cnt == 0;
             int width = p.K - u.k0 < BN<HALF> ? p.K - u.k0 : BN<HALF>;
+            auto tmem_of = [&](int a) { return tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * ACC_COLS); };
+            int held = acc;                            // the accumulator that holds the sum
             if constexpr (TOTAL) {
-                // a sum that goes on: the first part stays where it is, a
-                // later one is added to it
-                if (!last) {
-                    if (!more) continue;
+                // a later part is added to the first one, which stays where it is
+                if (more) {
+                    held = acc ^ 1;
                     for (int c0 = 0; c0 < width; c0 += 32) {
                         uint32_t v[32], sum[32];
-                        tmem_ld32(tbase + c0, v);
-                        tmem_ld32(ttotal + c0, sum);
+                        tmem_ld32(tmem_of(acc) + c0, v);
+                        tmem_ld32(tmem_of(held) + c0, sum);
                         tmem_ld_wait(v);
                         tmem_ld_wait(sum);
                         add_to(sum, v);
-                        tmem_st32(ttotal + c0, sum);
+                        tmem_st32(tmem_of(held) + c0, sum);
                     }
                     tmem_st_wait();
                     release(acc);
-                    continue;
                 }
+                if (!last) continue;
             }
-            // 32 columns of the sum from c0 on
-            auto read_sum = [&](int c0, uint32_t (&v)[32]) {
-                tmem_ld32(tbase + c0, v);
-                tmem_ld_wait(v);
-                if (TOTAL && more) {
-                    uint32_t sum[32];
-                    tmem_ld32(ttotal + c0, sum);
-                    tmem_ld_wait(sum);
-                    add_to(v, sum);
-                }
-            };
+            const uint32_t tbase = tmem_of(held);
             if constexpr (SPLIT) {
                 // the partial sums stay here, [column][row] in FP32 (16-bit
                 // gradients: over the ring, whose last MMA is done)
                 float *mine = reinterpret_cast<float *>(S.ring + PARTIAL_AT<HALF>) + q * 32 + lane;
                 for (int c0 = 0; c0 < width; c0 += 32) {
                     uint32_t v[32];
-                    read_sum(c0, v);
+                    tmem_ld32(tbase + c0, v);
+                    tmem_ld_wait(v);
 #pragma unroll
                     for (int i = 0; i < 32; ++i) {
                         const float x = empty ? 0.0f : __uint_as_float(v[i]);
@@ -512,15 +500,15 @@ grouped_wgrad_kernel(const __grid_constant__ CUtensorMap map_g, const __grid_con
             };
             for (int c0 = 0; c0 < width; c0 += 32) {
                 uint32_t v[32];
-                read_sum(c0, v);
+                tmem_ld32(tbase + c0, v);
+                tmem_ld_wait(v);
                 if (empty) {
 #pragma unroll
                     for (int i = 0; i < 32; ++i) v[i] = 0u;
                 }
                 emit(v, c0);
             }
-            release(acc);
-            if (TOTAL && more) release(acc ^ 1);
+            release(held);
         }
         // the stores have read their buffers and written what they carried
         if (on) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
