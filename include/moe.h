@@ -746,7 +746,8 @@ int moe_grouped_gemm_weight_grad(const void *grad, int64_t ldg, const void *a, i
  *        around these calls report such offsets.
  *   2.06 bytes per value instead of moe_experts_forward_training's 8.
  *   rows and I bounded as rows and N above. g, u and h need only their elements' alignment; rows
- *   that all start on 16 bytes are read and written in vectors.
+ *   that all start on 16 bytes are read and written in vectors, others by
+ *   element (16-bit rows: 1.7 times the time, in the backward 4 times).
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_ALIGN,
  * MOE_ERR_WORKSPACE (ckpt too small or not aligned), MOE_ERR_CUDA.
  */

@@ -241,6 +241,12 @@ cudaError_t launch_tile(const SimtOperand &x, const SimtOperand &y, const int32_
 //   64 x 64    227   225    214   414    903   3243
 // (128 x 64 and 128 x 128: 381 to 412 at 96 rows, 2952 to 3156 at 1024). Weight
 // gradient, N = 16, 32, 64: 17.7 22.2 33.1 us flat, 22.8 22.8 23.7 square.
+// Fewer 64-row tiles than SMs also take the flat one, which gives four times as
+// many: us flat and tall, 8 experts of 100 rows, N = 512, K = 2048: 73 and 127
+// ([E, K, N] weights 72 and 112); of 64 rows, N = 256: 47 and 126; gradients of
+// 128 x 256 over 1000 rows 22 and 54, of 512 x 128 over 200 rows 10 and 14. Just
+// below the SMs' number it loses: 3 experts of 579 rows, N = 520, K = 1024, 150
+// tiles: 76 and 65.
 constexpr int64_t kFlatTile = 40;
 
 template <bool WG, bool Y_MAJOR>

@@ -705,7 +705,10 @@ cudaError_t launch_dt(const void *a, int64_t lda, const int32_t *offsets, int64_
     // Pairs or single CTAs, by the average rows of an expert. 64 experts, N = K =
     // 2048 (16 experts, N = K = 4096), us at 4, 32, 48, 64, 96 rows on average:
     // singles 82.7 87.0 89.4 93.7 113 (87.1 89.9 91.5 101 106),
-    // pairs   87.9 92.9 93.5 95.2 98.1 (91.9 95.2 95.1 97.0 98.6).
+    // pairs   87.9 92.9 93.5 95.2 98.1 (91.9 95.2 95.1 97.0 98.6) in 16 bits;
+    // FP32 outputs, there and at 192: singles 82.8 87.3 90.0 91.6 114 156 (86.5
+    // 89.2 92.0 92.0 108 151), pairs 87.4 93.2 95.4 97.2 101 135 (92.2 94.8 97.0
+    // 97.7 101 126).
     if (rows >= 64 * (int64_t)E)
         return launch_cg<DT, 2, false>(a, lda, offsets, rows, w, E, N, K, kn, out, ldo, out_f32,
                                        out_f32 && num_kb > kPartStages ? PARTS_CAP : 256, 1, status, s);

@@ -20,7 +20,10 @@
 // shuffles for the block's maximum), so a warp touches whole 32-byte sectors
 // of every plane and no shared memory is needed. A thread keeps two blocks
 // (backward: three) in flight. At 32768 x 14336 in BF16 the forward takes
-// 0.62 ms (91 % of the measured copy bandwidth), the backward 0.71 ms (100 %).
+// 0.62 ms (91 % of the measured copy bandwidth), the backward 0.71 ms (100 %). Rows
+// that do not all start on 16 bytes are read and written by element, and bound by
+// that: 24576 x 1408, BF16, forward 52 -> 88 us, backward 65 -> 279; FP32 84 -> 108
+// and 117 -> 377.
 #include <cuda_fp8.h>
 
 #include "common.cuh"
