@@ -46,13 +46,13 @@
 #include "common.cuh"
 #include "grouped.cuh"
 #include "grouped_issue.cuh"
+#include "grouped_units.cuh"
 #include "kernels.h"
 
 namespace moe {
 
 namespace {
 
-constexpr int BM = 128;                  // weight columns per CTA
 constexpr int BK = 64;                   // k per stage: 128 bytes
 constexpr int UK = 16;                   // k per tcgen05.mma
 constexpr int W_BYTES = BM * BK * 2;     // 16 KiB
@@ -67,10 +67,6 @@ constexpr int SPLIT_CAP = 64;            // rows of a split unit at most
 constexpr int PARTS_CAP = 128;           // rows of a unit whose parts are added in registers
 constexpr int PARTIAL_BYTES = SPLIT_CAP * BM * 4;
 constexpr uint64_t kDrainLimitNs = 100000000ull;
-// Bytes of rows a block of row units may cover, well inside the 129 MB L2
-// that also carries the streamed weights and the output.
-constexpr int64_t kRowBlockBytes = 48ll << 20;
-
 struct __align__(1024) Smem {
     uint8_t ring[RING_BYTES];
     uint8_t stg[2][2][STG_BYTES];        // two per group of epilogue warps
@@ -108,78 +104,6 @@ struct GemmParams {
 struct RowMaps {
     CUtensorMap m[4];
 };
-
-struct Unit {
-    int e;
-    int row0;        // first row (in the dispatched matrix)
-    int rows;        // rows to store
-    int mma_n;       // the same rounded up to the MMA's width
-    int w0;          // first weight column of this CTA
-};
-
-// Walks a CTA's units in order. What depends on the expert alone is kept, and
-// the common case divides once: with five divisions and a search per unit the
-// MMA warp spent a thousand cycles between short units.
-template <int CG>
-struct UnitWalk {
-    const Segments &S;
-    const GemmParams &p;
-    int rank, e, cnt, n_units, each;
-
-    __device__ __forceinline__ UnitWalk(const Segments &seg, const GemmParams &params, int r)
-        : S(seg), p(params), rank(r), e(-1), cnt(0), n_units(1), each(1) {}
-
-    __device__ __forceinline__ Unit at(int unit)
-    {
-        if (e < 0 || unit >= S.unit[e + 1]) {
-            e = expert_of(S, p.E, unit);
-            cnt = S.count[e];
-            n_units = (cnt + p.tok_cap - 1) / p.tok_cap;
-            // equal widths: at most tok_cap, which is a multiple of the
-            // quantum, so that none of the n_units comes out empty
-            constexpr int Q = 16 * CG;
-            each = ((cnt + n_units - 1) / n_units + Q - 1) / Q * Q;
-        }
-        Unit u;
-        u.e = e;
-        const int local = unit - S.unit[e];
-        int wt, j;
-        if (n_units <= p.row_block) {
-            wt = local / n_units;
-            j = local - wt * n_units;
-        } else {
-            const int span = p.row_block * p.w_tiles;
-            const int b = local / span, rem = local - b * span;
-            const int left = n_units - b * p.row_block, width = left < p.row_block ? left : p.row_block;
-            wt = rem / width;
-            j = b * p.row_block + rem - wt * width;
-        }
-        const int at = j * each;
-        u.rows = cnt - at < each ? cnt - at : each;
-        u.row0 = S.first[e] + at;
-        u.mma_n = (u.rows + 16 * CG - 1) / (16 * CG) * (16 * CG);
-        u.w0 = (wt * CG + rank) * BM;
-        return u;
-    }
-};
-
-// Barrier over the four warps of an epilogue group (id: 1 or 2).
-__device__ __forceinline__ void epi_sync(int id) { asm volatile("bar.sync %0, 128;" ::"r"(id) : "memory"); }
-
-// The same, true in all of them if `ok` is in all.
-__device__ __forceinline__ bool epi_all(int id, bool ok)
-{
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.and.pred q, %2, 128, p;\n\t"
-        "selp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)ok), "r"(id)
-        : "memory");
-    return r != 0;
-}
 
 // 32 TMEM lanes x 8 consecutive fp32 columns.
 __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
@@ -264,7 +188,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
     const uint32_t tmem_base = S.tmem_base;
     const int total = S.seg.unit[p.E];
     volatile int *abort_flag = &S.abort;
-    UnitWalk<CG> walk(S.seg, p, rank);
+    UnitWalk<CG, GemmParams> walk(S.seg, p, rank);
 
     if (warp == 0) {
         // ------------------------------------------- TMA producer: weights
@@ -537,7 +461,7 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
         __syncwarp();
         cluster_sync();
         if (unit0 < total) {
-            const Unit u = UnitWalk<CG>(S.seg, p, rank).at(unit0);
+            const Unit u = UnitWalk<CG, GemmParams>(S.seg, p, rank).at(unit0);
             const uint32_t partial = smem_u32(S.ring + RING_BYTES - PARTIAL_BYTES);
             for (int i = threadIdx.x; ; i += THREADS) {
                 const int t = i / BM * ways + slice, n = i % BM;
@@ -573,44 +497,6 @@ grouped_gemm_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_cons
 
 // ---- host side ---------------------------------------------------------------
 
-// Opts this kernel instance in to its shared memory, and (pairs) asks how many
-// clusters the GPU holds at once, once per device.
-template <typename Kernel>
-cudaError_t prepare_kernel(Kernel kernel, int cg, std::atomic<int> *cache, int *ctas)
-{
-    int dev = 0;
-    cudaError_t err = cudaGetDevice(&dev);
-    if (err != cudaSuccess) return err;
-    const bool cached = dev >= 0 && dev < kCachedDevices;
-    int n = cached ? cache[dev].load() : 0;
-    if (n == 0) {
-        err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes);
-        if (err != cudaSuccess) return err;
-        n = device_sm_count();
-        if (cg == 2) {
-            cudaLaunchConfig_t cfg = {};
-            cfg.gridDim = dim3((unsigned)(n & ~1));
-            cfg.blockDim = dim3(THREADS);
-            cfg.dynamicSmemBytes = kSmemBytes;
-            cudaLaunchAttribute attr[1];
-            attr[0].id = cudaLaunchAttributeClusterDimension;
-            attr[0].val.clusterDim.x = 2;
-            attr[0].val.clusterDim.y = 1;
-            attr[0].val.clusterDim.z = 1;
-            cfg.attrs = attr;
-            cfg.numAttrs = 1;
-            int pairs = 0;
-            err = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg);
-            if (err != cudaSuccess) return err;
-            if (pairs < 1) return cudaErrorInvalidConfiguration;
-            n = 2 * pairs;
-        }
-        if (cached) cache[dev].store(n);
-    }
-    *ctas = n;
-    return cudaSuccess;
-}
-
 template <int DT, int CG, bool KN, bool OUT_F32, bool SPLIT, bool PARTS>
 cudaError_t launch_kernel(int64_t units, const CUtensorMap &mw, const RowMaps &ma, const GemmParams &p,
                           cudaStream_t s)
@@ -618,7 +504,7 @@ cudaError_t launch_kernel(int64_t units, const CUtensorMap &mw, const RowMaps &m
     static std::atomic<int> cache[kCachedDevices];
     auto kernel = grouped_gemm_kernel<DT, CG, KN, OUT_F32, SPLIT, PARTS>;
     int ctas = 0;
-    cudaError_t err = prepare_kernel(kernel, CG, cache, &ctas);
+    cudaError_t err = prepare_kernel(kernel, CG, THREADS, kSmemBytes, cache, &ctas);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
     const int ways = SPLIT ? p.split : CG;

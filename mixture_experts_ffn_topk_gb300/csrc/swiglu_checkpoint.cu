@@ -28,120 +28,19 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "rows8.cuh"
 
 namespace moe {
 
 namespace {
 
 constexpr int kBlock = 32;       // columns that share a scale
-constexpr int kLaneCols = 8;     // columns a lane handles
-constexpr int kThreads = 256;
+constexpr int kLanes = kBlock / kLaneCols;
 // Blocks a thread has in flight at once: on 32768 x 14336 values in BF16, 1, 2 and
 // 3 take the forward 614, 619 and 632 us (24576 x 1408: 58, 53, 55), the backward
 // 771, 737 and 707.
 constexpr int kForwardItems = 2;
 constexpr int kBackwardItems = 3;
-
-// Item = one block of one row; a thread walks items first, first + step, ...
-// as (row, blk) pairs without dividing: step = step_row * S + step_blk.
-struct Walk {
-    int64_t rows;            // rows of the call
-    int S;                   // blocks per row
-    int64_t step_row;
-    int step_blk;
-    const int32_t *end;      // offsets + E (rows from *end on are left alone), or nullptr
-};
-
-__device__ __forceinline__ int64_t rows_to_do(const Walk &w)
-{
-    if (w.end == nullptr) return w.rows;
-    const int64_t e = *w.end;
-    return e < 0 ? 0 : (e < w.rows ? e : w.rows);
-}
-
-// Eight consecutive columns of a row as they are stored.
-template <int DT>
-struct Raw8 {
-    uint4 q[DT == DT_F32 ? 2 : 1];
-
-    __device__ __forceinline__ float at(int i) const
-    {
-        const uint32_t *w = reinterpret_cast<const uint32_t *>(q);
-        if constexpr (DT == DT_F32) return __uint_as_float(w[i]);
-        const uint32_t h = w[i >> 1];
-        if constexpr (DT == DT_BF16) return __uint_as_float(i & 1 ? h & 0xffff0000u : h << 16);
-        return __half2float(__ushort_as_half((unsigned short)(i & 1 ? h >> 16 : h)));
-    }
-};
-
-// VEC: rows start on 16 bytes. A piece that is not whole (the end of a row, or
-// any piece without VEC) is read by element; columns past `left` read 0.
-template <int DT, bool VEC>
-__device__ __forceinline__ Raw8<DT> load8(const void *row, int col, int left)
-{
-    using T = typename Elem<DT>::T;
-    const T *p = static_cast<const T *>(row) + col;
-    Raw8<DT> r;
-    if (VEC && left >= 8) {
-#pragma unroll
-        for (int i = 0; i < (DT == DT_F32 ? 2 : 1); ++i) r.q[i] = __ldcs(reinterpret_cast<const uint4 *>(p) + i);
-    } else {
-#pragma unroll
-        for (int i = 0; i < (DT == DT_F32 ? 2 : 1); ++i) r.q[i] = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < left) reinterpret_cast<T *>(&r)[i] = p[i];
-    }
-    return r;
-}
-
-template <int DT, bool VEC>
-__device__ __forceinline__ void store8(void *row, int col, int left, const float (&v)[8])
-{
-    using T = typename Elem<DT>::T;
-    T *p = static_cast<T *>(row) + col;
-    if (VEC && left >= 8) {
-        if constexpr (DT == DT_F32) {
-            reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-        } else {
-            Vec16 q;
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                q.w[i] = DT == DT_BF16 ? float2_to_bf16x2(v[2 * i], v[2 * i + 1])
-                                       : float2_to_f16x2(v[2 * i], v[2 * i + 1]);
-            *reinterpret_cast<uint4 *>(p) = q.u;
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (i < left) p[i] = Elem<DT>::from_f(v[i]);
-    }
-}
-
-// t = 1 / (1 + exp(-g)) and 1 - t, from z = exp(-|g|) <= 1: nothing overflows,
-// and where t is tiny it fades through FP32's subnormals instead of dropping
-// to 0 at exp(89). FP32 outputs take the full exponential and division; the
-// 16-bit ones the hardware's approximations (errors of about 2^-21 (1 + |g|), far
-// below their rounding), of exp(-|g| / 2), whose square fades as it should
-// where the approximation itself, which knows no subnormals, would be 0.
-template <int DT>
-__device__ __forceinline__ void sigmoid_of(float g, float &t, float &not_t)
-{
-    float z, r;
-    if constexpr (DT == DT_F32) {
-        z = expf(-fabsf(g));
-        r = 1.0f / (1.0f + z);
-    } else {
-        float w;
-        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(w) : "f"(fabsf(g) * -0.72134752f));   // -log2(e) / 2
-        z = w * w;
-        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + z));
-    }
-    const float zr = z * r;
-    t = g >= 0.0f ? r : zr;
-    not_t = g >= 0.0f ? zr : r;
-}
 
 // The block's scale byte from its largest finite magnitude's bits, which all
 // four lanes of the block hold: 1.75 * 2^8 = 448.
@@ -149,30 +48,6 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top)
 {
     const int b = (int)(top >> 23) - 8 + ((top & 0x7fffffu) > 0x600000u ? 1 : 0);
     return (uint32_t)min(max(b, 0), 246);
-}
-
-// Largest magnitude of this lane's eight values as FP32 bits; FINITE: of the
-// finite ones only. 16-bit values are compared two at a time.
-template <int DT, bool FINITE>
-__device__ __forceinline__ uint32_t top8(const Raw8<DT> &v)
-{
-    if constexpr (DT == DT_F32 || FINITE) {
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t a = __float_as_uint(v.at(i)) & 0x7fffffffu;
-            top = max(top, !FINITE || a < 0x7f800000u ? a : 0u);
-        }
-        return top;
-    } else {
-        constexpr uint32_t M = 0x7fff7fffu;
-        uint32_t m = __vimax3_u16x2(v.q[0].x & M, v.q[0].y & M, v.q[0].z & M);
-        m = __vimax3_u16x2(m, v.q[0].w & M, m);
-        m = max(m & 0xffffu, m >> 16);
-        if constexpr (DT == DT_BF16) return m << 16;
-        // F16 infinities and NaN stay at or above FP32's infinity
-        return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
-    }
 }
 
 // Codes of this lane's eight values, and the block's scale byte. All lanes of
@@ -220,30 +95,8 @@ __device__ __forceinline__ void decode8(uint2 c, uint32_t sb, float (&v)[8])
     }
 }
 
-// Where a thread is in the walk.
-struct Place {
-    int64_t row;
-    int blk;
-
-    __device__ __forceinline__ void advance(const Walk &w)
-    {
-        row += w.step_row;
-        blk += w.step_blk;
-        if (blk >= w.S) { blk -= w.S; ++row; }
-    }
-};
-
-__device__ __forceinline__ Place first_place(const Walk &w)
-{
-    const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 2;
-    Place p;
-    p.row = item / w.S;
-    p.blk = (int)(item - p.row * w.S);
-    return p;
-}
-
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kRowThreads)
 swiglu_checkpoint_kernel(const void *__restrict__ g, const void *__restrict__ u, int64_t ld_bytes,
                          int I, Walk w, void *__restrict__ h, int64_t ldh_bytes,
                          uint8_t *__restrict__ codes_g, uint8_t *__restrict__ codes_u,
@@ -253,7 +106,7 @@ swiglu_checkpoint_kernel(const void *__restrict__ g, const void *__restrict__ u,
     pdl_launch_dependents();
     const int64_t rows = rows_to_do(w);
     const int part = (threadIdx.x & 3) * kLaneCols;
-    Place at = first_place(w);
+    Place at = first_place<kLanes>(w);
     // the four lanes of a block stay together; a warp leaves when all its
     // blocks are done, so the shuffles always have every lane
     while (__any_sync(0xffffffffu, at.row < rows)) {
@@ -295,7 +148,7 @@ swiglu_checkpoint_kernel(const void *__restrict__ g, const void *__restrict__ u,
 }
 
 template <int DT, bool VEC>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kRowThreads)
 swiglu_checkpoint_backward_kernel(const void *__restrict__ grad_h, int64_t ld_bytes,
                                   const uint8_t *__restrict__ codes_g,
                                   const uint8_t *__restrict__ codes_u,
@@ -308,7 +161,7 @@ swiglu_checkpoint_backward_kernel(const void *__restrict__ grad_h, int64_t ld_by
     pdl_launch_dependents();
     const int64_t rows = rows_to_do(w);
     const int part = (threadIdx.x & 3) * kLaneCols;
-    Place at = first_place(w);
+    Place at = first_place<kLanes>(w);
     while (at.row < rows) {
         Place p[kBackwardItems];
         Raw8<DT> d[kBackwardItems];
@@ -351,31 +204,6 @@ swiglu_checkpoint_backward_kernel(const void *__restrict__ grad_h, int64_t ld_by
     }
 }
 
-// At least 8 CTAs per SM (the whole work, if less), more where each thread
-// would walk over 16 blocks: on 32768 x 14336 values 8, 16 and 64 per SM took
-// 645, 637 and 634 us (backward 769, 760, 743), on 24576 x 1408 53, 57, 60.
-Walk make_walk(int64_t rows, int64_t I, const int32_t *end, unsigned *grid)
-{
-    Walk w;
-    w.rows = rows;
-    w.S = (int)((I + kBlock - 1) / kBlock);
-    w.end = end;
-    const int64_t per = kThreads / 4, items = rows * w.S;
-    const int64_t want = (items + per - 1) / per, fill = (int64_t)device_sm_count() * 8;
-    int64_t n = want / 16 > fill ? want / 16 : want < fill ? want : fill;
-    if (n > 0x7fffffff) n = 0x7fffffff;
-    *grid = (unsigned)n;
-    const int64_t step = n * per;
-    w.step_row = step / w.S;
-    w.step_blk = (int)(step % w.S);
-    return w;
-}
-
-bool rows16(const void *p, int64_t ld_bytes)
-{
-    return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld_bytes % 16 == 0;
-}
-
 template <int DT>
 cudaError_t forward_dt(const void *g, const void *u, int64_t ld, int64_t rows, int64_t I,
                        const int32_t *end, void *h, int64_t ldh, uint8_t *cg, uint8_t *cu,
@@ -383,10 +211,10 @@ cudaError_t forward_dt(const void *g, const void *u, int64_t ld, int64_t rows, i
 {
     const int64_t eb = sizeof(typename Elem<DT>::T);
     unsigned grid;
-    const Walk w = make_walk(rows, I, end, &grid);
+    const Walk w = make_walk<kLanes>(rows, I, end, &grid);
     const bool vec = rows16(g, ld * eb) && rows16(u, ld * eb) && rows16(h, ldh * eb);
     auto k = vec ? swiglu_checkpoint_kernel<DT, true> : swiglu_checkpoint_kernel<DT, false>;
-    return launch_pdl(k, dim3(grid), dim3(kThreads), 0, s, g, u, ld * eb, (int)I, w, h, ldh * eb,
+    return launch_pdl(k, dim3(grid), dim3(kRowThreads), 0, s, g, u, ld * eb, (int)I, w, h, ldh * eb,
                       cg, cu, sg, su);
 }
 
@@ -398,12 +226,12 @@ cudaError_t backward_dt(const void *gh, int64_t ld, const uint8_t *cg, const uin
 {
     const int64_t eb = sizeof(typename Elem<DT>::T);
     unsigned grid;
-    const Walk w = make_walk(rows, I, end, &grid);
+    const Walk w = make_walk<kLanes>(rows, I, end, &grid);
     const bool vec = rows16(gh, ld * eb) && rows16(dg, ldg * eb) && rows16(du, ldg * eb) &&
                      (h == nullptr || rows16(h, ldh * eb));
     auto k = vec ? swiglu_checkpoint_backward_kernel<DT, true>
                  : swiglu_checkpoint_backward_kernel<DT, false>;
-    return launch_pdl(k, dim3(grid), dim3(kThreads), 0, s, gh, ld * eb, cg, cu, sg, su, (int)I, w,
+    return launch_pdl(k, dim3(grid), dim3(kRowThreads), 0, s, gh, ld * eb, cg, cu, sg, su, (int)I, w,
                       dg, du, ldg * eb, h, ldh * eb);
 }
 
