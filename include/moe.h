@@ -787,6 +787,140 @@ int moe_swiglu_checkpoint_backward(const void *grad_h, int64_t ld, const void *c
                                    void *grad_u, int64_t ldg, void *h, int64_t ldh,
                                    void *stream);
 
+/* ======================================================================
+ * Experts in 8 bits: rows and matrices as e4m3 codes with an FP32 scale per
+ * block of 128 columns (matrices: 128 rows x 128 columns), and their grouped
+ * product. An 8-bit layer is dispatch -> moe_quantize_rows ->
+ * moe_grouped_gemm_f8 (gate and up) -> moe_swiglu_quantize ->
+ * moe_grouped_gemm_f8 (down) -> combine. For training: the input gradient of a
+ * product is the product of the quantized gradient rows with the same codes and
+ * scales read as MOE_WEIGHT_KN; the weight gradient is
+ * moe_grouped_gemm_weight_grad of the rows before they were quantized; SwiGLU's
+ * backward is moe_swiglu_checkpoint_backward.
+ *
+ * A block's scale is s = m / 448 in FP32, m the largest magnitude of its finite
+ * values, 2^-100 at least; a value v is kept as e4m3(v * (448 / m)), to nearest
+ * even: code * s is within (2^-4 + 2^-22) |v| of v, or 2^-10 s where the code is
+ * subnormal. NaN and infinities are kept as NaN. Blocks begin at column (and
+ * row) 0 of each row (matrix); the last one may be narrower.
+ *
+ * The conventions of the grouped products above hold: rows of unit column stride
+ * `ld` elements (codes: bytes) apart, no output overlapping an input or another
+ * output, no workspace, bit-reproducible results, offsets as there. Scales are
+ * dense.
+ * ====================================================================== */
+
+/*
+ * moe_quantize_rows
+ *   x       [rows, K] in dtype (F32/BF16/F16), row stride ld, read only.
+ *   codes   [rows, K] e4m3, row stride ldc bytes, written.
+ *   scales  [rows, ceil(K / 128)] FP32, written.
+ *   offsets NULL (every row), or [E + 1] int32: rows from offsets[E] on are
+ *           left alone (as in moe_swiglu_checkpoint).
+ *   0 <= rows <= 2^31 - 1024, 1 <= K <= 2^24, strides up to 2^32. x needs its
+ *   elements' alignment, codes none; rows of x that all start on 16 bytes, with
+ *   rows of codes on 8, are moved in vectors, others by element.
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_ALIGN, MOE_ERR_CUDA.
+ */
+int moe_quantize_rows(const void *x, int64_t ld, const int32_t *offsets, int64_t E, int64_t rows,
+                      int64_t K, int dtype, uint8_t *codes, int64_t ldc, float *scales, void *stream);
+
+/*
+ * moe_swiglu_quantize -- moe_quantize_rows of h = g / (1 + exp(-g)) * u.
+ *   g, u    [rows, I] in dtype, row stride ld (both), read only: the gate and up
+ *           products. h is FP32, not rounded before it is quantized.
+ *   codes, scales, offsets, limits and errors as moe_quantize_rows.
+ */
+int moe_swiglu_quantize(const void *g, const void *u, int64_t ld, const int32_t *offsets, int64_t E,
+                        int64_t rows, int64_t I, int dtype, uint8_t *codes, int64_t ldc,
+                        float *scales, void *stream);
+
+/*
+ * moe_quantize_weights
+ *   w       [E, N, K] in dtype, dense, read only.
+ *   codes   [E, N, K] e4m3, dense, written.
+ *   scales  [E, ceil(N / 128), ceil(K / 128)] FP32, written.
+ *   1 <= E <= 1024, 1 <= N, K <= 2^24, at most 2^31 - 1 blocks. Alignment as
+ *   moe_quantize_rows.
+ */
+int moe_quantize_weights(const void *w, int64_t E, int64_t N, int64_t K, int dtype, uint8_t *codes,
+                         float *scales, void *stream);
+
+/*
+ * moe_grouped_gemm_f8 -- the product of every row with its expert's matrix.
+ *   a         [rows, K] e4m3, row stride lda bytes; a_scales [rows, KB] FP32,
+ *             KB = ceil(K / 128).
+ *   w         [E, N, K] (MOE_WEIGHT_NK) or [E, K, N] (MOE_WEIGHT_KN) e4m3, dense;
+ *             w_scales [E, NB, KB] or [E, KB, NB] FP32, NB = ceil(N / 128).
+ *             Any FP32 scales will do, also those of a checkpoint quantized elsewhere.
+ *   out       [rows, N] in out_dtype (F32, BF16 or F16), row stride ldo, written
+ *             for the rows of every expert: out[r, n] = sum over the blocks b of
+ *             a_scales[r, b] w_scales[e, n / 128, b] * (sum over k in b of
+ *             a[r, k] w[e][n, k]); the inner sums and the outer one in FP32,
+ *             rounded once.
+ *   K and lda, and N with MOE_WEIGHT_KN, take multiples of 16; other N, and any
+ *   ldo >= N, are fine. Other limits, offsets and errors as moe_grouped_gemm.
+ */
+int moe_grouped_gemm_f8(const uint8_t *a, int64_t lda, const float *a_scales, const int32_t *offsets,
+                        int64_t rows, const uint8_t *w, const float *w_scales, int weight_layout,
+                        int64_t E, int64_t N, int64_t K, void *out, int64_t ldo, int out_dtype,
+                        void *stream);
+
+/* ======================================================================
+ * The whole layer for a few tokens (a decode step), in two kernels: routing, the
+ * gate and up products and SwiGLU; the down product and the combine. It reads the
+ * touched experts' matrices once and is bound by that.
+ * ====================================================================== */
+
+/*
+ * The experts of the few-token forward: gate, up [E, I, H] and down [E, H, I], in the
+ * activations' dtype with all scales NULL, or as e4m3 codes with scales
+ * [E, ceil(I / 128), ceil(H / 128)] (gate, up) and [E, ceil(H / 128), ceil(I / 128)]
+ * (down), as moe_quantize_weights makes them. Device pointers; the structure is read
+ * during the call.
+ */
+typedef struct moe_few_experts {
+    const void *gate;
+    const void *up;
+    const void *down;
+    const float *gate_scales;
+    const float *up_scales;
+    const float *down_scales;
+} moe_few_experts;
+
+/*
+ * moe_forward_few -- moe_forward for T <= 32 tokens.
+ *   x        [T, H] in dtype; logits [T, E] in logits_dtype; y [T, H] in dtype,
+ *            written.
+ *   Routing as moe_route (same experts; weights equal up to the order of the
+ *   softmax's FP32 sum), h rounded to dtype, expert outputs FP32 into the combine,
+ *   which adds in slot order. 8-bit weights meet unquantized activations: a
+ *   block's 128 products are summed in FP32 and multiplied by its scale.
+ *   Bit-reproducible.
+ *   0 <= T <= 32, 1 <= E <= 1024, 1 <= top_k <= min(E, 32); H and I at most 2^20,
+ *   multiples of 16 bytes of weights (F32: 4, BF16 / F16: 8, e4m3: 16 elements);
+ *   e4m3 weights need BF16 or F16 activations.
+ *   workspace  moe_forward_few_workspace_size(T, I, top_k, dtype) bytes (holds h).
+ * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_ALIGN,
+ * MOE_ERR_WORKSPACE, MOE_ERR_CUDA.
+ */
+size_t moe_forward_few_workspace_size(int64_t T, int64_t I, int top_k, int dtype);
+int moe_forward_few(const void *x, int dtype, const void *logits, int logits_dtype,
+                    const moe_few_experts *experts, int64_t T, int64_t H, int64_t I, int64_t E,
+                    int top_k, int renormalize, void *y, void *workspace, size_t workspace_bytes,
+                    void *stream);
+
+/*
+ * moe_forward_few_routed -- the same from a routing made before (for example by
+ * moe_route_sigmoid_grouped): expert_indices [T, top_k] uint32 and weights
+ * [T, top_k] in weights_dtype. A token may name an expert twice. An index >= E makes
+ * the token's row NaN and the status word records MOE_ERR_BAD_INDEX.
+ */
+int moe_forward_few_routed(const void *x, int dtype, const uint32_t *expert_indices, const void *weights,
+                           int weights_dtype, const moe_few_experts *experts, int64_t T, int64_t H,
+                           int64_t I, int64_t E, int top_k, void *y, void *workspace,
+                           size_t workspace_bytes, void *stream);
+
 /*
  * moe_device_status -- read the current device's status word.
  * Synchronises `stream`, then returns MOE_OK, MOE_ERR_BAD_INDEX,

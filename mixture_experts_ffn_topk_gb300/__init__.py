@@ -68,7 +68,9 @@ EXPORTED = ["moe_status_string", "moe_abi_version", "moe_last_error_detail",
             "moe_selftest_wait_expiry_workspace_size", "moe_selftest_wait_expiry",
             "moe_grouped_gemm", "moe_grouped_gemm_weight_grad", "moe_swiglu_checkpoint_size",
             "moe_swiglu_checkpoint_layout", "moe_swiglu_checkpoint",
-            "moe_swiglu_checkpoint_backward"]
+            "moe_swiglu_checkpoint_backward", "moe_quantize_rows", "moe_quantize_weights",
+            "moe_swiglu_quantize", "moe_grouped_gemm_f8", "moe_forward_few_workspace_size",
+            "moe_forward_few", "moe_forward_few_routed"]
 
 MOE_FORWARD_DETERMINISTIC = 1
 
@@ -120,6 +122,12 @@ class CheckpointLayout(ctypes.Structure):
     """Mirror of ``moe_checkpoint_layout`` (include/moe.h)."""
     _fields_ = [(n, ctypes.c_size_t) for n in ("gate_codes", "up_codes", "gate_scales", "up_scales",
                                                "row_codes", "row_scales", "total")]
+
+
+class FewExperts(ctypes.Structure):
+    """Mirror of ``moe_few_experts`` (include/moe.h)."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("gate", "up", "down", "gate_scales", "up_scales",
+                                               "down_scales")]
 
 
 class MoeError(RuntimeError):
@@ -196,6 +204,16 @@ def _bind(lib):
                                    _P], _INT),
         "moe_swiglu_checkpoint_backward": ([_P, _I64, _P, _SZ, _P, _I64, _I64, _I64, _INT, _P,
                                             _P, _I64, _P, _I64, _P], _INT),
+        "moe_quantize_rows": ([_P, _I64, _P, _I64, _I64, _I64, _INT, _P, _I64, _P, _P], _INT),
+        "moe_quantize_weights": ([_P, _I64, _I64, _I64, _INT, _P, _P, _P], _INT),
+        "moe_swiglu_quantize": ([_P, _P, _I64, _P, _I64, _I64, _I64, _INT, _P, _I64, _P, _P], _INT),
+        "moe_grouped_gemm_f8": ([_P, _I64, _P, _P, _I64, _P, _P, _INT, _I64, _I64, _I64, _P, _I64,
+                                 _INT, _P], _INT),
+        "moe_forward_few_workspace_size": ([_I64, _I64, _INT, _INT], _SZ),
+        "moe_forward_few": ([_P, _INT, _P, _INT, ctypes.POINTER(FewExperts), _I64, _I64, _I64, _I64,
+                             _INT, _INT, _P, _P, _SZ, _P], _INT),
+        "moe_forward_few_routed": ([_P, _INT, _P, _P, _INT, ctypes.POINTER(FewExperts), _I64, _I64,
+                                    _I64, _I64, _INT, _P, _P, _SZ, _P], _INT),
     }
     for name, (args, res) in sig.items():
         f = getattr(lib, name)
@@ -1001,3 +1019,185 @@ def moe_swiglu_checkpoint_backward(grad_h: torch.Tensor, ckpt: torch.Tensor, off
              _code(dt), grad_g.data_ptr(), grad_u.data_ptr(), ldg,
              None if h is None else h.data_ptr(), ldh)
     return grad_g, grad_u, h
+
+
+# ---- experts in 8 bits ------------------------------------------------------
+# As the grouped products: on the device of their tensors, outputs from the pool of
+# the stream that writes them.
+
+_F8 = torch.float8_e4m3fn
+_BLOCK = 128
+
+
+def _blocks(n: int) -> int:
+    return (n + _BLOCK - 1) // _BLOCK
+
+
+def _dense(name: str, t: torch.Tensor, shape, dtype, index: int) -> int:
+    """Checks a contiguous tensor; returns its address."""
+    if (t.shape != shape or t.dtype is not dtype or not t.is_cuda or t.get_device() != index or
+            not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous {dtype} of shape {tuple(shape)} on cuda:{index}, not "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _quantize_outputs(rows: int, K: int, codes, scales, like, index: int, stream):
+    if codes is None:
+        codes, ldc = _empty((rows, K), _F8, like, stream), K
+    else:
+        ldc = _ld("codes", codes, rows, K, _F8, index)
+    if scales is None:
+        scales = _empty((rows, _blocks(K)), torch.float32, like, stream)
+    return codes, ldc, scales, _dense("scales", scales, (rows, _blocks(K)), torch.float32, index)
+
+
+def moe_quantize_rows(x: torch.Tensor, offsets=None, codes=None, scales=None, stream=None):
+    """Rows ``[rows, K]`` in 8 bits, with a scale for each 128 columns. Returns
+    ``(codes float8_e4m3fn [rows, K], scales float32 [rows, ceil(K / 128)])``: a value
+    is ``code * scale`` of its block. ``x`` and ``codes`` may be columns of wider
+    matrices. With ``offsets`` the rows past ``offsets[E]`` are left alone."""
+    dev, dt = _cuda(x), x.dtype
+    rows, K = x.shape
+    E = 0 if offsets is None else _experts(offsets, dev)
+    ld = _ld("x", x, rows, K, dt, dev)
+    codes, ldc, scales, sp = _quantize_outputs(rows, K, codes, scales, x, dev, stream)
+    _enqueue("moe_quantize_rows", dev, stream, x.data_ptr(), ld,
+             None if offsets is None else offsets.data_ptr(), E, rows, K, _code(dt), codes.data_ptr(),
+             ldc, sp)
+    return codes, scales
+
+
+def moe_swiglu_quantize(g: torch.Tensor, u: torch.Tensor, offsets=None, codes=None, scales=None,
+                        stream=None):
+    """``SiLU(g) * u`` of the gate and up products ``[rows, I]`` (of equal row
+    stride; the halves of a stacked ``[rows, 2I]`` matrix will do), straight into
+    what :func:`moe_quantize_rows` returns."""
+    dev, dt = _cuda(g), g.dtype
+    rows, I = g.shape
+    E = 0 if offsets is None else _experts(offsets, dev)
+    ld = _ld("g", g, rows, I, dt, dev)
+    if _ld("u", u, rows, I, dt, dev) != ld:
+        raise ValueError("g and u must have the same row stride")
+    codes, ldc, scales, sp = _quantize_outputs(rows, I, codes, scales, g, dev, stream)
+    _enqueue("moe_swiglu_quantize", dev, stream, g.data_ptr(), u.data_ptr(), ld,
+             None if offsets is None else offsets.data_ptr(), E, rows, I, _code(dt), codes.data_ptr(),
+             ldc, sp)
+    return codes, scales
+
+
+def moe_quantize_weights(w: torch.Tensor, codes=None, scales=None, stream=None):
+    """Matrices ``[E, N, K]`` in 8 bits, with a scale for each 128 x 128 block.
+    Returns ``(codes float8_e4m3fn [E, N, K], scales float32
+    [E, ceil(N / 128), ceil(K / 128)])``."""
+    dev, dt = _cuda(w), w.dtype
+    if w.dim() != 3 or not w.is_contiguous():
+        raise ValueError("w must be contiguous, of three dimensions")
+    E, N, K = w.shape
+    if codes is None:
+        codes = _empty((E, N, K), _F8, w, stream)
+    if scales is None:
+        scales = _empty((E, _blocks(N), _blocks(K)), torch.float32, w, stream)
+    _enqueue("moe_quantize_weights", dev, stream, w.data_ptr(), E, N, K, _code(dt),
+             _dense("codes", codes, (E, N, K), _F8, dev),
+             _dense("scales", scales, (E, _blocks(N), _blocks(K)), torch.float32, dev))
+    return codes, scales
+
+
+def moe_grouped_gemm_f8(a: torch.Tensor, a_scales: torch.Tensor, offsets: torch.Tensor,
+                        w: torch.Tensor, w_scales: torch.Tensor, transposed: bool = False, out=None,
+                        out_dtype: torch.dtype | None = None, stream=None) -> torch.Tensor:
+    """:func:`moe_grouped_gemm` of 8-bit rows and matrices: ``a`` (float8_e4m3fn
+    ``[rows, K]``, scales ``[rows, ceil(K / 128)]``) with ``w`` (``[E, N, K]``, scales
+    ``[E, ceil(N / 128), ceil(K / 128)]``) or, ``transposed``, ``w [E, K, N]`` with
+    scales ``[E, ceil(K / 128), ceil(N / 128)]``. Returns ``out [rows, N]`` in
+    ``out_dtype`` (default bfloat16)."""
+    dev = _cuda(a)
+    rows, K = a.shape
+    E = _experts(offsets, dev)
+    if w.dim() != 3:
+        raise ValueError("w must have three dimensions")
+    N = w.shape[2 if transposed else 1]
+    lda = _ld("a", a, rows, K, _F8, dev)
+    ap = _dense("a_scales", a_scales, (rows, _blocks(K)), torch.float32, dev)
+    shape = (E, K, N) if transposed else (E, N, K)
+    wp = _dense("w", w, shape, _F8, dev)
+    sp = _dense("w_scales", w_scales, (E, _blocks(shape[1]), _blocks(shape[2])), torch.float32, dev)
+    if out is None:
+        out, ldo = _empty((rows, N), out_dtype or torch.bfloat16, a, stream), N
+    else:
+        ldo = _ld("out", out, rows, N, out_dtype or out.dtype, dev)
+    _enqueue("moe_grouped_gemm_f8", dev, stream, a.data_ptr(), lda, ap, offsets.data_ptr(), rows, wp, sp,
+             MOE_WEIGHT_KN if transposed else MOE_WEIGHT_NK, E, N, K, out.data_ptr(), ldo,
+             _code(out.dtype))
+    return out
+
+
+# ---- the whole layer for a few tokens ---------------------------------------
+
+def moe_forward_few_workspace_size(T: int, I: int, top_k: int, dtype: torch.dtype) -> int:
+    return int(load_library().moe_forward_few_workspace_size(T, I, top_k, _code(dtype)))
+
+
+def _forward_few(name: str, x, routing, top_k: int, gate, up, down, gate_scales, up_scales, down_scales,
+                 y, workspace, stream, tail):
+    """Checks and calls; ``routing`` and ``tail``: the arguments in front of the
+    experts and behind top_k."""
+    dev, dt = _cuda(x), x.dtype
+    T, H = x.shape
+    if gate.dim() != 3:
+        raise ValueError("gate must be [E, I, H]")
+    E, I, _ = gate.shape
+    f8 = gate_scales is not None or up_scales is not None or down_scales is not None
+    wdt = _F8 if f8 else dt
+    xp = _dense("x", x, (T, H), dt, dev)
+    e = FewExperts(_dense("gate", gate, (E, I, H), wdt, dev), _dense("up", up, (E, I, H), wdt, dev),
+                   _dense("down", down, (E, H, I), wdt, dev))
+    if f8:
+        if gate_scales is None or up_scales is None or down_scales is None:
+            raise ValueError("give all three scales, or none")
+        h, i, f32 = _blocks(H), _blocks(I), torch.float32
+        e.gate_scales = _dense("gate_scales", gate_scales, (E, i, h), f32, dev)
+        e.up_scales = _dense("up_scales", up_scales, (E, i, h), f32, dev)
+        e.down_scales = _dense("down_scales", down_scales, (E, h, i), f32, dev)
+    if y is None:
+        y = _empty((T, H), dt, x, stream)
+    yp = _dense("y", y, (T, H), dt, dev)
+    if workspace is None:
+        workspace = _empty((T * top_k * I * dt.itemsize + 255) & -256, torch.uint8, x, stream)
+    elif not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous on cuda:{dev}")
+    _enqueue(name, dev, stream, xp, _code(dt), *routing(dev, T, E), ctypes.byref(e), T, H, I, E, top_k, *tail,
+             yp, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    return y
+
+
+def moe_forward_few(x: torch.Tensor, logits: torch.Tensor, gate: torch.Tensor, up: torch.Tensor,
+                    down: torch.Tensor, top_k: int, renormalize: bool, gate_scales=None, up_scales=None,
+                    down_scales=None, y=None, workspace=None, stream=None) -> torch.Tensor:
+    """:func:`moe_forward` for at most 32 tokens, in two kernels. ``gate, up
+    [E, I, H]`` and ``down [E, H, I]`` in x's dtype, or float8_e4m3fn with the scales
+    of :func:`moe_quantize_weights` (x in bfloat16 or float16). Returns ``y [T, H]``.
+    The workspace (:func:`moe_forward_few_workspace_size` bytes) must not be shared by
+    calls that overlap."""
+    def routing(dev, T, E):
+        return _dense("logits", logits, (T, E), logits.dtype, dev), _code(logits.dtype)
+    return _forward_few("moe_forward_few", x, routing, int(top_k), gate, up, down, gate_scales, up_scales,
+                        down_scales, y, workspace, stream, (int(bool(renormalize)),))
+
+
+def moe_forward_few_routed(x: torch.Tensor, expert_indices: torch.Tensor, weights: torch.Tensor,
+                           gate: torch.Tensor, up: torch.Tensor, down: torch.Tensor, gate_scales=None,
+                           up_scales=None, down_scales=None, y=None, workspace=None,
+                           stream=None) -> torch.Tensor:
+    """:func:`moe_forward_few` from a routing made before: ``expert_indices``
+    (int32 ``[T, k]``) and ``weights`` (``[T, k]`` in any float type), for example
+    :func:`moe_route_sigmoid_grouped`'s. An index outside ``[0, E)`` makes the token's
+    row NaN and sets the device status."""
+    top_k = expert_indices.shape[-1]
+
+    def routing(dev, T, E):
+        return (_dense("expert_indices", expert_indices, (T, top_k), torch.int32, dev),
+                _dense("weights", weights, (T, top_k), weights.dtype, dev), _code(weights.dtype))
+    return _forward_few("moe_forward_few_routed", x, routing, top_k, gate, up, down, gate_scales, up_scales,
+                        down_scales, y, workspace, stream, ())

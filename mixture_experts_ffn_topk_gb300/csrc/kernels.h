@@ -240,4 +240,56 @@ cudaError_t launch_swiglu_checkpoint_backward(int dt, const void *grad_h, int64_
                                               int64_t I, void *grad_g, void *grad_u, int64_t ldg,
                                               void *h, int64_t ldh, cudaStream_t s);
 
+// Rows, SwiGLU activations and expert matrices in e4m3 codes with an FP32 scale per
+// block of 128 columns (matrices: 128 x 128). end: offsets + E, or nullptr for all
+// rows; rows of x, g and u lie ld elements apart, rows of codes ldc bytes.
+cudaError_t launch_quantize_rows(int dt, const void *x, int64_t ld, const int32_t *end, int64_t rows,
+                                 int64_t K, uint8_t *codes, int64_t ldc, float *scales, cudaStream_t s);
+cudaError_t launch_swiglu_quantize(int dt, const void *g, const void *u, int64_t ld, const int32_t *end,
+                                   int64_t rows, int64_t I, uint8_t *codes, int64_t ldc, float *scales,
+                                   cudaStream_t s);
+cudaError_t launch_quantize_weights(int dt, const void *w, int64_t E, int64_t N, int64_t K,
+                                    uint8_t *codes, float *scales, cudaStream_t s);
+
+// Grouped product of such rows and matrices ([E, N, K], transposed: [E, K, N]) on
+// tcgen05 (cudaErrorInvalidValue: a tensor map was refused).
+struct GroupedF8 {
+    const uint8_t *a;
+    int64_t lda;
+    const float *a_scales;
+    const int32_t *offsets;
+    int64_t rows;
+    const uint8_t *w;
+    const float *w_scales;
+    int E;
+    int64_t N, K;
+    bool transposed;
+    void *out;
+    int64_t ldo;
+    int out_dt;
+};
+cudaError_t launch_grouped_gemm_f8(const GroupedF8 &g, unsigned *status, cudaStream_t s);
+
+// The whole layer for a few tokens in two kernels. Routing from logits, or (logits
+// NULL) from indices and weights. gate_scales, up_scales, down_scales: NULL, or the
+// weights are e4m3 codes with these scales per 128 x 128 block.
+constexpr int kFewMaxTokens = 32, kFewMaxTopK = 32;
+constexpr size_t kFewSharedBytes = 200 << 10;        // of a CTA at most
+struct FewArgs {
+    const void *x;
+    const void *logits;
+    const uint32_t *indices;
+    const void *weights;
+    const void *gate, *up, *down;
+    const float *gate_scales, *up_scales, *down_scales;
+    void *h;                     // [T * top_k, I], scratch
+    void *y;
+    unsigned *status;
+    int ldt, wdt;                // types of logits and weights
+    int T, E, top_k, renormalize, H, I;
+};
+cudaError_t launch_few_f32(const FewArgs &a, cudaStream_t s);
+cudaError_t launch_few_bf16(const FewArgs &a, cudaStream_t s);
+cudaError_t launch_few_f16(const FewArgs &a, cudaStream_t s);
+
 }  // namespace moe

@@ -91,6 +91,7 @@ constexpr uint64_t kMaxWaitLimitNs = 60ull * 1000000000ull;   // moe_set_wait_li
 constexpr int64_t kMaxRows = 0x7fffffff;   // dispatched rows are int32
 constexpr int64_t kMaxGroupedRows = 0x7fffffff - 1023;   // rows round up to a unit in int32
 constexpr int64_t kMaxGroupedDim = 1 << 24;      // N, K, I of the grouped products and checkpoints
+constexpr int64_t kMaxFewDim = 1 << 20;         // H, I of the few-token forward
 constexpr int64_t kMaxStride = int64_t(1) << 32; // their row strides (a TMA stride is below 2^40 bytes)
 
 // Vector width rule shared by the experts and combine kernels: rows are moved
@@ -1121,6 +1122,201 @@ int moe_swiglu_checkpoint_backward(const void *grad_h, int64_t ld, const void *c
         dtype, grad_h, ld, ckpt, offsets ? offsets + E : nullptr, rows, I, grad_g, grad_u, ldg, h, ldh,
         static_cast<cudaStream_t>(stream));
     return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_swiglu_checkpoint_backward");
+}
+
+constexpr int64_t kBlockCols = 128;     // columns that share a scale
+
+static int64_t blocks_of(int64_t n) { return (n + kBlockCols - 1) / kBlockCols; }
+
+static int check_quantize_args(int64_t rows, int64_t K, int dt, const int32_t *offsets, int64_t E,
+                               int64_t ld, int64_t ldc)
+{
+    if (!valid_dtype(dt)) return fail(MOE_ERR_DTYPE, "dtype must be F32, BF16 or F16");
+    if (rows < 0 || rows > kMaxGroupedRows || K < 1 || K > kMaxGroupedDim)
+        return fail(MOE_ERR_SHAPE, "need 0 <= rows <= 2^31 - 1024 and 1 <= columns <= 2^24");
+    if (offsets != nullptr && (E < 1 || E > kMaxE)) return fail(MOE_ERR_SHAPE, "need 1 <= E <= 1024");
+    if (ld < K || ld > kMaxStride || ldc < K || ldc > kMaxStride)
+        return fail(MOE_ERR_SHAPE, "row strides must be >= the columns");
+    return MOE_OK;
+}
+
+// The rows need their elements' alignment, the offsets and scales 16 bytes.
+static int check_quantize_ptrs(const char *name, int dt, const int32_t *offsets, const void *scales,
+                               const void *codes, std::initializer_list<const void *> rows)
+{
+    if (!codes || !scales) return fail(MOE_ERR_NULL, name);
+    for (const void *q : rows)
+        if (!q) return fail(MOE_ERR_NULL, name);
+    for (const void *q : rows)
+        if (reinterpret_cast<uintptr_t>(q) % elem_bytes(dt)) return fail(MOE_ERR_ALIGN, name);
+    if (!aligned16(scales) || (offsets != nullptr && !aligned16(offsets))) return fail(MOE_ERR_ALIGN, name);
+    return MOE_OK;
+}
+
+int moe_quantize_rows(const void *x, int64_t ld, const int32_t *offsets, int64_t E, int64_t rows,
+                      int64_t K, int dtype, uint8_t *codes, int64_t ldc, float *scales, void *stream)
+{
+    const NvtxRange nvtx("moe_quantize_rows");
+    int rc = check_quantize_args(rows, K, dtype, offsets, E, ld, ldc);
+    if (rc != MOE_OK || rows == 0) return rc;
+    rc = check_quantize_ptrs("moe_quantize_rows: tensors must be non-NULL and aligned", dtype, offsets,
+                             scales, codes, {x});
+    if (rc != MOE_OK) return rc;
+    cudaError_t err = launch_quantize_rows(dtype, x, ld, offsets ? offsets + E : nullptr, rows, K, codes,
+                                           ldc, scales, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_quantize_rows");
+}
+
+int moe_swiglu_quantize(const void *g, const void *u, int64_t ld, const int32_t *offsets, int64_t E,
+                        int64_t rows, int64_t I, int dtype, uint8_t *codes, int64_t ldc,
+                        float *scales, void *stream)
+{
+    const NvtxRange nvtx("moe_swiglu_quantize");
+    int rc = check_quantize_args(rows, I, dtype, offsets, E, ld, ldc);
+    if (rc != MOE_OK || rows == 0) return rc;
+    rc = check_quantize_ptrs("moe_swiglu_quantize: tensors must be non-NULL and aligned", dtype, offsets,
+                             scales, codes, {g, u});
+    if (rc != MOE_OK) return rc;
+    cudaError_t err = launch_swiglu_quantize(dtype, g, u, ld, offsets ? offsets + E : nullptr, rows, I,
+                                             codes, ldc, scales, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_swiglu_quantize");
+}
+
+int moe_quantize_weights(const void *w, int64_t E, int64_t N, int64_t K, int dtype, uint8_t *codes,
+                         float *scales, void *stream)
+{
+    const NvtxRange nvtx("moe_quantize_weights");
+    if (!valid_dtype(dtype)) return fail(MOE_ERR_DTYPE, "dtype must be F32, BF16 or F16");
+    if (E < 1 || E > kMaxE || N < 1 || K < 1 || N > kMaxGroupedDim || K > kMaxGroupedDim)
+        return fail(MOE_ERR_SHAPE, "need 1 <= E <= 1024 and 1 <= N, K <= 2^24");
+    if (E * blocks_of(N) * blocks_of(K) > 0x7fffffff) return fail(MOE_ERR_SHAPE, "more than 2^31 - 1 blocks");
+    const int rc = check_quantize_ptrs("moe_quantize_weights: tensors must be non-NULL and aligned", dtype,
+                                       nullptr, scales, codes, {w});
+    if (rc != MOE_OK) return rc;
+    cudaError_t err = launch_quantize_weights(dtype, w, E, N, K, codes, scales, static_cast<cudaStream_t>(stream));
+    return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_quantize_weights");
+}
+
+int moe_grouped_gemm_f8(const uint8_t *a, int64_t lda, const float *a_scales, const int32_t *offsets,
+                        int64_t rows, const uint8_t *w, const float *w_scales, int weight_layout,
+                        int64_t E, int64_t N, int64_t K, void *out, int64_t ldo, int out_dtype,
+                        void *stream)
+{
+    const NvtxRange nvtx("moe_grouped_gemm_f8");
+    int rc = check_grouped_args(rows, E, N, K, out_dtype, out_dtype);
+    if (rc != MOE_OK) return rc;
+    const bool kn = weight_layout == MOE_WEIGHT_KN;
+    if (!kn && weight_layout != MOE_WEIGHT_NK)
+        return fail(MOE_ERR_VALUE, "weight_layout must be MOE_WEIGHT_NK or MOE_WEIGHT_KN");
+    if (K % 16 != 0 || (kn && N % 16 != 0))
+        return fail(MOE_ERR_SHAPE, "K, and N of [E, K, N] weights, must be multiples of 16");
+    if (lda < K || lda % 16 != 0 || lda > kMaxStride)
+        return fail(MOE_ERR_SHAPE, "lda must be >= K and a multiple of 16");
+    if (ldo < N || ldo > kMaxStride) return fail(MOE_ERR_SHAPE, "ldo must be >= N");
+    if (rows == 0) return MOE_OK;
+    rc = check_experts_ptrs("moe_grouped_gemm_f8: tensors must be non-NULL and 16-byte aligned",
+                            {a, a_scales, offsets, w, w_scales, out});
+    if (rc != MOE_OK) return rc;
+    unsigned *st = status_ptr();
+    if (!st) return fail(MOE_ERR_CUDA, "cannot resolve the device status word");
+    const GroupedF8 g{a, lda, a_scales, offsets, rows, w, w_scales, (int)E, N, K, kn, out, ldo, out_dtype};
+    cudaError_t err = launch_grouped_gemm_f8(g, st, static_cast<cudaStream_t>(stream));
+    if (err == cudaErrorInvalidValue) return fail(MOE_ERR_SHAPE, "TMA descriptor rejected (matrix too large)");
+    return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_grouped_gemm_f8");
+}
+
+// Sizes of the few-token forward; the workspace holds h.
+static size_t few_workspace(int64_t T, int64_t I, int top_k, int dt)
+{
+    return round_up((size_t)T * (size_t)top_k * (size_t)I * elem_bytes(dt), 256);
+}
+
+size_t moe_forward_few_workspace_size(int64_t T, int64_t I, int top_k, int dtype)
+{
+    if (T < 1 || T > kFewMaxTokens || I < 1 || I > kMaxFewDim || top_k < 1 || top_k > kFewMaxTopK ||
+        !valid_dtype(dtype))
+        return 0;
+    return few_workspace(T, I, top_k, dtype);
+}
+
+static int forward_few(const char *name, const void *x, int dtype, const void *logits, int logits_dtype,
+                       const uint32_t *indices, const void *weights, int weights_dtype,
+                       const moe_few_experts *experts, int64_t T, int64_t H, int64_t I, int64_t E,
+                       int top_k, int renormalize, void *y, void *workspace, size_t workspace_bytes,
+                       void *stream)
+{
+    if (!valid_dtype(dtype)) return fail(MOE_ERR_DTYPE, "dtype must be F32, BF16 or F16");
+    if (!valid_dtype(logits_dtype) || !valid_dtype(weights_dtype))
+        return fail(MOE_ERR_DTYPE, "the logits' or routing weights' dtype must be F32, BF16 or F16");
+    if (!experts) return fail(MOE_ERR_NULL, name);
+    const bool f8 = experts->gate_scales || experts->up_scales || experts->down_scales;
+    if (f8 && dtype == MOE_F32) return fail(MOE_ERR_DTYPE, "8-bit weights need BF16 or F16 activations");
+    if (T < 0 || T > kFewMaxTokens) return fail(MOE_ERR_SHAPE, "need 0 <= T <= 32");
+    if (E < 1 || E > kMaxE || top_k < 1 || top_k > E || top_k > kFewMaxTopK)
+        return fail(MOE_ERR_SHAPE, "need 1 <= E <= 1024 and 1 <= top_k <= min(E, 32)");
+    const int64_t mult = f8 ? 16 : 16 / (int64_t)elem_bytes(dtype);
+    if (H < 1 || I < 1 || H > kMaxFewDim || I > kMaxFewDim || H % mult != 0 || I % mult != 0)
+        return fail(MOE_ERR_SHAPE, "H and I must be multiples of 16 bytes of weights, and at most 2^20");
+    if (T == 0) return MOE_OK;
+    const void *routing = logits ? logits : weights;
+    int rc = check_experts_ptrs(name, {x, routing, logits ? logits : indices, experts->gate, experts->up,
+                                       experts->down, y});
+    if (rc == MOE_OK && f8)
+        rc = check_experts_ptrs(name, {experts->gate_scales, experts->up_scales, experts->down_scales});
+    if (rc != MOE_OK) return rc;
+    if (!workspace || workspace_bytes < few_workspace(T, I, top_k, dtype) ||
+        (reinterpret_cast<uintptr_t>(workspace) & 255u))
+        return fail(MOE_ERR_WORKSPACE, "few-token workspace too small or not 256-byte aligned");
+    FewArgs a{};
+    a.x = x;
+    a.logits = logits;
+    a.indices = indices;
+    a.weights = weights;
+    a.gate = experts->gate;
+    a.up = experts->up;
+    a.down = experts->down;
+    a.gate_scales = experts->gate_scales;
+    a.up_scales = experts->up_scales;
+    a.down_scales = experts->down_scales;
+    a.h = workspace;
+    a.y = y;
+    a.status = status_ptr();
+    if (!a.status) return fail(MOE_ERR_CUDA, "cannot resolve the device status word");
+    a.ldt = logits_dtype;
+    a.wdt = weights_dtype;
+    a.T = (int)T;
+    a.E = (int)E;
+    a.top_k = top_k;
+    a.renormalize = renormalize;
+    a.H = (int)H;
+    a.I = (int)I;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t err = dtype == MOE_F32 ? launch_few_f32(a, s) : dtype == MOE_BF16 ? launch_few_bf16(a, s)
+                                                                                 : launch_few_f16(a, s);
+    return err == cudaSuccess ? MOE_OK : cuda_fail(err, "moe_forward_few");
+}
+
+int moe_forward_few(const void *x, int dtype, const void *logits, int logits_dtype,
+                    const moe_few_experts *experts, int64_t T, int64_t H, int64_t I, int64_t E,
+                    int top_k, int renormalize, void *y, void *workspace, size_t workspace_bytes,
+                    void *stream)
+{
+    const NvtxRange nvtx("moe_forward_few");
+    if (T > 0 && !logits) return fail(MOE_ERR_NULL, "moe_forward_few: NULL logits");
+    return forward_few("moe_forward_few: tensors must be non-NULL and 16-byte aligned", x, dtype, logits,
+                       logits_dtype, nullptr, nullptr, MOE_F32, experts, T, H, I, E, top_k, renormalize, y,
+                       workspace, workspace_bytes, stream);
+}
+
+int moe_forward_few_routed(const void *x, int dtype, const uint32_t *expert_indices, const void *weights,
+                           int weights_dtype, const moe_few_experts *experts, int64_t T, int64_t H,
+                           int64_t I, int64_t E, int top_k, void *y, void *workspace,
+                           size_t workspace_bytes, void *stream)
+{
+    const NvtxRange nvtx("moe_forward_few_routed");
+    return forward_few("moe_forward_few_routed: tensors must be non-NULL and 16-byte aligned", x, dtype,
+                       nullptr, MOE_F32, expert_indices, weights, weights_dtype, experts, T, H, I, E, top_k,
+                       0, y, workspace, workspace_bytes, stream);
 }
 
 int moe_device_status(void *stream, int clear)
