@@ -32,6 +32,7 @@
 // Every wait is bounded (wait_ns); on expiry the kernel records ST_TIMEOUT, stops
 // issuing work, drains its own copies and MMAs, frees TMEM and exits.
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "grouped.cuh"
@@ -50,17 +51,20 @@ constexpr int RING_BYTES = 192 << 10;
 constexpr int MAX_STAGES = 10;
 constexpr int THREADS = 384;
 constexpr int EPI_WARPS = 8;
-constexpr int STG_BYTES = 4096;          // one epilogue staging buffer
+constexpr int STG_ROWS = 8;              // rows staged at a time
+constexpr int STG_F32_ROW = 528;         // bytes of a staged row: 16 more than 128 FP32 values
+constexpr int STG_BYTES = STG_ROWS * STG_F32_ROW;    // a group's buffer; in 16 bits two halves of it
 constexpr int PAIR_CAP = 256, SINGLE_CAP = 64;       // rows of a unit at most
-constexpr int SCALE_STAGES = 4;
+constexpr int SCALE_STAGES = 3, SCALE_KB = 4;        // scales are staged for four blocks at a time
 constexpr int MAX_ACCS = 4;
 constexpr int PARTIAL_BYTES = SINGLE_CAP * BM * 4;
 constexpr uint64_t kDrainLimitNs = 100000000ull;
 
 struct __align__(1024) Smem {
     uint8_t ring[RING_BYTES];
-    uint8_t stg[2][2][STG_BYTES];        // two per group of epilogue warps
-    float scale[SCALE_STAGES][PAIR_CAP];
+    uint8_t stg[2][STG_BYTES];           // one per group of epilogue warps
+    float scale[SCALE_STAGES][SCALE_KB][PAIR_CAP];
+    float w_scale[SCALE_STAGES][SCALE_KB];
     uint64_t full[MAX_STAGES];
     uint64_t empty[MAX_STAGES];
     uint64_t acc_full[MAX_ACCS];
@@ -119,6 +123,14 @@ __device__ __forceinline__ void umma_f8_on(uint32_t on, uint32_t d, uint64_t ade
             : "memory");
 }
 
+// Arrives on a barrier of the pair's other CTA. The default scope: what the barrier
+// orders is tensor memory, by the tcgen05 fences on both sides, and a release at
+// cluster scope, a full memory barrier, cost a microsecond per block.
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_addr)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
 // Instruction descriptor, kind::f8f6f4: FP32 accumulator, A and B e4m3 (0), A
 // MN-major where a_mn, N >> 3 at bit 17, M >> 4 at bit 24.
 __host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn)
@@ -134,8 +146,60 @@ __device__ __forceinline__ void fma2(uint64_t &sum, uint32_t v0, uint32_t v1, ui
         : "r"(v0), "r"(v1), "l"(s));
 }
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 __device__ __forceinline__ float low(uint64_t v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float high(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+
+// 16 TMEM lanes x 32 consecutive fp32 columns as blocks of 8 x 8: thread T holds
+// lanes T / 4 (r[4 i], r[4 i + 1]) and T / 4 + 8 (r[4 i + 2], r[4 i + 3]), columns
+// 8 i + 2 (T % 4) and the next.
+__device__ __forceinline__ void tmem_ld_blocks32(uint32_t taddr, uint32_t (&r)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+
+// Stores four 8 x 8 blocks of 16-bit values, one register each, transposed; the
+// lanes 8 m .. 8 m + 7 give the addresses of block m's eight rows of 16 bytes.
+__device__ __forceinline__ void store_blocks_transposed(uint32_t saddr, uint32_t r0, uint32_t r1, uint32_t r2,
+                                                        uint32_t r3)
+{
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(r0),
+                 "r"(r1), "r"(r2), "r"(r3)
+                 : "memory");
+}
+
+// 4 bytes of global memory into shared memory, asynchronously.
+__device__ __forceinline__ void copy4_async(float *dst, const float *src)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// This thread's copies so far arrive on the barrier when they have landed.
+__device__ __forceinline__ void copies_arrive(uint64_t *bar)
+{
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// warp_wait on two barriers whose phases may well be complete: both are asked at once.
+__device__ __forceinline__ bool warp_wait_both(uint64_t *a, uint32_t pa, uint64_t *b, uint32_t pb,
+                                               volatile int *abort_flag, unsigned *status, uint64_t limit_ns)
+{
+    const bool ok_a = mbar_try_wait(a, pa), ok_b = mbar_try_wait(b, pb);
+    if (__all_sync(0xffffffffu, ok_a && ok_b)) return true;
+    return warp_wait<1>(a, pa, abort_flag, status, limit_ns) && warp_wait<1>(b, pb, abort_flag, status, limit_ns);
+}
 
 template <int CG, bool KN, bool OUT_F32, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
@@ -160,7 +224,7 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) { mbar_init(&S.full[s], 1); mbar_init(&S.empty[s], 1); }
         for (int a = 0; a < ACCS; ++a) { mbar_init(&S.acc_full[a], 1); mbar_init(&S.acc_empty[a], EPI_WARPS * CG); }
-        for (int s = 0; s < SCALE_STAGES; ++s) { mbar_init(&S.scale_full[s], 1); mbar_init(&S.scale_empty[s], EPI_WARPS); }
+        for (int s = 0; s < SCALE_STAGES; ++s) { mbar_init(&S.scale_full[s], 32); mbar_init(&S.scale_empty[s], EPI_WARPS); }
         mbar_init(&S.drain, 1);
         S.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -201,7 +265,7 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 // barrier, which expects them all
                 const uint32_t bytes = CG * (W_BYTES + u.mma_n / CG * BK);
                 for (int kb = kb_begin; kb < kb_end; ++kb) {
-                    ok = warp_wait<CG>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns);
+                    ok = warp_wait<1>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns);
                     if (!ok) break;
                     const uint32_t here = smem_u32(&S.full[stage]), bar = CG == 2 ? mapa_shared(here, 0) : here;
                     expect_tx_on(arm, &S.full[stage], bytes);
@@ -222,7 +286,7 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 const int mine = u.mma_n / CG;               // rows this CTA loads
                 const int row0 = u.row0 + rank * mine;
                 for (int kb = kb_begin; kb < kb_end; ++kb) {
-                    ok = warp_wait<CG>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns);
+                    ok = warp_wait<1>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns);
                     if (!ok) break;
                     const uint32_t sa = ring + stage * p.slot_bytes + W_BYTES, here = smem_u32(&S.full[stage]);
                     const uint32_t bar = CG == 2 ? mapa_shared(here, 0) : here;
@@ -249,8 +313,8 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 const Unit u = walk.at(unit);
                 const uint32_t idesc = idesc0 | ((uint32_t)(u.mma_n >> 3) << 17);
                 for (int kb = kb_begin; kb < kb_end; ++kb) {
-                    ok = warp_wait<CG>(&S.acc_empty[acc], acc_phase ^ 1u, abort_flag, p.status, p.wait_ns) &&
-                         warp_wait<CG>(&S.full[stage], phase, abort_flag, p.status, p.wait_ns);
+                    ok = warp_wait_both(&S.acc_empty[acc], acc_phase ^ 1u, &S.full[stage], phase, abort_flag,
+                                        p.status, p.wait_ns);
                     if (!ok) break;
                     tc_fence_after();
                     const uint32_t d = tmem_base + (uint32_t)(acc * CAP);
@@ -274,45 +338,31 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             __syncwarp();
         } else if (warp == 3) {
             // ------------------------------------------------------ scales
-            constexpr int PER = CAP / 32;
-            const int n_blocks = (p.N + BM - 1) / BM;
-            int unit = unit0, kb = kb_begin, stage = 0;
+            // of the unit's rows, four blocks at a time: four lanes to a row
+            const int n_blocks = (p.N + BM - 1) / BM, k = lane & 3;
+            int stage = 0;
             uint32_t phase = 0;
-            Unit u = {};
-            // the scales of the next block: one block is loaded ahead of the one stored
-            auto next = [&](float (&v)[PER], float &w) {
-                if (kb >= kb_end) { kb = kb_begin; unit += unit_step; }
-                if (unit >= total || kb >= kb_end) return false;
-                if (kb == kb_begin) u = walk.at(unit);
-                const int nb = u.w0 / BM;
-                w = nb < n_blocks
-                        ? __ldg(p.w_scales + (KN ? ((int64_t)u.e * all_kb + kb) * n_blocks + nb
-                                                 : ((int64_t)u.e * n_blocks + nb) * all_kb + kb))
-                        : 0.0f;
-                const float *s = p.a_scales + (int64_t)u.row0 * all_kb + kb;
-#pragma unroll
-                for (int i = 0; i < PER; ++i)
-                    v[i] = i * 32 + lane < u.rows ? __ldg(s + (int64_t)(i * 32 + lane) * all_kb) : 0.0f;
-                ++kb;
-                return true;
-            };
-            auto put = [&](const float (&v)[PER], float w) {
-                if (!warp_wait<1>(&S.scale_empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns)) return false;
-#pragma unroll
-                for (int i = 0; i < PER; ++i) S.scale[stage][i * 32 + lane] = v[i] * w;
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.scale_full[stage]);
-                if (++stage == SCALE_STAGES) { stage = 0; phase ^= 1u; }
-                return true;
-            };
-            float v0[PER], v1[PER], w0, w1;
-            bool more = next(v0, w0);
-            while (more) {
-                const bool second = next(v1, w1);
-                if (!put(v0, w0) || !second) break;
-                more = next(v0, w0);
-                if (!put(v1, w1)) break;
+            bool ok = true;
+            for (int unit = unit0; unit < total && ok; unit += unit_step) {
+                const Unit u = walk.at(unit);
+                const int nb = u.w0 / BM < n_blocks ? u.w0 / BM : 0;     // columns past N are not stored
+                for (int kb = kb_begin; kb < kb_end; kb += SCALE_KB) {
+                    ok = warp_wait<1>(&S.scale_empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns);
+                    if (!ok) break;
+                    if (kb + k < kb_end) {
+                        const float *src = p.a_scales + (int64_t)(u.row0 + lane / 4) * all_kb + kb + k;
+                        float *dst = &S.scale[stage][k][lane / 4];
+                        for (int r = lane / 4; r < u.rows; r += 8, dst += 8, src += 8 * all_kb) copy4_async(dst, src);
+                        if (lane < 4)
+                            copy4_async(&S.w_scale[stage][k],
+                                        p.w_scales + (KN ? ((int64_t)u.e * all_kb + kb + k) * n_blocks + nb
+                                                         : ((int64_t)u.e * n_blocks + nb) * all_kb + kb + k));
+                    }
+                    copies_arrive(&S.scale_full[stage]);
+                    if (++stage == SCALE_STAGES) { stage = 0; phase ^= 1u; }
+                }
             }
+            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else {
         // ------------------------------------------------------ epilogue
@@ -320,106 +370,133 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         const int q = warp & 3;                          // TMEM lane quadrant of this warp
         const int group = warp >= 8 ? 1 : 0;
         const int tid = threadIdx.x - (group ? 256 : 128);    // 0..127 in the group
-        constexpr int CHUNKS = CAP / 32;                 // 16 columns each
-        constexpr int CH = OUT_F32 ? 8 : 16;             // rows per staging buffer
-        constexpr int ESZ = OUT_F32 ? 4 : 2;
-        constexpr int ROW_BYTES = BM * ESZ;              // staged bytes per row: 512 / 256
-        constexpr int PIECES = ROW_BYTES / 16, PER_IT = 128 / PIECES;
-        int acc = 0, stage = 0, buf = 0;
+        constexpr int CHUNKS = CAP / 64;                 // of 32 columns, per group
+        int acc = 0, stage = 0;
         uint32_t acc_phase = 0, phase = 0;
-        const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16);
+        const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16) + group * 32;
         for (int unit = unit0; unit < total; unit += unit_step) {
             const Unit u = walk.at(unit);
-            // this group's chunks: rows [16 (2 j + group), + 16)
-            const int chunks = u.rows > group * 16 ? (u.rows - group * 16 + 31) / 32 : 0;
-            uint64_t sums[CHUNKS][8];                  // two rows each
+            // this group's columns: 32 from each 64 (2 j + group) on. Of a chunk a thread
+            // has lanes lane / 4 + 8 m (m = 2 h + e) and columns 8 i + 2 (lane % 4) and the
+            // next: sums[j][h][2 i + e], a pair each
+            uint64_t sums[CHUNKS][2][8];
 #pragma unroll
             for (int j = 0; j < CHUNKS; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sums[j][i] = 0;
-            bool ok = true;
-            for (int kb = kb_begin; kb < kb_end; ++kb) {
-                ok = warp_wait<CG>(&S.acc_full[acc], acc_phase, abort_flag, p.status, p.wait_ns) &&
-                     warp_wait<1>(&S.scale_full[stage], phase, abort_flag, p.status, p.wait_ns);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t tbase = tlane + (uint32_t)(acc * CAP + group * 16);
-                const float *sc = S.scale[stage] + group * 16;
-                auto release = [&] {
+                for (int i = 0; i < 16; ++i) sums[j][i / 8][i % 8] = 0;
+            // NJ of the chunks hold rows: no branch between a chunk's loads and the
+            // additions of the one before
+            auto add_blocks = [&](auto nj) {
+                constexpr int NJ = decltype(nj)::value;
+                for (int kb = kb_begin; kb < kb_end; ++kb) {
+                    const int k = (kb - kb_begin) % SCALE_KB;
+                    bool ok = warp_wait<1>(&S.acc_full[acc], acc_phase, abort_flag, p.status, p.wait_ns);
+                    if (k == 0) ok = ok && warp_wait<1>(&S.scale_full[stage], phase, abort_flag, p.status, p.wait_ns);
+                    if (!ok) return false;
+                    tc_fence_after();
+                    const uint32_t tbase = tlane + (uint32_t)(acc * CAP);
+                    const float *sc = S.scale[stage][k] + group * 32 + 2 * (lane & 3);
+                    const float w = S.w_scale[stage][k];
+                    const uint64_t w2 = (uint64_t)__float_as_uint(w) << 32 | __float_as_uint(w);
+                    uint32_t v[2][16];
+                    if constexpr (NJ > 0) tmem_ld_blocks32(tbase, v[0]);
+#pragma unroll
+                    for (int j = 0; j < NJ; ++j) {
+                        uint64_t s2[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            s2[i] = mul2(*reinterpret_cast<const uint64_t *>(sc + j * 64 + i * 8), w2);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            tmem_ld_wait16(v[h]);
+                            if (h == 0) tmem_ld_blocks32(tbase + j * 64 + (16u << 16), v[1]);
+                            else if (j + 1 < NJ) tmem_ld_blocks32(tbase + (j + 1) * 64, v[0]);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                fma2(sums[j][h][2 * i], v[h][4 * i], v[h][4 * i + 1], s2[i]);
+                                fma2(sums[j][h][2 * i + 1], v[h][4 * i + 2], v[h][4 * i + 3], s2[i]);
+                            }
+                        }
+                    }
                     tc_fence_before();
                     __syncwarp();
+                    const bool last = k == SCALE_KB - 1 || kb + 1 == kb_end;
                     if (lane == 0) {
-                        if (CG == 2 && !leader) mbar_arrive_cluster(mapa_shared(smem_u32(&S.acc_empty[acc]), 0));
+                        if (CG == 2 && !leader) arrive_remote(mapa_shared(smem_u32(&S.acc_empty[acc]), 0));
                         else mbar_arrive(&S.acc_empty[acc]);
+                        if (last) mbar_arrive(&S.scale_empty[stage]);
                     }
-                };
-                // a chunk is on its way while the one before is added up
-                uint32_t v[2][16];
-                if (chunks > 0) tmem_ld16(tbase, v[0]);
-                else release();
-#pragma unroll
-                for (int j = 0; j < CHUNKS; ++j) {
-                    if (j >= chunks) continue;
-                    tmem_ld_wait16(v[j & 1]);
-                    if (j + 1 < CHUNKS && j + 1 < chunks) tmem_ld16(tbase + (j + 1) * 32, v[(j + 1) & 1]);
-                    else release();
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const ulonglong2 s = *reinterpret_cast<const ulonglong2 *>(sc + j * 32 + i * 4);
-                        fma2(sums[j][2 * i], v[j & 1][4 * i], v[j & 1][4 * i + 1], s.x);
-                        fma2(sums[j][2 * i + 1], v[j & 1][4 * i + 2], v[j & 1][4 * i + 3], s.y);
-                    }
+                    if (last && ++stage == SCALE_STAGES) { stage = 0; phase ^= 1u; }
+                    if (++acc == ACCS) { acc = 0; acc_phase ^= 1u; }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&S.scale_empty[stage]);
-                if (++stage == SCALE_STAGES) { stage = 0; phase ^= 1u; }
-                if (++acc == ACCS) { acc = 0; acc_phase ^= 1u; }
+                return true;
+            };
+            bool ok;
+            const int nj = u.rows > group * 32 ? (u.rows - group * 32 + 63) / 64 : 0;
+            if constexpr (CHUNKS == 1) {
+                ok = nj == 0 ? add_blocks(std::integral_constant<int, 0>()) : add_blocks(std::integral_constant<int, 1>());
+            } else {
+                ok = nj == 4   ? add_blocks(std::integral_constant<int, 4>())
+                     : nj == 3 ? add_blocks(std::integral_constant<int, 3>())
+                     : nj == 2 ? add_blocks(std::integral_constant<int, 2>())
+                     : nj == 1 ? add_blocks(std::integral_constant<int, 1>())
+                               : add_blocks(std::integral_constant<int, 0>());
             }
             if constexpr (SPLIT) {
                 // the partial sums stay here, [row][n] in FP32
-                float *mine = reinterpret_cast<float *>(S.ring + RING_BYTES - PARTIAL_BYTES) + q * 32 + lane;
+                float *mine = reinterpret_cast<float *>(S.ring + RING_BYTES - PARTIAL_BYTES) + q * 32 + lane / 4;
 #pragma unroll
-                for (int j = 0; j < CHUNKS; ++j)
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const int t = j * 32 + group * 16 + 2 * i;
-                        mine[t * BM] = low(sums[j][i]);
-                        mine[(t + 1) * BM] = high(sums[j][i]);
+                        const int t = group * 32 + i / 2 * 8 + 2 * (lane & 3), n = h * 16 + (i & 1) * 8;
+                        mine[t * BM + n] = low(sums[0][h][i]);
+                        mine[(t + 1) * BM + n] = high(sums[0][h][i]);
                     }
                 continue;
             }
             // a group's warps leave together: none may wait at a barrier for
             // one that has given up
             if (!epi_all(1 + group, ok)) break;
+            constexpr int ESZ = OUT_F32 ? 4 : 2, PIECES = BM * ESZ / 16, PER_IT = 128 / PIECES;
             const int piece = tid % PIECES, col = u.w0 + piece * (16 / ESZ);
             uint8_t *out0 = p.out + (int64_t)u.row0 * p.out_row_bytes + (int64_t)col * ESZ;
             const bool whole = p.vec && col + 16 / ESZ <= p.N;
 #pragma unroll
             for (int j = 0; j < CHUNKS; ++j) {
 #pragma unroll
-                for (int h = 0; h < 16 / CH; ++h) {
-                    const int t0 = j * 32 + group * 16 + h * CH;
+                for (int i = 0; i < 4; ++i) {
+                    const int t0 = j * 64 + group * 32 + i * 8;
                     if (t0 >= u.rows) continue;
-                    // CH rows through shared memory: a barrier per buffer, who passes
-                    // it has read the other one
-                    uint8_t *stg = S.stg[group][buf], *mine = stg + (q * 32 + lane) * ESZ;
+                    // eight rows through shared memory. 16 bits: the halves of the buffer
+                    // take turns, and who passes the barrier has read the other one; the
+                    // 16-byte pieces of row t are permuted by t, so that a block's eight
+                    // rows meet no bank twice
+                    uint8_t *stg = S.stg[group] + (OUT_F32 ? 0 : (i & 1) * (STG_ROWS * BM * 2));
+                    if constexpr (OUT_F32) {
+                        epi_sync(1 + group);
 #pragma unroll
-                    for (int i = 0; i < CH; ++i) {
-                        const uint64_t two = sums[j][(h * CH + i) / 2];
-                        const float f = i & 1 ? high(two) : low(two);
-                        if constexpr (OUT_F32) {
-                            *reinterpret_cast<float *>(mine + i * ROW_BYTES) = f;
-                        } else if (p.out_bf16) {
-                            *reinterpret_cast<__nv_bfloat16 *>(mine + i * ROW_BYTES) = __float2bfloat16_rn(f);
-                        } else {
-                            *reinterpret_cast<__half *>(mine + i * ROW_BYTES) = __float2half_rn(f);
+                        for (int m = 0; m < 4; ++m) {
+                            const uint64_t two = sums[j][m / 2][2 * i + (m & 1)];
+                            uint8_t *to = stg + 2 * (lane & 3) * STG_F32_ROW + (q * 32 + m * 8 + lane / 4) * 4;
+                            *reinterpret_cast<float *>(to) = low(two);
+                            *reinterpret_cast<float *>(to + STG_F32_ROW) = high(two);
                         }
+                    } else {
+                        auto block = [&](int m) {
+                            const uint64_t two = sums[j][m / 2][2 * i + (m & 1)];
+                            return p.out_bf16 ? float2_to_bf16x2(low(two), high(two)) : float2_to_f16x2(low(two), high(two));
+                        };
+                        const int t = lane & 7, at = q * 4 + (lane >> 3);
+                        store_blocks_transposed(smem_u32(stg + t * (BM * 2) + ((at ^ t) << 4)), block(0), block(1),
+                                                block(2), block(3));
                     }
                     epi_sync(1 + group);
 #pragma unroll
-                    for (int i = 0; i < CH / PER_IT; ++i) {
-                        const int t = i * PER_IT + tid / PIECES;
-                        const uint4 v = *reinterpret_cast<const uint4 *>(stg + t * ROW_BYTES + piece * 16);
+                    for (int r = 0; r < STG_ROWS / PER_IT; ++r) {
+                        const int t = r * PER_IT + tid / PIECES;
+                        const uint4 v = *reinterpret_cast<const uint4 *>(
+                            stg + (OUT_F32 ? t * STG_F32_ROW + piece * 16 : t * (BM * 2) + ((piece ^ (t & 7)) << 4)));
                         if (t0 + t >= u.rows) continue;
                         uint8_t *dst = out0 + (int64_t)(t0 + t) * p.out_row_bytes;
                         if (whole) {
@@ -434,7 +511,6 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                             }
                         }
                     }
-                    buf ^= 1;
                 }
             }
         }
