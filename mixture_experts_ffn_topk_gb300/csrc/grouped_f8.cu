@@ -8,26 +8,27 @@
 // block's is multiplied by its two scales and added up in FP32 registers, so no
 // sum in the accumulator has more than 128 terms.
 //
-// Transposed as in grouped_tc.cu, out^T = w a^T: the weights' n on the MMA's
-// fixed side (M = 128 per CTA), the expert's rows on the other (N = 16 .. 256).
-// A weight tile of 128 n has one scale per block, a row (a column of the
-// accumulator) its own: one product of scales per column and block, the same in
-// all lanes of a warp.
+// Two forms. Experts of many rows: grouped_f8_wide.cu. This file's is for few rows,
+// where the kernel streams weights. It is transposed as in grouped_tc.cu, out^T =
+// w a^T: the weights' n on the MMA's fixed side (M = 128), the expert's rows, at most
+// 64, on the other (N = 16 .. 64), so that one or two rows per expert cost a
+// 16-wide MMA. A weight tile of 128 n has one scale per block, a row (a column of the
+// accumulator) its own.
 //
 // Per CTA (one per SM, 384 threads, persistent over the units):
 //   warp 0   TMA producer of the weights: 128 n x 128 k (16 KiB) per stage;
 //   warp 2   TMA producer of the unit's rows x 128 k, into the same stages;
-//   warp 1   tcgen05.mma issuer, K = 32 per instruction, one accumulator per block,
-//            two of 256 columns (pairs) or four of 64 in turn;
-//   warp 3   the products of scales of each block, into a ring of their own;
-//   warps 4-7, 8-11  two groups that take every second 16 columns of each
-//            accumulator: TMEM lane = n, column = row of the segment; sums stay in
-//            registers until the last block.
-// CTA pairs (CG = 2): M = 256, each CTA holds its 128 weight columns and half of
-// the unit's rows; the even CTA issues the MMAs for both.
-// Few units: a cluster of 2, 4 or 8 single CTAs shares each unit's k (SPLIT), every
+//   warp 1   tcgen05.mma issuer, K = 32 per instruction, one accumulator of 64
+//            columns per block, four in turn;
+//   warp 3   the scales of four blocks at a time, copied into shared memory;
+//   warps 4-7, 8-11  epilogue, 32 columns each: TMEM is read in 8 x 8 blocks, in
+//            which a thread meets two of every eight columns, so that it fetches a
+//            quarter of the scales; sums stay in registers until the last block.
+// Few units: a cluster of 2, 4 or 8 CTAs shares each unit's k (SPLIT), every
 // CTA with its own blocks; the FP32 partial sums meet through distributed shared
 // memory, each CTA adding its share of the rows in rank order.
+//
+// Bound by HBM where experts have few rows.
 //
 // Every wait is bounded (wait_ns); on expiry the kernel records ST_TIMEOUT, stops
 // issuing work, drains its own copies and MMAs, frees TMEM and exits.
@@ -36,17 +37,13 @@
 
 #include "common.cuh"
 #include "grouped.cuh"
-#include "grouped_issue.cuh"
-#include "grouped_units.cuh"
+#include "grouped_f8.cuh"
 #include "kernels.h"
 
 namespace moe {
 
 namespace {
 
-constexpr int BK = 128;                  // k per stage: 128 bytes, one block of scales
-constexpr int UK = 32;                   // k per tcgen05.mma
-constexpr int W_BYTES = BM * BK;         // 16 KiB
 constexpr int RING_BYTES = 192 << 10;
 constexpr int MAX_STAGES = 10;
 constexpr int THREADS = 384;
@@ -54,21 +51,20 @@ constexpr int EPI_WARPS = 8;
 constexpr int STG_ROWS = 8;              // rows staged at a time
 constexpr int STG_F32_ROW = 528;         // bytes of a staged row: 16 more than 128 FP32 values
 constexpr int STG_BYTES = STG_ROWS * STG_F32_ROW;    // a group's buffer; in 16 bits two halves of it
-constexpr int PAIR_CAP = 256, SINGLE_CAP = 64;       // rows of a unit at most
+constexpr int CAP = 64;                  // rows of a unit at most
 constexpr int SCALE_STAGES = 3, SCALE_KB = 4;        // scales are staged for four blocks at a time
-constexpr int MAX_ACCS = 4;
-constexpr int PARTIAL_BYTES = SINGLE_CAP * BM * 4;
-constexpr uint64_t kDrainLimitNs = 100000000ull;
+constexpr int ACCS = 4, TMEM_COLS = ACCS * CAP;
+constexpr int PARTIAL_BYTES = CAP * BM * 4;
 
 struct __align__(1024) Smem {
     uint8_t ring[RING_BYTES];
     uint8_t stg[2][STG_BYTES];           // one per group of epilogue warps
-    float scale[SCALE_STAGES][SCALE_KB][PAIR_CAP];
+    float scale[SCALE_STAGES][SCALE_KB][CAP];
     float w_scale[SCALE_STAGES][SCALE_KB];
     uint64_t full[MAX_STAGES];
     uint64_t empty[MAX_STAGES];
-    uint64_t acc_full[MAX_ACCS];
-    uint64_t acc_empty[MAX_ACCS];
+    uint64_t acc_full[ACCS];
+    uint64_t acc_empty[ACCS];
     uint64_t scale_full[SCALE_STAGES];
     uint64_t scale_empty[SCALE_STAGES];
     uint64_t drain;
@@ -85,10 +81,10 @@ struct F8Params {
     const float *a_scales;   // [rows, KB]
     const float *w_scales;   // [E, NB, KB] or [E, KB, NB]
     int E, rows, N, K;
-    int w_tiles;             // weight tiles of 128 * CG columns
+    int w_tiles;             // weight tiles of 128 columns
     int tok_cap;             // rows per unit at most
     int row_block;           // row units per block
-    int slot_bytes;          // ring slot: W_BYTES + this CTA's rows of a full unit
+    int slot_bytes;          // ring slot: W_BYTES + the rows of a full unit
     int stages;
     int split;               // SPLIT: CTAs that share a unit's k
     int out_bf16;            // 16-bit outputs: BF16 or F16
@@ -99,44 +95,10 @@ struct F8Params {
     uint64_t wait_ns;
 };
 
-// Four maps of the rows, for boxes of 128, 64, 32 and 16 of them.
+// Three maps of the rows, for boxes of 64, 32 and 16 of them.
 struct RowMaps {
-    CUtensorMap m[4];
+    CUtensorMap m[3];
 };
-
-// D (+)= A B^T of one K = 32 step of e4m3 operands.
-template <int CG>
-__device__ __forceinline__ void umma_f8_on(uint32_t on, uint32_t d, uint64_t adesc, uint64_t bdesc,
-                                           uint32_t idesc, uint32_t accumulate)
-{
-    if constexpr (CG == 2)
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %0, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-            "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%1], %2, %3, %4, p;\n\t}" ::"r"(on),
-            "r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-            : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 q, %0, 0;\n\tsetp.ne.b32 p, %5, 0;\n\t"
-            "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%1], %2, %3, %4, p;\n\t}" ::"r"(on),
-            "r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-            : "memory");
-}
-
-// Arrives on a barrier of the pair's other CTA. The default scope: what the barrier
-// orders is tensor memory, by the tcgen05 fences on both sides, and a release at
-// cluster scope, a full memory barrier, cost a microsecond per block.
-__device__ __forceinline__ void arrive_remote(uint32_t cluster_addr)
-{
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-
-// Instruction descriptor, kind::f8f6f4: FP32 accumulator, A and B e4m3 (0), A
-// MN-major where a_mn, N >> 3 at bit 17, M >> 4 at bit 24.
-__host__ __device__ constexpr uint32_t idesc_e4m3(int M, int N, bool a_mn)
-{
-    return (1u << 4) | ((a_mn ? 1u : 0u) << 15) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
-}
 
 // sum += v * s of two FP32 values in one register pair.
 __device__ __forceinline__ void fma2(uint64_t &sum, uint32_t v0, uint32_t v1, uint64_t s)
@@ -180,28 +142,7 @@ __device__ __forceinline__ void store_blocks_transposed(uint32_t saddr, uint32_t
                  : "memory");
 }
 
-// 4 bytes of global memory into shared memory, asynchronously.
-__device__ __forceinline__ void copy4_async(float *dst, const float *src)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-
-// This thread's copies so far arrive on the barrier when they have landed.
-__device__ __forceinline__ void copies_arrive(uint64_t *bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
-}
-
-// warp_wait on two barriers whose phases may well be complete: both are asked at once.
-__device__ __forceinline__ bool warp_wait_both(uint64_t *a, uint32_t pa, uint64_t *b, uint32_t pb,
-                                               volatile int *abort_flag, unsigned *status, uint64_t limit_ns)
-{
-    const bool ok_a = mbar_try_wait(a, pa), ok_b = mbar_try_wait(b, pb);
-    if (__all_sync(0xffffffffu, ok_a && ok_b)) return true;
-    return warp_wait<1>(a, pa, abort_flag, status, limit_ns) && warp_wait<1>(b, pb, abort_flag, status, limit_ns);
-}
-
-template <int CG, bool KN, bool OUT_F32, bool SPLIT>
+template <bool KN, bool OUT_F32, bool SPLIT>
 __global__ void __launch_bounds__(THREADS, 1)
 grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ RowMaps map_a,
                   const F8Params p)
@@ -209,12 +150,7 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     extern __shared__ uint8_t smem_raw[];
     Smem &S = *reinterpret_cast<Smem *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const int rank = CG == 2 ? (int)cluster_ctarank() : 0;
-    const bool leader = rank == 0;
-    static_assert(!SPLIT || CG == 1, "a split unit runs on single CTAs");
-    constexpr int CAP = CG == 2 ? PAIR_CAP : SINGLE_CAP;
-    constexpr int ACCS = CG == 2 ? 2 : 4, TMEM_COLS = ACCS * CAP;
-    const int ways = SPLIT ? p.split : CG;           // CTAs per unit
+    const int ways = SPLIT ? p.split : 1;            // CTAs per unit
     const int unit0 = (int)blockIdx.x / ways, unit_step = (int)gridDim.x / ways;
     // this CTA's blocks of k
     const int all_kb = (p.K + BK - 1) / BK, slice = SPLIT ? (int)cluster_ctarank() : 0;
@@ -223,54 +159,47 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) { mbar_init(&S.full[s], 1); mbar_init(&S.empty[s], 1); }
-        for (int a = 0; a < ACCS; ++a) { mbar_init(&S.acc_full[a], 1); mbar_init(&S.acc_empty[a], EPI_WARPS * CG); }
+        for (int a = 0; a < ACCS; ++a) { mbar_init(&S.acc_full[a], 1); mbar_init(&S.acc_empty[a], EPI_WARPS); }
         for (int s = 0; s < SCALE_STAGES; ++s) { mbar_init(&S.scale_full[s], 32); mbar_init(&S.scale_empty[s], EPI_WARPS); }
         mbar_init(&S.drain, 1);
         S.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        tmem_alloc<CG>(&S.tmem_base, TMEM_COLS);
-        tmem_relinquish<CG>();
+        tmem_alloc<1>(&S.tmem_base, TMEM_COLS);
+        tmem_relinquish<1>();
     }
     pdl_wait();
     pdl_launch_dependents();
     load_segments<THREADS>(S.seg, S.warp_sum, p.offsets, p.E, p.rows, p.status,
                            [&](int cnt) { return (cnt + p.tok_cap - 1) / p.tok_cap * p.w_tiles; });
     tc_fence_before();
-    // a pair also makes each CTA's barrier initialisation visible to the
-    // other before any copy or arrival targets it
-    if constexpr (CG == 2) cluster_sync();
-    else __syncthreads();
+    __syncthreads();
     tc_fence_after();
 
     const uint32_t tmem_base = S.tmem_base;
     const int total = S.seg.unit[p.E];
     volatile int *abort_flag = &S.abort;
-    UnitWalk<CG, F8Params> walk(S.seg, p, rank);
+    UnitWalk<1, F8Params> walk(S.seg, p, 0);
 
-    // 384 threads start with 168 registers each: 128 * (88 + 2 * 208) is the same
     if (warp < 4) {
-        if constexpr (CG == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
         if (warp == 0) {
             // ------------------------------------------- TMA producer: weights
-            const uint32_t on = elect_lane(), arm = leader ? on : 0u;
+            const uint32_t on = elect_lane();
             const uint32_t ring = smem_u32(S.ring);
             int stage = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int unit = unit0; unit < total && ok; unit += unit_step) {
                 const Unit u = walk.at(unit);
-                // both CTAs' copies of weights and rows complete on the leader's
-                // barrier, which expects them all
-                const uint32_t bytes = CG * (W_BYTES + u.mma_n / CG * BK);
+                const uint32_t bytes = W_BYTES + u.mma_n * BK;
                 for (int kb = kb_begin; kb < kb_end; ++kb) {
                     ok = warp_wait<1>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns);
                     if (!ok) break;
-                    const uint32_t here = smem_u32(&S.full[stage]), bar = CG == 2 ? mapa_shared(here, 0) : here;
-                    expect_tx_on(arm, &S.full[stage], bytes);
-                    if constexpr (KN) load_3d_on<CG>(on, ring + stage * p.slot_bytes, &map_w, bar, u.w0, kb * BK, u.e);
-                    else load_3d_on<CG>(on, ring + stage * p.slot_bytes, &map_w, bar, kb * BK, u.w0, u.e);
+                    const uint32_t bar = smem_u32(&S.full[stage]);
+                    expect_tx_on(on, &S.full[stage], bytes);
+                    if constexpr (KN) load_3d_on<1>(on, ring + stage * p.slot_bytes, &map_w, bar, u.w0, kb * BK, u.e);
+                    else load_3d_on<1>(on, ring + stage * p.slot_bytes, &map_w, bar, kb * BK, u.w0, u.e);
                     if (++stage == p.stages) { stage = 0; phase ^= 1u; }
                 }
             }
@@ -283,27 +212,24 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             bool ok = true;
             for (int unit = unit0; unit < total && ok; unit += unit_step) {
                 const Unit u = walk.at(unit);
-                const int mine = u.mma_n / CG;               // rows this CTA loads
-                const int row0 = u.row0 + rank * mine;
+                const int mine = u.mma_n;
                 for (int kb = kb_begin; kb < kb_end; ++kb) {
                     ok = warp_wait<1>(&S.empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns);
                     if (!ok) break;
-                    const uint32_t sa = ring + stage * p.slot_bytes + W_BYTES, here = smem_u32(&S.full[stage]);
-                    const uint32_t bar = CG == 2 ? mapa_shared(here, 0) : here;
+                    const uint32_t sa = ring + stage * p.slot_bytes + W_BYTES, bar = smem_u32(&S.full[stage]);
                     auto load = [&](int box, int at) {
-                        load_2d_on<CG>(on, sa + at * BK, &map_a.m[box], bar, kb * BK, row0 + at);
+                        load_2d_on<1>(on, sa + at * BK, &map_a.m[box], bar, kb * BK, u.row0 + at);
                     };
                     int at = 0;
-                    for (; mine - at >= 128; at += 128) load(0, at);
-                    if (mine & 64) { load(1, at); at += 64; }
-                    if (mine & 32) { load(2, at); at += 32; }
-                    if (mine & 16) load(3, at);
+                    if (mine & 64) { load(0, at); at += 64; }
+                    if (mine & 32) { load(1, at); at += 32; }
+                    if (mine & 16) load(2, at);
                     if (++stage == p.stages) { stage = 0; phase ^= 1u; }
                 }
             }
-        } else if (warp == 1 && leader) {
+        } else if (warp == 1) {
             // ------------------------------------------------------ MMA issuer
-            constexpr uint32_t idesc0 = idesc_e4m3(BM * CG, 0, KN);
+            constexpr uint32_t idesc0 = idesc_e4m3(BM, 0, KN, false);
             const uint32_t on = elect_lane();
             const uint32_t ring = smem_u32(S.ring);
             int stage = 0, acc = 0;
@@ -321,10 +247,10 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                     const uint32_t w = ring + stage * p.slot_bytes, a = w + W_BYTES;
 #pragma unroll
                     for (int k = 0; k < BK / UK; ++k)
-                        umma_f8_on<CG>(on, d, KN ? sdesc_mn_sw128(w + k * UK * 128, W_BYTES) : sdesc_k_sw128(w + k * UK),
+                        umma_f8_on<1>(on, d, KN ? sdesc_mn_sw128(w + k * UK * 128, W_BYTES) : sdesc_k_sw128(w + k * UK),
                                        sdesc_k_sw128(a + k * UK), idesc, k ? 1u : 0u);
-                    commit_on<CG>(on, &S.empty[stage]);
-                    commit_on<CG>(on, &S.acc_full[acc]);
+                    commit_on<1>(on, &S.empty[stage]);
+                    commit_on<1>(on, &S.acc_full[acc]);
                     if (++stage == p.stages) { stage = 0; phase ^= 1u; }
                     if (++acc == ACCS) { acc = 0; acc_phase ^= 1u; }
                 }
@@ -332,7 +258,7 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             // every MMA issued must finish before TMEM is released, also where
             // another role has given up
             if (on) {
-                umma_commit<CG>(&S.drain);
+                umma_commit<1>(&S.drain);
                 mbar_wait(&S.drain, 0, nullptr, p.status, kDrainLimitNs);
             }
             __syncwarp();
@@ -366,81 +292,57 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         }
     } else {
         // ------------------------------------------------------ epilogue
-        if constexpr (CG == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int q = warp & 3;                          // TMEM lane quadrant of this warp
         const int group = warp >= 8 ? 1 : 0;
         const int tid = threadIdx.x - (group ? 256 : 128);    // 0..127 in the group
-        constexpr int CHUNKS = CAP / 64;                 // of 32 columns, per group
         int acc = 0, stage = 0;
         uint32_t acc_phase = 0, phase = 0;
         const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16) + group * 32;
         for (int unit = unit0; unit < total; unit += unit_step) {
             const Unit u = walk.at(unit);
-            // this group's columns: 32 from each 64 (2 j + group) on. Of a chunk a thread
-            // has lanes lane / 4 + 8 m (m = 2 h + e) and columns 8 i + 2 (lane % 4) and the
-            // next: sums[j][h][2 i + e], a pair each
-            uint64_t sums[CHUNKS][2][8];
+            // this group's columns: 32 of the accumulator's 64. A thread has lanes
+            // lane / 4 + 8 m (m = 2 h + e) and columns 8 i + 2 (lane % 4) and the next:
+            // sums[h][2 i + e], a pair each
+            uint64_t sums[2][8];
 #pragma unroll
-            for (int j = 0; j < CHUNKS; ++j)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) sums[j][i / 8][i % 8] = 0;
-            // NJ of the chunks hold rows: no branch between a chunk's loads and the
-            // additions of the one before
-            auto add_blocks = [&](auto nj) {
-                constexpr int NJ = decltype(nj)::value;
-                for (int kb = kb_begin; kb < kb_end; ++kb) {
-                    const int k = (kb - kb_begin) % SCALE_KB;
-                    bool ok = warp_wait<1>(&S.acc_full[acc], acc_phase, abort_flag, p.status, p.wait_ns);
-                    if (k == 0) ok = ok && warp_wait<1>(&S.scale_full[stage], phase, abort_flag, p.status, p.wait_ns);
-                    if (!ok) return false;
-                    tc_fence_after();
+            for (int i = 0; i < 16; ++i) sums[i / 8][i % 8] = 0;
+            bool ok = true;
+            for (int kb = kb_begin; kb < kb_end; ++kb) {
+                const int k = (kb - kb_begin) % SCALE_KB;
+                ok = warp_wait<1>(&S.acc_full[acc], acc_phase, abort_flag, p.status, p.wait_ns);
+                if (k == 0) ok = ok && warp_wait<1>(&S.scale_full[stage], phase, abort_flag, p.status, p.wait_ns);
+                if (!ok) break;
+                tc_fence_after();
+                if (u.rows > group * 32) {
                     const uint32_t tbase = tlane + (uint32_t)(acc * CAP);
                     const float *sc = S.scale[stage][k] + group * 32 + 2 * (lane & 3);
                     const float w = S.w_scale[stage][k];
                     const uint64_t w2 = (uint64_t)__float_as_uint(w) << 32 | __float_as_uint(w);
                     uint32_t v[2][16];
-                    if constexpr (NJ > 0) tmem_ld_blocks32(tbase, v[0]);
+                    tmem_ld_blocks32(tbase, v[0]);
+                    tmem_ld_blocks32(tbase + (16u << 16), v[1]);
+                    uint64_t s2[4];
 #pragma unroll
-                    for (int j = 0; j < NJ; ++j) {
-                        uint64_t s2[4];
+                    for (int i = 0; i < 4; ++i) s2[i] = mul2(*reinterpret_cast<const uint64_t *>(sc + i * 8), w2);
+                    tmem_ld_wait16(v[0]);
+                    tmem_ld_wait16(v[1]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            s2[i] = mul2(*reinterpret_cast<const uint64_t *>(sc + j * 64 + i * 8), w2);
+                    for (int h = 0; h < 2; ++h)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            tmem_ld_wait16(v[h]);
-                            if (h == 0) tmem_ld_blocks32(tbase + j * 64 + (16u << 16), v[1]);
-                            else if (j + 1 < NJ) tmem_ld_blocks32(tbase + (j + 1) * 64, v[0]);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                fma2(sums[j][h][2 * i], v[h][4 * i], v[h][4 * i + 1], s2[i]);
-                                fma2(sums[j][h][2 * i + 1], v[h][4 * i + 2], v[h][4 * i + 3], s2[i]);
-                            }
+                        for (int i = 0; i < 4; ++i) {
+                            fma2(sums[h][2 * i], v[h][4 * i], v[h][4 * i + 1], s2[i]);
+                            fma2(sums[h][2 * i + 1], v[h][4 * i + 2], v[h][4 * i + 3], s2[i]);
                         }
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    const bool last = k == SCALE_KB - 1 || kb + 1 == kb_end;
-                    if (lane == 0) {
-                        if (CG == 2 && !leader) arrive_remote(mapa_shared(smem_u32(&S.acc_empty[acc]), 0));
-                        else mbar_arrive(&S.acc_empty[acc]);
-                        if (last) mbar_arrive(&S.scale_empty[stage]);
-                    }
-                    if (last && ++stage == SCALE_STAGES) { stage = 0; phase ^= 1u; }
-                    if (++acc == ACCS) { acc = 0; acc_phase ^= 1u; }
                 }
-                return true;
-            };
-            bool ok;
-            const int nj = u.rows > group * 32 ? (u.rows - group * 32 + 63) / 64 : 0;
-            if constexpr (CHUNKS == 1) {
-                ok = nj == 0 ? add_blocks(std::integral_constant<int, 0>()) : add_blocks(std::integral_constant<int, 1>());
-            } else {
-                ok = nj == 4   ? add_blocks(std::integral_constant<int, 4>())
-                     : nj == 3 ? add_blocks(std::integral_constant<int, 3>())
-                     : nj == 2 ? add_blocks(std::integral_constant<int, 2>())
-                     : nj == 1 ? add_blocks(std::integral_constant<int, 1>())
-                               : add_blocks(std::integral_constant<int, 0>());
+                tc_fence_before();
+                __syncwarp();
+                const bool last = k == SCALE_KB - 1 || kb + 1 == kb_end;
+                if (lane == 0) {
+                    mbar_arrive(&S.acc_empty[acc]);
+                    if (last) mbar_arrive(&S.scale_empty[stage]);
+                }
+                if (last && ++stage == SCALE_STAGES) { stage = 0; phase ^= 1u; }
+                if (++acc == ACCS) { acc = 0; acc_phase ^= 1u; }
             }
             if constexpr (SPLIT) {
                 // the partial sums stay here, [row][n] in FP32
@@ -450,8 +352,8 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int t = group * 32 + i / 2 * 8 + 2 * (lane & 3), n = h * 16 + (i & 1) * 8;
-                        mine[t * BM + n] = low(sums[0][h][i]);
-                        mine[(t + 1) * BM + n] = high(sums[0][h][i]);
+                        mine[t * BM + n] = low(sums[h][i]);
+                        mine[(t + 1) * BM + n] = high(sums[h][i]);
                     }
                 continue;
             }
@@ -463,52 +365,49 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             uint8_t *out0 = p.out + (int64_t)u.row0 * p.out_row_bytes + (int64_t)col * ESZ;
             const bool whole = p.vec && col + 16 / ESZ <= p.N;
 #pragma unroll
-            for (int j = 0; j < CHUNKS; ++j) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int t0 = j * 64 + group * 32 + i * 8;
-                    if (t0 >= u.rows) continue;
-                    // eight rows through shared memory. 16 bits: the halves of the buffer
-                    // take turns, and who passes the barrier has read the other one; the
-                    // 16-byte pieces of row t are permuted by t, so that a block's eight
-                    // rows meet no bank twice
-                    uint8_t *stg = S.stg[group] + (OUT_F32 ? 0 : (i & 1) * (STG_ROWS * BM * 2));
-                    if constexpr (OUT_F32) {
-                        epi_sync(1 + group);
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            const uint64_t two = sums[j][m / 2][2 * i + (m & 1)];
-                            uint8_t *to = stg + 2 * (lane & 3) * STG_F32_ROW + (q * 32 + m * 8 + lane / 4) * 4;
-                            *reinterpret_cast<float *>(to) = low(two);
-                            *reinterpret_cast<float *>(to + STG_F32_ROW) = high(two);
-                        }
-                    } else {
-                        auto block = [&](int m) {
-                            const uint64_t two = sums[j][m / 2][2 * i + (m & 1)];
-                            return p.out_bf16 ? float2_to_bf16x2(low(two), high(two)) : float2_to_f16x2(low(two), high(two));
-                        };
-                        const int t = lane & 7, at = q * 4 + (lane >> 3);
-                        store_blocks_transposed(smem_u32(stg + t * (BM * 2) + ((at ^ t) << 4)), block(0), block(1),
-                                                block(2), block(3));
-                    }
+            for (int i = 0; i < 4; ++i) {
+                const int t0 = group * 32 + i * 8;
+                if (t0 >= u.rows) continue;
+                // eight rows through shared memory. 16 bits: the halves of the buffer
+                // take turns, and who passes the barrier has read the other one; the
+                // 16-byte pieces of row t are permuted by t, so that a block's eight
+                // rows meet no bank twice
+                uint8_t *stg = S.stg[group] + (OUT_F32 ? 0 : (i & 1) * (STG_ROWS * BM * 2));
+                if constexpr (OUT_F32) {
                     epi_sync(1 + group);
 #pragma unroll
-                    for (int r = 0; r < STG_ROWS / PER_IT; ++r) {
-                        const int t = r * PER_IT + tid / PIECES;
-                        const uint4 v = *reinterpret_cast<const uint4 *>(
-                            stg + (OUT_F32 ? t * STG_F32_ROW + piece * 16 : t * (BM * 2) + ((piece ^ (t & 7)) << 4)));
-                        if (t0 + t >= u.rows) continue;
-                        uint8_t *dst = out0 + (int64_t)(t0 + t) * p.out_row_bytes;
-                        if (whole) {
-                            *reinterpret_cast<uint4 *>(dst) = v;
-                        } else {
-                            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+                    for (int m = 0; m < 4; ++m) {
+                        const uint64_t two = sums[m / 2][2 * i + (m & 1)];
+                        uint8_t *to = stg + 2 * (lane & 3) * STG_F32_ROW + (q * 32 + m * 8 + lane / 4) * 4;
+                        *reinterpret_cast<float *>(to) = low(two);
+                        *reinterpret_cast<float *>(to + STG_F32_ROW) = high(two);
+                    }
+                } else {
+                    auto block = [&](int m) {
+                        const uint64_t two = sums[m / 2][2 * i + (m & 1)];
+                        return p.out_bf16 ? float2_to_bf16x2(low(two), high(two)) : float2_to_f16x2(low(two), high(two));
+                    };
+                    const int t = lane & 7, at = q * 4 + (lane >> 3);
+                    store_blocks_transposed(smem_u32(stg + t * (BM * 2) + ((at ^ t) << 4)), block(0), block(1),
+                                            block(2), block(3));
+                }
+                epi_sync(1 + group);
 #pragma unroll
-                            for (int c = 0; c < 16 / ESZ; ++c) {
-                                if (col + c >= p.N) continue;
-                                if constexpr (OUT_F32) reinterpret_cast<uint32_t *>(dst)[c] = w[c];
-                                else reinterpret_cast<uint16_t *>(dst)[c] = (uint16_t)(w[c / 2] >> (c & 1) * 16);
-                            }
+                for (int r = 0; r < STG_ROWS / PER_IT; ++r) {
+                    const int t = r * PER_IT + tid / PIECES;
+                    const uint4 v = *reinterpret_cast<const uint4 *>(
+                        stg + (OUT_F32 ? t * STG_F32_ROW + piece * 16 : t * (BM * 2) + ((piece ^ (t & 7)) << 4)));
+                    if (t0 + t >= u.rows) continue;
+                    uint8_t *dst = out0 + (int64_t)(t0 + t) * p.out_row_bytes;
+                    if (whole) {
+                        *reinterpret_cast<uint4 *>(dst) = v;
+                    } else {
+                        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int c = 0; c < 16 / ESZ; ++c) {
+                            if (col + c >= p.N) continue;
+                            if constexpr (OUT_F32) reinterpret_cast<uint32_t *>(dst)[c] = w[c];
+                            else reinterpret_cast<uint16_t *>(dst)[c] = (uint16_t)(w[c / 2] >> (c & 1) * 16);
                         }
                     }
                 }
@@ -521,7 +420,7 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
         __syncwarp();
         cluster_sync();
         if (unit0 < total) {
-            const Unit u = UnitWalk<CG, F8Params>(S.seg, p, rank).at(unit0);
+            const Unit u = UnitWalk<1, F8Params>(S.seg, p, 0).at(unit0);
             const uint32_t partial = smem_u32(S.ring + RING_BYTES - PARTIAL_BYTES);
             for (int i = threadIdx.x; ; i += THREADS) {
                 const int t = i / BM * ways + slice, n = i % BM;
@@ -545,43 +444,27 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     // ------------------------------------------------------------ teardown
     __syncthreads();
     if (*abort_flag) let_copies_land();
-    // a pair keeps both CTAs (their shared memory is read by the leader's
-    // MMAs and signalled by its commits) until both are done
-    if constexpr (CG == 2) cluster_sync();
-    else __syncthreads();
+    __syncthreads();
     if (warp == 1) {
         __syncwarp();
         tc_fence_after();
-        tmem_dealloc<CG>(tmem_base, TMEM_COLS);
+        tmem_dealloc<1>(tmem_base, TMEM_COLS);
     }
 }
 
 // ---- host side ---------------------------------------------------------------
 
-// Bytes, row-major, of two or three dimensions, in boxes of 128 bytes by box_rows.
-bool encode_bytes(CUtensorMap *m, const void *base, int rank, const uint64_t (&dims)[3],
-                  const uint64_t (&strides)[2], uint32_t box_rows)
-{
-    EncodeTiledFn fn = encode_fn();
-    if (fn == nullptr) return false;
-    cuuint64_t d[3] = {dims[0], dims[1], dims[2]}, st[2] = {strides[0], strides[1]};
-    cuuint32_t box[3] = {128, box_rows, 1}, es[3] = {1, 1, 1};
-    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, (cuuint32_t)rank, const_cast<void *>(base), d, st, box, es,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-template <int CG, bool KN, bool OUT_F32, bool SPLIT>
+template <bool KN, bool OUT_F32, bool SPLIT>
 cudaError_t launch_kernel(int64_t units, const CUtensorMap &mw, const RowMaps &ma, const F8Params &p,
                           cudaStream_t s)
 {
     static std::atomic<int> cache[kCachedDevices];
-    auto kernel = grouped_f8_kernel<CG, KN, OUT_F32, SPLIT>;
+    auto kernel = grouped_f8_kernel<KN, OUT_F32, SPLIT>;
     int ctas = 0;
-    cudaError_t err = prepare_kernel(kernel, CG, THREADS, kSmemBytes, cache, &ctas);
+    cudaError_t err = prepare_kernel(kernel, 1, THREADS, kSmemBytes, cache, &ctas);
     if (err != cudaSuccess) return err;
     cudaLaunchConfig_t cfg = {};
-    const int ways = SPLIT ? p.split : CG;
+    const int ways = SPLIT ? p.split : 1;
     cfg.gridDim = dim3((unsigned)(SPLIT || ways * units < ctas ? ways * units : ctas));
     cfg.blockDim = dim3(THREADS);
     cfg.dynamicSmemBytes = kSmemBytes;
@@ -598,17 +481,16 @@ cudaError_t launch_kernel(int64_t units, const CUtensorMap &mw, const RowMaps &m
     return cudaLaunchKernelEx(&cfg, kernel, mw, ma, p);
 }
 
-template <int CG, bool SPLIT>
+template <bool SPLIT>
 cudaError_t launch_form(const GroupedF8 &g, int split, unsigned *status, cudaStream_t s)
 {
-    constexpr int CAP = CG == 2 ? PAIR_CAP : SINGLE_CAP;
     const uint64_t N = (uint64_t)g.N, K = (uint64_t)g.K, E = (uint64_t)g.E;
     CUtensorMap mw;
     RowMaps ma;
     bool ok = g.transposed ? encode_bytes(&mw, g.w, 3, {N, K, E}, {N, N * K}, BK)
                            : encode_bytes(&mw, g.w, 3, {K, N, E}, {K, N * K}, BM);
-    for (int i = 0; i < 4; ++i)
-        ok = ok && encode_bytes(&ma.m[i], g.a, 2, {K, (uint64_t)g.rows, 1}, {(uint64_t)g.lda, 0}, 128u >> i);
+    for (int i = 0; i < 3; ++i)
+        ok = ok && encode_bytes(&ma.m[i], g.a, 2, {K, (uint64_t)g.rows, 1}, {(uint64_t)g.lda, 0}, 64u >> i);
     if (!ok) return cudaErrorInvalidValue;
     F8Params p{};
     p.offsets = g.offsets;
@@ -618,11 +500,11 @@ cudaError_t launch_form(const GroupedF8 &g, int split, unsigned *status, cudaStr
     p.rows = (int)g.rows;
     p.N = (int)g.N;
     p.K = (int)g.K;
-    p.w_tiles = (int)((g.N + BM * CG - 1) / (BM * CG));
+    p.w_tiles = (int)((g.N + BM - 1) / BM);
     p.tok_cap = CAP;
     const int64_t block = kRowBlockBytes / (CAP * g.K), most = (g.rows + CAP - 1) / CAP;
     p.row_block = (int)(block < 1 ? 1 : block > most ? most : block);
-    p.slot_bytes = W_BYTES + CAP / CG * BK;
+    p.slot_bytes = W_BYTES + CAP * BK;
     const int slots = (RING_BYTES - (SPLIT ? PARTIAL_BYTES : 0)) / p.slot_bytes;
     p.stages = slots < MAX_STAGES ? slots : MAX_STAGES;
     p.split = split;
@@ -637,10 +519,10 @@ cudaError_t launch_form(const GroupedF8 &g, int split, unsigned *status, cudaStr
     // an upper bound: every expert adds at most one unit that is not full
     const int64_t units = (g.rows / CAP + (g.rows < g.E ? g.rows : g.E)) * p.w_tiles;
     if (g.out_dt == DT_F32)
-        return g.transposed ? launch_kernel<CG, true, true, SPLIT>(units, mw, ma, p, s)
-                            : launch_kernel<CG, false, true, SPLIT>(units, mw, ma, p, s);
-    return g.transposed ? launch_kernel<CG, true, false, SPLIT>(units, mw, ma, p, s)
-                        : launch_kernel<CG, false, false, SPLIT>(units, mw, ma, p, s);
+        return g.transposed ? launch_kernel<true, true, SPLIT>(units, mw, ma, p, s)
+                            : launch_kernel<false, true, SPLIT>(units, mw, ma, p, s);
+    return g.transposed ? launch_kernel<true, false, SPLIT>(units, mw, ma, p, s)
+                        : launch_kernel<false, false, SPLIT>(units, mw, ma, p, s);
 }
 
 }  // namespace
@@ -649,13 +531,16 @@ cudaError_t launch_grouped_gemm_f8(const GroupedF8 &g, unsigned *status, cudaStr
 {
     // Few units (of the single form's 64 rows by 128 columns): split k over as
     // many CTAs, 2 to 8, as the GPU has room for and as leave each two blocks.
-    const int64_t units = (g.rows / SINGLE_CAP + (g.rows < g.E ? g.rows : g.E)) * ((g.N + BM - 1) / BM);
+    const int64_t units = (g.rows / CAP + (g.rows < g.E ? g.rows : g.E)) * ((g.N + BM - 1) / BM);
     const int64_t num_kb = (g.K + BK - 1) / BK, sms = device_sm_count();
     int split = 1;
     while (split < 8 && units * split * 2 <= sms && num_kb >= split * 2 * 2) split *= 2;
-    if (split > 1) return launch_form<1, true>(g, split, status, s);
-    if (g.rows >= 64 * (int64_t)g.E) return launch_form<2, false>(g, 1, status, s);
-    return launch_form<1, false>(g, 1, status, s);
+    if (split > 1) return launch_form<true>(g, split, status, s);
+    // The two forms, by the average rows of an expert: us at 4, 32, 48, 64, 96, 192
+    // rows, on 64 experts of N = K = 2048 (16 of N = K = 4096): this one 64 65 66 79
+    // 105 177 (68 70 70 74 97 160), the wide one 76 79 79 79 83 85 (81 81 81 81 83 85).
+    if (g.rows >= 64 * (int64_t)g.E) return launch_grouped_gemm_f8_wide(g, status, s);
+    return launch_form<false>(g, 1, status, s);
 }
 
 }  // namespace moe

@@ -269,6 +269,8 @@ struct GroupedF8 {
     int out_dt;
 };
 cudaError_t launch_grouped_gemm_f8(const GroupedF8 &g, unsigned *status, cudaStream_t s);
+// The form for experts of many rows.
+cudaError_t launch_grouped_gemm_f8_wide(const GroupedF8 &g, unsigned *status, cudaStream_t s);
 
 // The whole layer for a few tokens in two kernels. Routing from logits, or (logits
 // NULL) from indices and weights. gate_scales, up_scales, down_scales: NULL, or the
