@@ -27,12 +27,25 @@
 //
 // A CTA's tiles x k-steps form one sequence, cut into 16 equal contiguous pieces, one
 // per warp, so that all warps stream for the whole time; a warp keeps kDepth steps of
-// 2 x 128 bytes per row in flight in registers, across tile borders. Tiles cut by a
+// 16 rows x 128 bytes in flight in registers, across tile borders. Tiles cut by a
 // border leave partial sums in shared memory, which the warp that has the tile's
 // beginning adds up in order: results do not depend on timing.
+//
+// What the rest costs is latency: x is loaded for a whole group of steps before its
+// products (one wait instead of one per product: 973 -> 754 us for 8 tokens on 256
+// experts of 7168 x 2048), and the code that finishes a tile is there once, since
+// weights that pass through L2 evict the kernel and each launch fetches its code from
+// memory anew; for the same reason weights are read evict-first. Deeper groups (4
+// steps) cost 8-bit weights their registers (528 us against 409), and a ring of
+// asynchronous copies in shared memory an issue slot per 16 bytes (1106 us).
+// 8 tokens, 256 experts, BF16: 0.74 ms, the touched weights at the copy bandwidth;
+// e4m3: 0.41 ms (91 %). One token, 64 experts of 2048 x 1408: 26 us, of which 15
+// stream; the routing in each kernel takes 2, the first loads after it 2.
 #pragma once
 
 #include <cuda_fp8.h>
+
+#include <atomic>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -40,27 +53,41 @@
 namespace moe {
 namespace {
 
-constexpr int kFewThreads = 512;
-constexpr int kFewWarps = kFewThreads / 32;
-constexpr int kFewPairs = kFewMaxTokens * kFewMaxTopK;
-constexpr int kDepth = 4;                 // steps in flight per warp
+constexpr int kFewWarps = 16;
+constexpr int kFewThreads = kFewWarps * 32;
+constexpr int kDepth = 2;                 // steps of a warp in flight
 constexpr int kStepBytes = 128;           // of each row per step
 constexpr uint16_t kNoExpert = 0xffff;
 constexpr unsigned kFull = 0xffffffffu;
 
-// What a CTA knows of the routing.
-struct alignas(16) FewPlan {
-    uint16_t ids[kFewPairs];              // expert of pair t * top_k + j
-    float w[kFewPairs];                   // its weight
-    uint16_t order[kFewPairs];            // pairs by expert
-    struct { uint16_t e, first, count, pad; } chunk[kFewPairs];
-    uint32_t starts[kFewPairs / 32];      // bit i: order[i] starts a chunk
-    int chunks;
+// What a CTA knows of the routing, in shared memory: `n` pairs.
+struct FewPlan {
+    float *w;                             // weight of pair t * top_k + j
+    uint16_t *ids;                        // its expert
+    uint16_t *order;                      // pairs by expert
+    uint16_t *len;                        // of the chunk that starts at order[i], or 0
+    uint16_t *chunk_e, *chunk_first, *chunk_len;
+    int *chunks;
+
+    __host__ __device__ static constexpr size_t bytes(int n) { return 16 + (size_t)((n + 7) & ~7) * 16; }
+
+    __device__ __forceinline__ FewPlan(uint8_t *at, int n)
+    {
+        n = (n + 7) & ~7;
+        chunks = reinterpret_cast<int *>(at);
+        w = reinterpret_cast<float *>(at + 16);
+        ids = reinterpret_cast<uint16_t *>(w + n);
+        order = ids + n;
+        len = order + n;
+        chunk_e = len + n;
+        chunk_first = chunk_e + n;
+        chunk_len = chunk_first + n;
+    }
 };
 
 // Routes one token with a warp; lane i holds logits i, i + 32, ...
 template <int EPL>
-__device__ __forceinline__ void few_route_token(const FewArgs &a, int t, FewPlan &S)
+__device__ __forceinline__ void few_route_token(const FewArgs &a, int t, const FewPlan &S)
 {
     const int lane = threadIdx.x & 31;
     uint32_t key[EPL];                    // larger key, larger logit; 0: none or taken
@@ -119,7 +146,7 @@ __device__ __forceinline__ void few_route_token(const FewArgs &a, int t, FewPlan
 }
 
 // Fills the plan; all threads call.
-__device__ __forceinline__ void few_plan(const FewArgs &a, int chunk_max, FewPlan &S)
+__device__ __forceinline__ void few_plan(const FewArgs &a, int chunk_max, const FewPlan &S)
 {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, pairs = a.T * a.top_k;
     if (a.logits != nullptr) {
@@ -141,65 +168,62 @@ __device__ __forceinline__ void few_plan(const FewArgs &a, int chunk_max, FewPla
     __syncthreads();
     // position of each pair in the order by (expert, pair); pairs without an
     // expert come last and start no chunk
-    bool start[kFewPairs / kFewThreads];
-    int at[kFewPairs / kFewThreads], before[kFewPairs / kFewThreads], same[kFewPairs / kFewThreads];
-#pragma unroll
-    for (int r = 0; r < kFewPairs / kFewThreads; ++r) {
-        const int i = threadIdx.x + r * kFewThreads;
-        start[r] = false;
-        at[r] = i;
-        if (i >= pairs) continue;
+    for (int i = threadIdx.x; i < pairs; i += kFewThreads) {
         const int e = S.ids[i];
-        int less = 0;
-        before[r] = same[r] = 0;
+        int less = 0, before = 0, same = 0;
         for (int k = 0; k < pairs; ++k) {
             const int f = S.ids[k];
             less += f < e;
-            same[r] += f == e;
-            before[r] += f == e && k < i;
+            same += f == e;
+            before += f == e && k < i;
         }
-        at[r] = less + before[r];
-        S.order[at[r]] = (uint16_t)i;
-        start[r] = e != kNoExpert && before[r] % chunk_max == 0;
+        S.order[less + before] = (uint16_t)i;
+        const int left = same - before;
+        S.len[less + before] = e != kNoExpert && before % chunk_max == 0 ? (uint16_t)min(left, chunk_max) : 0;
     }
-    if (threadIdx.x < kFewPairs / 32) S.starts[threadIdx.x] = 0;
     __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kFewPairs / kFewThreads; ++r)
-        if (start[r]) atomicOr(&S.starts[at[r] >> 5], 1u << (at[r] & 31));
-    __syncthreads();
-#pragma unroll
-    for (int r = 0; r < kFewPairs / kFewThreads; ++r) {
-        if (!start[r]) continue;
-        int c = __popc(S.starts[at[r] >> 5] & ((1u << (at[r] & 31)) - 1u));
-        for (int i = 0; i < at[r] >> 5; ++i) c += __popc(S.starts[i]);
-        const int left = same[r] - before[r];
-        S.chunk[c].e = S.ids[threadIdx.x + r * kFewThreads];
-        S.chunk[c].first = (uint16_t)at[r];
-        S.chunk[c].count = (uint16_t)(left < chunk_max ? left : chunk_max);
-    }
-    if (threadIdx.x == 0) {
+    if (warp == 0) {
         int n = 0;
-        for (int i = 0; i < kFewPairs / 32; ++i) n += __popc(S.starts[i]);
-        S.chunks = n;
+        for (int i0 = 0; i0 < pairs; i0 += 32) {
+            const int i = i0 + lane, len = i < pairs ? S.len[i] : 0;
+            const unsigned starts = __ballot_sync(kFull, len != 0);
+            if (len != 0) {
+                const int c = n + __popc(starts & ((1u << lane) - 1u));
+                S.chunk_e[c] = S.ids[S.order[i]];
+                S.chunk_first[c] = (uint16_t)i;
+                S.chunk_len[c] = (uint16_t)len;
+            }
+            n += __popc(starts);
+        }
+        if (lane == 0) *S.chunks = n;
     }
-    (void)lane;
     __syncthreads();
 }
 
-// 16 bytes of weights, read once.
-__device__ __forceinline__ uint4 load_weights(const uint8_t *p)
+// 32 bytes of weights, read once. WIDE: at once, or in two loads of 16 (rows that do
+// not all start on 32 bytes; the second half may lie behind the row).
+struct Raw32 {
+    uint32_t w[8];
+};
+
+__device__ __forceinline__ void load_weights32(Raw32 &v, const uint8_t *p)
 {
-    uint4 v;
-    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
-        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+    asm("ld.global.nc.L1::no_allocate.L2::evict_first.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(v.w[0]), "=r"(v.w[1]), "=r"(v.w[2]), "=r"(v.w[3]), "=r"(v.w[4]), "=r"(v.w[5]), "=r"(v.w[6]),
+          "=r"(v.w[7])
         : "l"(p));
-    return v;
+}
+
+__device__ __forceinline__ void load_weights16(uint32_t *w, const uint8_t *p)
+{
+    asm("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+        : "l"(p));
 }
 
 // 16 bytes of x or h. Not the read-only path: h was written by the kernel before,
 // which this one may have started under.
-__device__ __forceinline__ uint4 load_x(const uint8_t *p)
+__device__ __forceinline__ uint4 load_x(const void *p)
 {
     uint4 v;
     asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -235,8 +259,9 @@ __device__ __forceinline__ uint32_t two_codes(uint32_t codes)
 }
 
 // DOWN: the second kernel. `rows`: of down per CTA, in tiles of `tile_rows`; `pass`:
-// tiles whose outputs fit in shared memory at once.
-template <int DT, bool F8, int NT, bool DOWN>
+// tiles whose outputs fit in shared memory at once. WIDE: rows of weights start on 32
+// bytes.
+template <int DT, bool F8, int NT, bool DOWN, bool WIDE>
 __global__ void __launch_bounds__(kFewThreads, 1)
 few_kernel(const FewArgs a, int rows, int tile_rows, int pass)
 {
@@ -246,9 +271,12 @@ few_kernel(const FewArgs a, int rows, int tile_rows, int pass)
     constexpr int EPC = 16 / WB;                         // weights in 16 bytes
     constexpr int STEP = kStepBytes / WB;                // k per step
     constexpr int NC = 8 * NT;                           // tokens of a chunk at most
-    extern __shared__ uint8_t smem[];
-    FewPlan &S = *reinterpret_cast<FewPlan *>(smem);
-    float4 *pieces = reinterpret_cast<float4 *>(smem + sizeof(FewPlan));     // [warp][2][NT][32]
+    // x of so many half steps is loaded before their products, in at most 32 registers
+    constexpr int XV = F8 ? 2 : 1, XH = NT * XV <= 2 ? 4 : NT * XV == 4 ? 2 : 1;
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int pairs = a.T * a.top_k;
+    const FewPlan S(smem, pairs);
+    float4 *pieces = reinterpret_cast<float4 *>(smem + FewPlan::bytes(pairs));   // [warp][2][NT][32]
     float *out = reinterpret_cast<float *>(pieces + kFewWarps * 2 * NT * 32);    // DOWN: [pair][row]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int K = DOWN ? a.I : a.H;                      // summed over
@@ -266,42 +294,41 @@ few_kernel(const FewArgs a, int rows, int tile_rows, int pass)
     const int row_begin = DOWN ? (int)blockIdx.x * rows : 0;
     const int row_end = DOWN ? min(row_begin + rows, a.H) : a.I;
     const int row_tiles = DOWN ? (row_end - row_begin + tile_rows - 1) / tile_rows : (a.I + 7) / 8;
-
     bool waited = !DOWN;
     for (int pass0 = 0; pass0 < (DOWN ? row_tiles : 1); pass0 += pass) {
         const int per_chunk = DOWN ? min(pass, row_tiles - pass0) : row_tiles;
-        const int64_t all = (int64_t)S.chunks * per_chunk;
+        const int64_t all = (int64_t)*S.chunks * per_chunk;
         const int tile0 = DOWN ? 0 : (int)(all * blockIdx.x / gridDim.x);
         const int tile1 = DOWN ? (int)all : (int)(all * (blockIdx.x + 1) / gridDim.x);
         const int64_t work = (int64_t)(tile1 - tile0) * steps;
         auto begin_of = [&](int w) { return work * w / kFewWarps; };
         const int64_t begin = begin_of(warp), end = begin_of(warp + 1);
+        const int first_tile = tile0 + (int)(begin / steps), first_m = (int)(begin % steps);
 
-        // what is loaded: rows p0, p1 of a tile from step `m` on, n steps of it
-        struct Group { int tile, m, n; };
-        auto group_at = [&](int64_t at) {
-            Group r;
-            const int local = (int)(at / steps);
-            r.tile = tile0 + local;
-            r.m = (int)(at - (int64_t)local * steps);
-            const int64_t n = min((int64_t)(steps - r.m), end - at);
-            r.n = (int)min((int64_t)kDepth, max(n, (int64_t)0));
+        // steps m .. m + n of a tile, loaded together
+        struct Group {
+            int tile, m, n;
+        };
+        int64_t ungrouped = end - begin;
+        auto group_at = [&](int tile, int m) {
+            Group r{tile, m, (int)min((int64_t)min(kDepth, steps - m), ungrouped)};
+            ungrouped -= r.n;
             return r;
         };
-        const uint8_t *p0 = nullptr, *p1 = nullptr;
-        const float *s0 = nullptr, *s1 = nullptr;
+        const uint8_t *p0 = nullptr, *p1 = nullptr;      // this lane's rows g, g + 8, or NULL
+        const float *s0 = nullptr, *s1 = nullptr;        // their scales
         int loading = -1;
         auto point = [&](int tile) {
             if (tile == loading) return;
             loading = tile;
             const int c = tile / per_chunk, r = tile - c * per_chunk;
-            const int64_t e = S.chunk[c].e;
+            const int64_t e = S.chunk_e[c], row_bytes = (int64_t)K * WB;
             if constexpr (DOWN) {
                 const int first = row_begin + (pass0 + r) * tile_rows;
                 const int top = min(first + tile_rows, row_end), r0 = first + g, r1 = r0 + 8;
-                const uint8_t *base = static_cast<const uint8_t *>(a.down) + t * 16;
-                p0 = r0 < top ? base + (e * a.H + r0) * K * WB : nullptr;
-                p1 = r1 < top ? base + (e * a.H + r1) * K * WB : nullptr;
+                const uint8_t *base = static_cast<const uint8_t *>(a.down) + e * a.H * row_bytes + t * 32;
+                p0 = r0 < top ? base + r0 * row_bytes : nullptr;
+                p1 = r1 < top ? base + r1 * row_bytes : nullptr;
                 if constexpr (F8) {
                     const int64_t nb = (a.H + 127) / 128;
                     s0 = a.down_scales + (e * nb + (r0 < top ? r0 : first) / 128) * kb;
@@ -309,7 +336,7 @@ few_kernel(const FewArgs a, int rows, int tile_rows, int pass)
                 }
             } else {
                 const int row = r * 8 + g;
-                const int64_t off = (e * a.I + row) * K * WB + t * 16;
+                const int64_t off = (e * a.I + row) * row_bytes + t * 32;
                 p0 = row < a.I ? static_cast<const uint8_t *>(a.gate) + off : nullptr;
                 p1 = row < a.I ? static_cast<const uint8_t *>(a.up) + off : nullptr;
                 if constexpr (F8) {
@@ -319,24 +346,32 @@ few_kernel(const FewArgs a, int rows, int tile_rows, int pass)
                 }
             }
         };
-        uint4 buf[kDepth][2][2];                          // [step][half][row]
-        float scale[kDepth][2];
+        Raw32 buf[kDepth][2];                              // [step][row]
+        float scale[F8 ? kDepth : 1][2];
+        (void)scale;
         auto issue = [&](int i, const Group &r) {
+            const int k = (r.m + i) * STEP + t * 2 * EPC;
+            const int64_t off = (int64_t)(r.m + i) * kStepBytes;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = (r.m + i) * STEP + h * (STEP / 2) + t * EPC;
-                const int64_t off = (int64_t)(r.m + i) * kStepBytes + h * (kStepBytes / 2);
-                const bool in = i < r.n && k < K;
-                buf[i][h][0] = in && p0 != nullptr ? load_weights(p0 + off) : make_uint4(0u, 0u, 0u, 0u);
-                buf[i][h][1] = in && p1 != nullptr ? load_weights(p1 + off) : make_uint4(0u, 0u, 0u, 0u);
+            for (int b = 0; b < 2; ++b) {
+                const uint8_t *p = b ? p1 : p0;
+                const bool in = i < r.n && p != nullptr;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) buf[i][b].w[q] = 0;
+                if constexpr (WIDE) {
+                    if (in && k < K) load_weights32(buf[i][b], p + off);
+                } else {
+                    if (in && k < K) load_weights16(buf[i][b].w, p + off);
+                    if (in && k + EPC < K) load_weights16(buf[i][b].w + 4, p + off + 16);
+                }
             }
             if constexpr (F8) {
                 scale[i][0] = i < r.n ? __ldg(s0 + r.m + i) : 0.0f;
                 scale[i][1] = i < r.n ? __ldg(s1 + r.m + i) : 0.0f;
             }
         };
-        Group now = group_at(begin);
-        if (begin < end) {
+        Group now = group_at(first_tile, first_m);
+        if (now.n > 0) {
             point(now.tile);
 #pragma unroll
             for (int i = 0; i < kDepth; ++i) issue(i, now);
@@ -347,184 +382,211 @@ few_kernel(const FewArgs a, int rows, int tile_rows, int pass)
             waited = true;
         }
 
-        const uint8_t *px[NT];
-        int computing = -1;
+        const uint8_t *px[NT];                           // x (h) of this lane's tokens
+        int x_off = 0, count = 0;                        // FP32: of token `lane`
         float c[NT][4];
         constexpr int FR = DT == DT_F32 ? NC : 1;
-        float f[FR][2];                                   // FP32: this lane's part of rows g, g + 8
+        float f[FR][2];                                  // FP32: this lane's part of rows g, g + 8
         (void)f;
-        auto clear = [&] {
+        int split = -1;                                  // a tile that begins here and goes on in later warps
+        // once over the groups, then once more for a split tile: one copy of the
+        // code that finishes a tile, which comes from memory on every launch
+#pragma unroll 1
+        for (int round = 0; round < 2; ++round) {
+            bool fresh = true;
+#pragma unroll 1
+            while (round == 0 ? now.n > 0 : split >= 0) {
+                int tile;
+                bool whole;
+                if (round == 0) {
+                    tile = now.tile;
+                    if (fresh) {
+                        // another tile
+                        fresh = false;
+                        const int ch = tile / per_chunk, first = S.chunk_first[ch];
+                        count = S.chunk_len[ch];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) c[n][i] = 0.0f;
-#pragma unroll
-            for (int n = 0; n < FR; ++n) f[n][0] = f[n][1] = 0.0f;
-        };
-        clear();
-        // a tile's sums: c[n][0..1] row g, tokens 8 n + 2 t and the next; c[n][2..3] row g + 8
-        auto finish = [&](int tile, const float (&v)[NT][4]) {
-            const int ch = tile / per_chunk, r = tile - ch * per_chunk;
-            const int first = S.chunk[ch].first, count = S.chunk[ch].count;
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int tok = n * 8 + 2 * t + q;
-                    if (tok >= count) continue;
-                    const int pair = S.order[first + tok];
-                    if constexpr (DOWN) {
-                        float *o = out + pair * (pass * tile_rows) + r * tile_rows;
-                        if (g < tile_rows) o[g] = v[n][q];
-                        if (g + 8 < tile_rows) o[g + 8] = v[n][2 + q];
-                    } else {
-                        const int row = r * 8 + g;
-                        const float z = v[n][q], h = z / (1.0f + expf(-z)) * v[n][2 + q];
-                        if (row < a.I) static_cast<T *>(a.h)[(int64_t)pair * a.I + row] = Elem<DT>::from_f(h);
-                    }
-                }
-        };
-        int64_t at = begin;
-        while (at < end) {
-            // the next group's loads take the places of this one's
-            const int64_t then = at + now.n;
-            const Group next = then < end ? group_at(then) : Group{now.tile, 0, 0};
-            const int ch = now.tile / per_chunk;
-            if (ch != computing) {
-                computing = ch;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const int tok = n * 8 + g;
-                    px[n] = nullptr;
-                    if (DT != DT_F32 && tok < S.chunk[ch].count) {
-                        const int pair = S.order[S.chunk[ch].first + tok];
-                        px[n] = DOWN ? static_cast<const uint8_t *>(a.h) + (int64_t)pair * K * sizeof(T)
-                                     : static_cast<const uint8_t *>(a.x) + (int64_t)(pair / a.top_k) * K * sizeof(T);
-                    }
-                }
-            }
-            const int count = S.chunk[ch].count;
-            point(next.tile);
-#pragma unroll
-            for (int i = 0; i < kDepth; ++i) {
-                float part[F8 ? NT : 1][4];
-                if constexpr (F8) {
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) part[n][q] = 0.0f;
-                }
-                if (i < now.n) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int k = (now.m + i) * STEP + h * (STEP / 2) + t * EPC;
-                        const uint32_t w0[4] = {buf[i][h][0].x, buf[i][h][0].y, buf[i][h][0].z, buf[i][h][0].w};
-                        const uint32_t w1[4] = {buf[i][h][1].x, buf[i][h][1].y, buf[i][h][1].z, buf[i][h][1].w};
-                        if constexpr (DT == DT_F32) {
-                            const int first = S.chunk[ch].first;
-#pragma unroll
-                            for (int n = 0; n < NC; ++n) {
-                                if (n >= count) continue;
-                                const int pair = S.order[first + n];
-                                const float *row = DOWN ? static_cast<const float *>(a.h) + (int64_t)pair * K
-                                                        : static_cast<const float *>(a.x) + (int64_t)(pair / a.top_k) * K;
-                                Vec16 xv;
-                                xv.u = k < K ? load_x(reinterpret_cast<const uint8_t *>(row + k)) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-                                for (int q = 0; q < 4; ++q) {
-                                    f[n][0] = fmaf(__uint_as_float(w0[q]), xv.f[q], f[n][0]);
-                                    f[n][1] = fmaf(__uint_as_float(w1[q]), xv.f[q], f[n][1]);
-                                }
+                        for (int n = 0; n < NT; ++n) {
+                            const int tok = n * 8 + g;
+                            px[n] = nullptr;
+                            if (DT != DT_F32 && tok < count) {
+                                const int pair = S.order[first + tok];
+                                px[n] = DOWN ? static_cast<const uint8_t *>(a.h) + (int64_t)pair * K * sizeof(T)
+                                             : static_cast<const uint8_t *>(a.x) + (int64_t)(pair / a.top_k) * K * sizeof(T);
                             }
-                        } else {
-                            uint32_t w0x[F8 ? 8 : 4], w1x[F8 ? 8 : 4];
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) c[n][q] = 0.0f;
+                        }
+                        if constexpr (DT == DT_F32) {
+                            const int pair = S.order[first + min(lane, count - 1)];
+                            x_off = (DOWN ? pair : pair / a.top_k) * K;
+#pragma unroll
+                            for (int n = 0; n < FR; ++n) f[n][0] = f[n][1] = 0.0f;
+                        }
+                    }
+                    // the next group's loads take the places of this one's
+                    const bool done = now.m + now.n == steps;
+                    const Group next = group_at(done ? tile + 1 : tile, done ? 0 : now.m + now.n);
+                    if (next.n > 0) point(next.tile);
+                    float part[F8 ? NT : 1][4];
+                    uint4 xs[XH][DT == DT_F32 ? 1 : NT][XV];
+                    (void)part;
+                    (void)xs;
+#pragma unroll
+                    for (int hs = 0; hs < 2 * kDepth; ++hs) {
+                        const int i = hs / 2, h = hs % 2;                // step, half of the 32 bytes
+                        if constexpr (DT != DT_F32) {
+                            if (hs % XH == 0) {
+#pragma unroll
+                                for (int j = 0; j < XH; ++j)
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                        for (int v = 0; v < XV; ++v) {
+                                            const int at = now.m + (hs + j) / 2;
+                                            const int k = at * STEP + t * 2 * EPC + (hs + j) % 2 * EPC;
+                                            xs[j][n][v] = px[n] != nullptr && (hs + j) / 2 < now.n && k < K
+                                                              ? load_x(px[n] + (int64_t)k * sizeof(T) + v * 16)
+                                                              : make_uint4(0u, 0u, 0u, 0u);
+                                        }
+                            }
+                        }
+                        if constexpr (F8) {
+                            if (h == 0) {
+#pragma unroll
+                                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                    for (int q = 0; q < 4; ++q) part[n][q] = 0.0f;
+                            }
+                        }
+                        const uint32_t *u0 = buf[i][0].w + 4 * h, *u1 = buf[i][1].w + 4 * h;
+                        if constexpr (DT == DT_F32) {
+                            // both halves of the step, four tokens at a time
+                            const float *x = static_cast<const float *>(DOWN ? a.h : a.x);
+                            const int k = (now.m + i) * STEP + t * 2 * EPC;
+#pragma unroll
+                            for (int n0 = 0; n0 < NC; n0 += 4) {
+                                if (n0 >= count || i >= now.n || h == 1) continue;
+                                Vec16 xv[4][2];
+#pragma unroll
+                                for (int n = 0; n < 4; ++n) {
+                                    const int off = __shfl_sync(kFull, x_off, n0 + n);
+                                    xv[n][0].u = k < K ? load_x(x + off + k) : make_uint4(0u, 0u, 0u, 0u);
+                                    xv[n][1].u = k + EPC < K ? load_x(x + off + k + EPC) : make_uint4(0u, 0u, 0u, 0u);
+                                }
+#pragma unroll
+                                for (int n = 0; n < 4; ++n)
+#pragma unroll
+                                    for (int q = 0; q < 8; ++q) {
+                                        f[n0 + n][0] = fmaf(__uint_as_float(u0[q]), xv[n][q / 4].f[q % 4], f[n0 + n][0]);
+                                        f[n0 + n][1] = fmaf(__uint_as_float(u1[q]), xv[n][q / 4].f[q % 4], f[n0 + n][1]);
+                                    }
+                            }
+                        } else if (i < now.n) {
+                            uint32_t v0[F8 ? 8 : 4], v1[F8 ? 8 : 4];
                             if constexpr (F8) {
 #pragma unroll
                                 for (int q = 0; q < 4; ++q) {
-                                    w0x[2 * q] = two_codes<DT>(w0[q] & 0xffffu);
-                                    w0x[2 * q + 1] = two_codes<DT>(w0[q] >> 16);
-                                    w1x[2 * q] = two_codes<DT>(w1[q] & 0xffffu);
-                                    w1x[2 * q + 1] = two_codes<DT>(w1[q] >> 16);
+                                    v0[2 * q] = two_codes<DT>(u0[q] & 0xffffu);
+                                    v0[2 * q + 1] = two_codes<DT>(u0[q] >> 16);
+                                    v1[2 * q] = two_codes<DT>(u1[q] & 0xffffu);
+                                    v1[2 * q + 1] = two_codes<DT>(u1[q] >> 16);
                                 }
                             } else {
 #pragma unroll
-                                for (int q = 0; q < 4; ++q) { w0x[q] = w0[q]; w1x[q] = w1[q]; }
+                                for (int q = 0; q < 4; ++q) { v0[q] = u0[q]; v1[q] = u1[q]; }
                             }
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
                                 if (n * 8 >= count) continue;
+                                float (&acc)[4] = F8 ? part[n] : c[n];
 #pragma unroll
-                                for (int v = 0; v < (F8 ? 2 : 1); ++v) {
-                                    const uint4 xv = px[n] != nullptr && k < K
-                                                         ? load_x(px[n] + (int64_t)k * sizeof(T) + v * 16)
-                                                         : make_uint4(0u, 0u, 0u, 0u);
-                                    float (&acc)[4] = F8 ? part[n] : c[n];
-                                    mma16<DT>(acc, w0x[4 * v], w1x[4 * v], w0x[4 * v + 1], w1x[4 * v + 1], xv.x, xv.y);
-                                    mma16<DT>(acc, w0x[4 * v + 2], w1x[4 * v + 2], w0x[4 * v + 3], w1x[4 * v + 3], xv.z, xv.w);
+                                for (int v = 0; v < XV; ++v) {
+                                    const uint4 xv = xs[hs % XH][n][v];
+                                    mma16<DT>(acc, v0[4 * v], v1[4 * v], v0[4 * v + 1], v1[4 * v + 1], xv.x, xv.y);
+                                    mma16<DT>(acc, v0[4 * v + 2], v1[4 * v + 2], v0[4 * v + 3], v1[4 * v + 3], xv.z, xv.w);
+                                }
+                            }
+                            if constexpr (F8) {
+                                if (h == 1) {
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n) {
+                                        c[n][0] = fmaf(part[n][0], scale[i][0], c[n][0]);
+                                        c[n][1] = fmaf(part[n][1], scale[i][0], c[n][1]);
+                                        c[n][2] = fmaf(part[n][2], scale[i][1], c[n][2]);
+                                        c[n][3] = fmaf(part[n][3], scale[i][1], c[n][3]);
+                                    }
                                 }
                             }
                         }
+                        if (h == 1) issue(i, next);
                     }
-                    if constexpr (F8) {
+                    now = next;
+                    if (!done && next.n > 0) continue;
+                    if constexpr (DT == DT_F32) {
+                        // the quad's lanes hold sums over their own k
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            c[n][0] = fmaf(part[n][0], scale[i][0], c[n][0]);
-                            c[n][1] = fmaf(part[n][1], scale[i][0], c[n][1]);
-                            c[n][2] = fmaf(part[n][2], scale[i][1], c[n][2]);
-                            c[n][3] = fmaf(part[n][3], scale[i][1], c[n][3]);
-                        }
+                        for (int n = 0; n < NC; ++n)
+#pragma unroll
+                            for (int r = 0; r < 2; ++r) {
+                                f[n][r] += __shfl_xor_sync(kFull, f[n][r], 1);
+                                f[n][r] += __shfl_xor_sync(kFull, f[n][r], 2);
+                                if (n % 8 / 2 == t) c[n / 8][r * 2 + n % 2] = f[n][r];
+                            }
                     }
-                }
-                issue(i, next);
-            }
-            const bool done = now.m + now.n == steps;
-            if (done || then == end) {
-                if constexpr (DT == DT_F32) {
-                    // the quad's lanes hold sums over their own k
+                    const bool begun = tile != first_tile || first_m == 0;       // here, not in an earlier warp
+                    whole = done && begun;
+                    if (!whole) {
+                        // part of a tile: 1 has its beginning, 0 has not
+                        if (begun) split = tile;
+                        float4 *to = pieces + ((warp * 2 + begun) * NT) * 32 + lane;
 #pragma unroll
-                    for (int n = 0; n < NC; ++n)
-#pragma unroll
-                        for (int r = 0; r < 2; ++r) {
-                            f[n][r] += __shfl_xor_sync(kFull, f[n][r], 1);
-                            f[n][r] += __shfl_xor_sync(kFull, f[n][r], 2);
-                            if (n % 8 / 2 == t) c[n / 8][r * 2 + n % 2] = f[n][r];
-                        }
-                }
-                const int64_t tile_begin = (int64_t)(now.tile - tile0) * steps;
-                if (done && begin <= tile_begin) {
-                    finish(now.tile, c);
+                        for (int n = 0; n < NT; ++n) to[n * 32] = make_float4(c[n][0], c[n][1], c[n][2], c[n][3]);
+                    }
+                    fresh = true;
                 } else {
-                    // part of a tile: 1 has its beginning, 0 has not
-                    float4 *to = pieces + ((warp * 2 + (begin <= tile_begin)) * NT) * 32 + lane;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) to[n * 32] = make_float4(c[n][0], c[n][1], c[n][2], c[n][3]);
-                }
-                clear();
-            }
-            at = then;
-            now = next;
-        }
-        __syncthreads();
-        if (begin < end) {
-            // a tile that begins here and goes on in later warps
-            const int last = (int)((end - 1) / steps);
-            const int64_t tile_begin = (int64_t)last * steps, tile_end = tile_begin + steps;
-            if (begin <= tile_begin && tile_end > end) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float4 v = pieces[((warp * 2 + 1) * NT + n) * 32 + lane];
-                    c[n][0] = v.x; c[n][1] = v.y; c[n][2] = v.z; c[n][3] = v.w;
-                }
-                for (int w = warp + 1; w < kFewWarps && begin_of(w) < tile_end; ++w) {
-                    if (begin_of(w) == begin_of(w + 1)) continue;
+                    whole = true;
+                    tile = split;
+                    split = -1;
+                    count = S.chunk_len[tile / per_chunk];
+                    const int64_t tile_end = (int64_t)(tile - tile0 + 1) * steps;
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        const float4 v = pieces[((w * 2) * NT + n) * 32 + lane];
-                        c[n][0] += v.x; c[n][1] += v.y; c[n][2] += v.z; c[n][3] += v.w;
+                        const float4 v = pieces[((warp * 2 + 1) * NT + n) * 32 + lane];
+                        c[n][0] = v.x; c[n][1] = v.y; c[n][2] = v.z; c[n][3] = v.w;
+                    }
+                    for (int w = warp + 1; w < kFewWarps && begin_of(w) < tile_end; ++w) {
+                        if (begin_of(w) == begin_of(w + 1)) continue;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const float4 v = pieces[((w * 2) * NT + n) * 32 + lane];
+                            c[n][0] += v.x; c[n][1] += v.y; c[n][2] += v.z; c[n][3] += v.w;
+                        }
                     }
                 }
-                finish(tile0 + last, c);
+                if (whole) {
+                    // c[n][0..1]: row g, tokens 8 n + 2 t and the next; c[n][2..3]: row g + 8
+                    const int ch = tile / per_chunk, r = tile - ch * per_chunk, first = S.chunk_first[ch];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            const int tok = n * 8 + 2 * t + q;
+                            if (tok >= count) continue;
+                            const int pair = S.order[first + tok];
+                            if constexpr (DOWN) {
+                                float *o = out + pair * (pass * tile_rows) + r * tile_rows;
+                                if (g < tile_rows) o[g] = c[n][q];
+                                if (g + 8 < tile_rows) o[g + 8] = c[n][2 + q];
+                            } else {
+                                const int row = r * 8 + g;
+                                const float z = c[n][q], h = z / (1.0f + expf(-z)) * c[n][2 + q];
+                                if (row < a.I) static_cast<T *>(a.h)[(int64_t)pair * a.I + row] = Elem<DT>::from_f(h);
+                            }
+                        }
+                }
             }
+            if (round == 0) __syncthreads();
         }
         if constexpr (DOWN) {
             __syncthreads();
@@ -546,33 +608,54 @@ few_kernel(const FewArgs a, int rows, int tile_rows, int pass)
     }
 }
 
-template <int DT, bool F8, int NT>
-cudaError_t launch_few_nt(const FewArgs &a, cudaStream_t s)
+template <int DT, bool F8, int NT, bool WIDE>
+cudaError_t launch_few_wide(const FewArgs &a, cudaStream_t s)
 {
-    auto up = few_kernel<DT, F8, NT, false>, down = few_kernel<DT, F8, NT, true>;
-    const size_t fixed = sizeof(FewPlan) + (size_t)kFewWarps * 2 * NT * 32 * sizeof(float4);
-    const int pairs = a.T * a.top_k, sms = device_sm_count();
+    static std::atomic<int> opted[kCachedDevices];
+    auto up = few_kernel<DT, F8, NT, false, WIDE>, down = few_kernel<DT, F8, NT, true, WIDE>;
+    const int pairs = a.T * a.top_k, ctas = device_sm_count();
+    const size_t fixed = FewPlan::bytes(pairs) + (size_t)kFewWarps * 2 * NT * 32 * sizeof(float4);
     // equal shares of down's rows, in equal tiles of at most 16
-    const int rows = (a.H + sms - 1) / sms, tiles = (rows + 15) / 16, tile_rows = (rows + tiles - 1) / tiles;
+    const int rows = (a.H + ctas - 1) / ctas, tiles = (rows + 15) / 16, tile_rows = (rows + tiles - 1) / tiles;
     const int fit = (int)((kFewSharedBytes - fixed) / ((size_t)pairs * tile_rows * sizeof(float)));
     const int pass = fit < tiles ? fit : tiles;
     const size_t smem = fixed + (size_t)pairs * pass * tile_rows * sizeof(float);
-    cudaError_t err = cudaFuncSetAttribute(up, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)fixed);
-    if (err == cudaSuccess) err = cudaFuncSetAttribute(down, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSharedBytes);
+    int dev = 0;
+    cudaError_t err = cudaGetDevice(&dev);
     if (err != cudaSuccess) return err;
+    const bool cached = dev >= 0 && dev < kCachedDevices;
+    if (!cached || opted[dev].load() == 0) {
+        err = cudaFuncSetAttribute(up, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSharedBytes);
+        if (err == cudaSuccess) err = cudaFuncSetAttribute(down, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFewSharedBytes);
+        if (err != cudaSuccess) return err;
+        if (cached) opted[dev].store(1);
+    }
     const int64_t up_tiles = (int64_t)pairs * ((a.I + 7) / 8);
-    err = launch_pdl(up, dim3((unsigned)(up_tiles < sms ? up_tiles : sms)), dim3(kFewThreads), fixed, s, a, 0, 0, 1);
+    err = launch_pdl(up, dim3((unsigned)(up_tiles < ctas ? up_tiles : ctas)), dim3(kFewThreads), fixed, s, a, 0, 0, 1);
     if (err != cudaSuccess) return err;
     return launch_pdl(down, dim3((unsigned)((a.H + rows - 1) / rows)), dim3(kFewThreads), smem, s, a, rows,
                       tile_rows, pass);
 }
 
+template <int DT, bool F8, int NT>
+cudaError_t launch_few_nt(const FewArgs &a, cudaStream_t s)
+{
+    const uint64_t wb = F8 ? 1 : sizeof(typename Elem<DT>::T);
+    const uint64_t at = reinterpret_cast<uintptr_t>(a.gate) | reinterpret_cast<uintptr_t>(a.up) |
+                        reinterpret_cast<uintptr_t>(a.down) | (uint64_t)a.H * wb | (uint64_t)a.I * wb;
+    return at % 32 == 0 ? launch_few_wide<DT, F8, NT, true>(a, s) : launch_few_wide<DT, F8, NT, false>(a, s);
+}
+
 template <int DT, bool F8>
 cudaError_t launch_few_form(const FewArgs &a, cudaStream_t s)
 {
-    if (a.T <= 8) return launch_few_nt<DT, F8, 1>(a, s);
-    if (a.T <= 16) return launch_few_nt<DT, F8, 2>(a, s);
-    return launch_few_nt<DT, F8, 4>(a, s);
+    // Two blocks of eight tokens per tile where experts have four and more on average:
+    // 8 experts of 4096 x 4096, top_k 2, us for 12, 24, 32 tokens: one block 131 142
+    // 163, two 134 136 137. 8-bit and FP32 weights take one: a second costs registers
+    // (8 bits: 80 94 112 against 103 113 117; FP32: 406 517 652 against 535 893 950).
+    if constexpr (!F8 && DT != DT_F32)
+        if (a.T * a.top_k >= 4 * a.E) return launch_few_nt<DT, F8, 2>(a, s);
+    return launch_few_nt<DT, F8, 1>(a, s);
 }
 
 }  // namespace
