@@ -897,7 +897,7 @@ typedef struct moe_few_experts {
  *   which adds in slot order. 8-bit weights meet unquantized activations: a
  *   block's 128 products are summed in FP32 and multiplied by its scale.
  *   Bit-reproducible.
- *   0 <= T <= 32, 1 <= E <= 1024, 1 <= top_k <= min(E, 32); H and I at most 2^20,
+ *   0 <= T <= 32, 1 <= E <= 1024, 1 <= top_k <= min(E, 32); H and I at most 65536,
  *   multiples of 16 bytes of weights (F32: 4, BF16 / F16: 8, e4m3: 16 elements);
  *   e4m3 weights need BF16 or F16 activations.
  *   workspace  moe_forward_few_workspace_size(T, I, top_k, dtype) bytes (holds h).

@@ -297,21 +297,22 @@ few_kernel(const FewArgs a, int rows, int tile_rows, int pass)
     bool waited = !DOWN;
     for (int pass0 = 0; pass0 < (DOWN ? row_tiles : 1); pass0 += pass) {
         const int per_chunk = DOWN ? min(pass, row_tiles - pass0) : row_tiles;
-        const int64_t all = (int64_t)*S.chunks * per_chunk;
-        const int tile0 = DOWN ? 0 : (int)(all * blockIdx.x / gridDim.x);
-        const int tile1 = DOWN ? (int)all : (int)(all * (blockIdx.x + 1) / gridDim.x);
-        const int64_t work = (int64_t)(tile1 - tile0) * steps;
-        auto begin_of = [&](int w) { return work * w / kFewWarps; };
-        const int64_t begin = begin_of(warp), end = begin_of(warp + 1);
-        const int first_tile = tile0 + (int)(begin / steps), first_m = (int)(begin % steps);
+        // kFewMaxDim keeps all of this within 31 bits
+        const int all = *S.chunks * per_chunk, share = all / (int)gridDim.x, rest = all - share * (int)gridDim.x;
+        auto tile_of = [&](int b) { return share * b + rest * b / (int)gridDim.x; };
+        const int tile0 = DOWN ? 0 : tile_of(blockIdx.x), tile1 = DOWN ? all : tile_of(blockIdx.x + 1);
+        const int work = (tile1 - tile0) * steps;
+        auto begin_of = [&](int w) { return (int)((int64_t)work * w / kFewWarps); };
+        const int begin = begin_of(warp), end = begin_of(warp + 1);
+        const int skipped = begin / steps, first_tile = tile0 + skipped, first_m = begin - skipped * steps;
 
         // steps m .. m + n of a tile, loaded together
         struct Group {
             int tile, m, n;
         };
-        int64_t ungrouped = end - begin;
+        int ungrouped = end - begin;
         auto group_at = [&](int tile, int m) {
-            Group r{tile, m, (int)min((int64_t)min(kDepth, steps - m), ungrouped)};
+            Group r{tile, m, min(min(kDepth, steps - m), ungrouped)};
             ungrouped -= r.n;
             return r;
         };
@@ -549,7 +550,7 @@ few_kernel(const FewArgs a, int rows, int tile_rows, int pass)
                     tile = split;
                     split = -1;
                     count = S.chunk_len[tile / per_chunk];
-                    const int64_t tile_end = (int64_t)(tile - tile0 + 1) * steps;
+                    const int tile_end = (tile - tile0 + 1) * steps;
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const float4 v = pieces[((warp * 2 + 1) * NT + n) * 32 + lane];

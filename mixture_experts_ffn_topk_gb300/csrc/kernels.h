@@ -275,7 +275,7 @@ cudaError_t launch_grouped_gemm_f8_wide(const GroupedF8 &g, unsigned *status, cu
 // The whole layer for a few tokens in two kernels. Routing from logits, or (logits
 // NULL) from indices and weights. gate_scales, up_scales, down_scales: NULL, or the
 // weights are e4m3 codes with these scales per 128 x 128 block.
-constexpr int kFewMaxTokens = 32, kFewMaxTopK = 32;
+constexpr int kFewMaxTokens = 32, kFewMaxTopK = 32, kFewMaxDim = 1 << 16;
 constexpr size_t kFewSharedBytes = 200 << 10;        // of a CTA at most
 struct FewArgs {
     const void *x;

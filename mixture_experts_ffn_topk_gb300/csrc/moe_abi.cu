@@ -91,7 +91,6 @@ constexpr uint64_t kMaxWaitLimitNs = 60ull * 1000000000ull;   // moe_set_wait_li
 constexpr int64_t kMaxRows = 0x7fffffff;   // dispatched rows are int32
 constexpr int64_t kMaxGroupedRows = 0x7fffffff - 1023;   // rows round up to a unit in int32
 constexpr int64_t kMaxGroupedDim = 1 << 24;      // N, K, I of the grouped products and checkpoints
-constexpr int64_t kMaxFewDim = 1 << 20;         // H, I of the few-token forward
 constexpr int64_t kMaxStride = int64_t(1) << 32; // their row strides (a TMA stride is below 2^40 bytes)
 
 // Vector width rule shared by the experts and combine kernels: rows are moved
@@ -1233,7 +1232,7 @@ static size_t few_workspace(int64_t T, int64_t I, int top_k, int dt)
 
 size_t moe_forward_few_workspace_size(int64_t T, int64_t I, int top_k, int dtype)
 {
-    if (T < 1 || T > kFewMaxTokens || I < 1 || I > kMaxFewDim || top_k < 1 || top_k > kFewMaxTopK ||
+    if (T < 1 || T > kFewMaxTokens || I < 1 || I > kFewMaxDim || top_k < 1 || top_k > kFewMaxTopK ||
         !valid_dtype(dtype))
         return 0;
     return few_workspace(T, I, top_k, dtype);
@@ -1255,8 +1254,8 @@ static int forward_few(const char *name, const void *x, int dtype, const void *l
     if (E < 1 || E > kMaxE || top_k < 1 || top_k > E || top_k > kFewMaxTopK)
         return fail(MOE_ERR_SHAPE, "need 1 <= E <= 1024 and 1 <= top_k <= min(E, 32)");
     const int64_t mult = f8 ? 16 : 16 / (int64_t)elem_bytes(dtype);
-    if (H < 1 || I < 1 || H > kMaxFewDim || I > kMaxFewDim || H % mult != 0 || I % mult != 0)
-        return fail(MOE_ERR_SHAPE, "H and I must be multiples of 16 bytes of weights, and at most 2^20");
+    if (H < 1 || I < 1 || H > kFewMaxDim || I > kFewMaxDim || H % mult != 0 || I % mult != 0)
+        return fail(MOE_ERR_SHAPE, "H and I must be multiples of 16 bytes of weights, and at most 65536");
     if (T == 0) return MOE_OK;
     const void *routing = logits ? logits : weights;
     int rc = check_experts_ptrs(name, {x, routing, logits ? logits : indices, experts->gate, experts->up,

@@ -170,6 +170,40 @@ def test_odd_multiples_and_block_borders(dtype, f8):
         check(L.few(x, logits, 2, True), y, slack, dtype)
 
 
+@pytest.mark.parametrize("dtype,f8", KINDS)
+def test_outputs_of_the_down_product_in_passes(dtype, f8):
+    """1024 pairs: a CTA's outputs do not fit in shared memory at once."""
+    T, k, E, H, I = 32, 32, 33, 7168, 32
+    L = Layer(E, H, I, dtype, f8, 5)
+    x = torch.randn((T, H), generator=gen(6), device="cuda").to(dtype)
+    logits = torch.randn((T, E), generator=gen(7), device="cuda")
+    ids, w, ws = softmax_routing(logits, k, True)
+    y, slack = L.ref(x, ids, w, ws)
+    check(L.few(x, logits, k, True), y, slack, dtype)
+
+
+def test_the_largest_sizes():
+    """H and I at their limit."""
+    H = I = 65536
+    x = torch.randn((2, H), generator=gen(1), device="cuda").to(BF16)
+    gate = torch.empty((1, I, H), dtype=BF16, device="cuda").normal_(0, H ** -0.5, generator=gen(2))
+    up = torch.empty((1, I, H), dtype=BF16, device="cuda").normal_(0, H ** -0.5, generator=gen(3))
+    down = torch.empty((1, H, I), dtype=BF16, device="cuda").normal_(0, I ** -0.5, generator=gen(4))
+    y = moe.moe_forward_few(x, torch.zeros((2, 1), device="cuda"), gate, up, down, 1, True)
+    # the first and last columns against 64 bits (the products of all rows in FP32 first)
+    g, u = x.float() @ gate[0].float().T, x.float() @ up[0].float().T
+    h = g * torch.sigmoid(g) * u
+    rows = torch.tensor([0, 1, 127, 128, H // 2, H - 2, H - 1], device="cuda")
+    D = down[0, rows].double()
+    ref = h.double() @ D.T
+    # g and u of both sides: (H + 2) 2^-23 of terms of which sum |x w| is about 0.64 sqrt(H)
+    size = h.double().abs() @ D.abs().T
+    e = (H + 2) * U * 0.7 * H ** 0.5
+    slack = size * ((I + 2) * U + 2.0 ** -8) + (e * (1.1 * u.abs() + g.abs() + 1).double()) @ D.abs().T
+    check(y[:, rows], ref, slack, BF16)
+    assert torch.all(torch.isfinite(y))
+
+
 def test_ties_and_rows_without_a_softmax():
     E, H, I, k = 12, 64, 64, 3
     L = Layer(E, H, I, BF16, False, 3)
