@@ -11,6 +11,13 @@
 // expert's last unit may leave half a tile idle; with 64 rows per expert and less the
 // other form is faster.
 //
+// What bounds it is the epilogue's latency per block of k: a barrier, 128 columns out
+// of TMEM, 128 multiply-adds (256 issue cycles of an SM partition's two warps), a
+// barrier; some 950 cycles, where the MMAs take 512. Without the multiply-adds 16384
+// rows on 8 experts of 4096 x 4096 take 199 us instead of 241. Tried: paired
+// multiply-adds (320 against 273 us), four groups of epilogue warps with 64 columns
+// each (302), accumulators of 128 columns, four in turn (284).
+//
 // Per CTA (one per SM, 384 threads, persistent over the units):
 //   warp 0   TMA producer of the weights: half of 256 n x 128 k (16 KiB) per stage;
 //   warp 2   TMA producer of its 128 rows x 128 k (16 KiB), into the same stages;
@@ -45,8 +52,8 @@ constexpr int SCALE_STAGES = 3, SCALE_KB = 4;        // scales are staged for fo
 
 struct __align__(1024) Smem {
     uint8_t ring[STAGES * SLOT_BYTES];
-    float scale[SCALE_STAGES][SCALE_KB][ROWS];
-    float w_scale[SCALE_STAGES][SCALE_KB][2];
+    float scale[SCALE_STAGES][ROWS][SCALE_KB];
+    float w_scale[SCALE_STAGES][2][SCALE_KB];
     uint64_t scale_full[SCALE_STAGES];
     uint64_t scale_empty[SCALE_STAGES];
     uint64_t full[STAGES];
@@ -85,6 +92,33 @@ __device__ __forceinline__ void store32(uint8_t *p, const uint32_t (&v)[8])
                  : "memory");
 }
 
+// The four MMAs of a block and the commits of its stage and accumulator, under one
+// predicate. alo, blo: the low words of the operands' descriptors, whose high word is
+// the same; a step of 32 k is 32 bytes further, or 32 rows of 128 in an MN-major B.
+template <bool KN>
+__device__ __forceinline__ void block_mmas(uint32_t on, uint32_t d, uint32_t alo, uint32_t blo, uint32_t hi,
+                                           uint32_t idesc, uint32_t empty, uint32_t full)
+{
+    constexpr uint32_t SB = KN ? UK * 128 / 16 : UK / 16;
+    static_assert(BK / UK == 4 && UK / 16 == 2, "four steps, two units of 16 bytes each");
+    asm volatile(
+        "{\n\t.reg .pred q, p0, p1;\n\t.reg .b64 a, b;\n\t.reg .b32 x, y;\n\t.reg .b16 m;\n\t"
+        "setp.ne.u32 q, %0, 0;\n\tsetp.ne.u32 p0, 0, 0;\n\tsetp.eq.u32 p1, 0, 0;\n\t"
+        "mov.b64 a, {%2, %4};\n\tmov.b64 b, {%3, %4};\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%1], a, b, %5, p0;\n\t"
+        "add.u32 x, %2, 2;\n\tadd.u32 y, %3, %8;\n\tmov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%1], a, b, %5, p1;\n\t"
+        "add.u32 x, %2, 4;\n\tadd.u32 y, %3, %9;\n\tmov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%1], a, b, %5, p1;\n\t"
+        "add.u32 x, %2, 6;\n\tadd.u32 y, %3, %10;\n\tmov.b64 a, {x, %4};\n\tmov.b64 b, {y, %4};\n\t"
+        "@q tcgen05.mma.cta_group::2.kind::f8f6f4 [%1], a, b, %5, p1;\n\t"
+        "mov.b16 m, 3;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%6], m;\n\t"
+        "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%7], m;\n\t}"
+        ::"r"(on), "r"(d), "r"(alo), "r"(blo), "r"(hi), "r"(idesc), "r"(empty), "r"(full), "n"(SB), "n"(2 * SB),
+          "n"(3 * SB)
+        : "memory");
+}
 template <bool KN, bool OUT_F32>
 __global__ void __launch_bounds__(THREADS, 1)
 grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
@@ -176,23 +210,29 @@ grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
             int stage = 0, acc = 0;
             uint32_t phase = 0, acc_phase = 0;
             bool ok = true;
+            const uint64_t da = sdesc_k_sw128(ring + W_BYTES);
+            const uint64_t db = KN ? sdesc_mn_sw128(ring, W_BYTES) : sdesc_k_sw128(ring);
+            uint32_t alo = (uint32_t)da, blo = (uint32_t)db;
+            const uint32_t hi = (uint32_t)(da >> 32);
+            const uint32_t empty0 = smem_u32(&S.empty[0]), full0 = smem_u32(&S.acc_full[0]);
             for (int unit = unit0; unit < total && ok; unit += unit_step) {
                 const Unit u = walk.at(unit);
                 const uint32_t idesc = idesc_e4m3(2 * ROWS, cols_of(u.w0), false, KN);
                 for (int kb = 0; kb < num_kb; ++kb) {
-                    ok = warp_wait_both(&S.acc_empty[acc], acc_phase ^ 1u, &S.full[stage], phase, abort_flag, p.status, p.wait_ns);
+                    ok = warp_wait_both(&S.acc_empty[acc], acc_phase ^ 1u, &S.full[stage], phase, abort_flag,
+                                        p.status, p.wait_ns);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t d = tmem_base + (uint32_t)(acc * COLS);
-                    const uint32_t w = ring + stage * SLOT_BYTES, a = w + W_BYTES;
-#pragma unroll
-                    for (int k = 0; k < BK / UK; ++k)
-                        umma_f8_on<2>(on, d, sdesc_k_sw128(a + k * UK),
-                                      KN ? sdesc_mn_sw128(w + k * UK * 128, W_BYTES) : sdesc_k_sw128(w + k * UK), idesc,
-                                      k ? 1u : 0u);
-                    commit_on<2>(on, &S.empty[stage]);
-                    commit_on<2>(on, &S.acc_full[acc]);
-                    if (++stage == STAGES) { stage = 0; phase ^= 1u; }
+                    block_mmas<KN>(on, tmem_base + (uint32_t)(acc * COLS), alo, blo, hi, idesc, empty0 + stage * 8,
+                                   full0 + acc * 8);
+                    alo += SLOT_BYTES / 16;
+                    blo += SLOT_BYTES / 16;
+                    if (++stage == STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                        alo -= STAGES * (SLOT_BYTES / 16);
+                        blo -= STAGES * (SLOT_BYTES / 16);
+                    }
                     if (++acc == ACCS) { acc = 0; acc_phase ^= 1u; }
                 }
             }
@@ -218,10 +258,10 @@ grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
                     if (!ok) break;
                     if (kb + k < num_kb) {
                         const float *src = p.a_scales + (int64_t)(u.row0 + rank * ROWS + lane / 4) * num_kb + kb + k;
-                        float *dst = &S.scale[stage][k][lane / 4];
-                        for (int r = lane / 4; r < rows; r += 8, dst += 8, src += 8 * num_kb) copy4_async(dst, src);
+                        float *dst = &S.scale[stage][lane / 4][k];
+                        for (int r = lane / 4; r < rows; r += 8, dst += 8 * SCALE_KB, src += 8 * num_kb) copy4_async(dst, src);
                         if (lane < 8)
-                            copy4_async(&S.w_scale[stage][k][lane >> 2],
+                            copy4_async(&S.w_scale[stage][lane >> 2][k],
                                         p.w_scales + (KN ? ((int64_t)u.e * num_kb + kb + k) * n_blocks + nb
                                                          : ((int64_t)u.e * n_blocks + nb) * num_kb + kb + k));
                     }
@@ -239,8 +279,8 @@ grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
         const int mine = rank * ROWS + q * 32 + lane;    // this thread's row of the unit
         const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16) + group * BM;
         const uint32_t acc_free = mapa_shared(smem_u32(&S.acc_empty[0]), 0);
-        int acc = 0, stage = 0;
-        uint32_t acc_phase = 0, phase = 0;
+        int stage = 0;
+        uint32_t phase = 0, block = 0;               // blocks so far: accumulators and phases go by them
         for (int unit = unit0; unit < total; unit += unit_step) {
             const Unit u = walk.at(unit);
             float sums[4][32];                           // [chunk of 32 columns][column]
@@ -248,33 +288,48 @@ grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) sums[j][i] = 0.0f;
+            // NJ chunks of 32 columns. Four blocks per round of scales, two of them
+            // unrolled: what a block costs beside its multiply-adds is a chain of short
+            // instructions (1070 -> 950 cycles per block)
             auto add_blocks = [&](auto chunks) {
                 constexpr int NJ = decltype(chunks)::value;
-                for (int kb = 0; kb < num_kb; ++kb) {
-                    const int k = kb % SCALE_KB;
-                    if (k == 0 && !warp_wait<1>(&S.scale_full[stage], phase, abort_flag, p.status, p.wait_ns)) return false;
-                    const float s = S.scale[stage][k][q * 32 + lane] * S.w_scale[stage][k][group];
-                    if (!warp_wait<1>(&S.acc_full[acc], acc_phase, abort_flag, p.status, p.wait_ns)) return false;
-                    tc_fence_after();
-                    const uint32_t tbase = tlane + (uint32_t)(acc * COLS);
-                    // 16 columns are on their way while the 16 before are added up
-                    uint32_t v[2][16];
-                    if constexpr (NJ > 0) tmem_ld16(tbase, v[0]);
-#pragma unroll
-                    for (int j = 0; j < 2 * NJ; ++j) {
-                        tmem_ld_wait16(v[j & 1]);
-                        if (j + 1 < 2 * NJ) tmem_ld16(tbase + (j + 1) * 16, v[(j + 1) & 1]);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            sums[j / 2][j % 2 * 16 + i] = fmaf(__uint_as_float(v[j & 1][i]), s, sums[j / 2][j % 2 * 16 + i]);
-                    }
-                    tc_fence_before();
+                for (int kb = 0; kb < num_kb; kb += SCALE_KB) {
+                    if (!warp_wait<1>(&S.scale_full[stage], phase, abort_flag, p.status, p.wait_ns)) return false;
+                    const float4 sa = *reinterpret_cast<const float4 *>(S.scale[stage][q * 32 + lane]);
+                    const float4 sw = *reinterpret_cast<const float4 *>(S.w_scale[stage][group]);
+                    float s4[SCALE_KB] = {sa.x * sw.x, sa.y * sw.y, sa.z * sw.z, sa.w * sw.w};
                     __syncwarp();
-                    const bool last = k == SCALE_KB - 1 || kb + 1 == num_kb;
-                    arrive_relaxed_on(lane == 0, acc_free + acc * 8);
-                    arrive_on(lane == 0 && last, &S.scale_empty[stage]);
-                    if (last && ++stage == SCALE_STAGES) { stage = 0; phase ^= 1u; }
-                    if (++acc == ACCS) { acc = 0; acc_phase ^= 1u; }
+                    arrive_on(lane == 0, &S.scale_empty[stage]);
+                    if (++stage == SCALE_STAGES) { stage = 0; phase ^= 1u; }
+                    const int n = num_kb - kb;
+#pragma unroll 2
+                    for (int b = 0; b < SCALE_KB; ++b) {
+                        if (b >= n) break;
+                        const uint32_t acc = block & 1u;
+                        if (!__all_sync(0xffffffffu, mbar_try_wait(&S.acc_full[acc], block >> 1 & 1u)) &&
+                            !warp_wait<1>(&S.acc_full[acc], block >> 1 & 1u, abort_flag, p.status, p.wait_ns))
+                            return false;
+                        tc_fence_after();
+                        const uint32_t tbase = tlane + acc * COLS;
+                        const float s = s4[0];
+#pragma unroll
+                        for (int i = 0; i + 1 < SCALE_KB; ++i) s4[i] = s4[i + 1];
+                        // 16 columns are on their way while the 16 before are added up
+                        uint32_t v[2][16];
+                        if constexpr (NJ > 0) tmem_ld16(tbase, v[0]);
+#pragma unroll
+                        for (int j = 0; j < 2 * NJ; ++j) {
+                            tmem_ld_wait16(v[j & 1]);
+                            if (j + 1 < 2 * NJ) tmem_ld16(tbase + (j + 1) * 16, v[(j + 1) & 1]);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                sums[j / 2][j % 2 * 16 + i] = fmaf(__uint_as_float(v[j & 1][i]), s, sums[j / 2][j % 2 * 16 + i]);
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        arrive_relaxed_on(lane == 0, acc_free + acc * 8);
+                        ++block;
+                    }
                 }
                 return true;
             };
