@@ -1049,7 +1049,9 @@ def _quantize_outputs(rows: int, K: int, codes, scales, like, index: int, stream
         ldc = _ld("codes", codes, rows, K, _F8, index)
     if scales is None:
         scales = _empty((rows, _blocks(K)), torch.float32, like, stream)
-    return codes, ldc, scales, _dense("scales", scales, (rows, _blocks(K)), torch.float32, index)
+    else:
+        _dense("scales", scales, (rows, _blocks(K)), torch.float32, index)
+    return codes, ldc, scales, scales.data_ptr()
 
 
 def moe_quantize_rows(x: torch.Tensor, offsets=None, codes=None, scales=None, stream=None):
@@ -1162,13 +1164,14 @@ def _forward_few(name: str, x, routing, top_k: int, gate, up, down, gate_scales,
         e.down_scales = _dense("down_scales", down_scales, (E, h, i), f32, dev)
     if y is None:
         y = _empty((T, H), dt, x, stream)
-    yp = _dense("y", y, (T, H), dt, dev)
+    else:
+        _dense("y", y, (T, H), dt, dev)
     if workspace is None:
         workspace = _empty((T * top_k * I * dt.itemsize + 255) & -256, torch.uint8, x, stream)
     elif not workspace.is_cuda or workspace.get_device() != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous on cuda:{dev}")
     _enqueue(name, dev, stream, xp, _code(dt), *routing(dev, T, E), ctypes.byref(e), T, H, I, E, top_k, *tail,
-             yp, workspace.data_ptr(), workspace.numel() * workspace.element_size())
+             y.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return y
 
 
