@@ -21,7 +21,7 @@
 // take 128 rows, and these sums need no more than a few percent of the pipe. In the
 // first kernel rows 0-7 are gate rows and 8-15 the up rows of the same columns, so
 // that a thread holds both factors of its h; in the second 16 rows of down. Lane
-// (g, t) = (lane / 4, lane % 4) loads 16 bytes of rows g and g + 8 as they lie: the
+// (g, t) = (lane / 4, lane % 4) loads 32 bytes of rows g and g + 8 as they lie: the
 // order of k within an MMA is free as long as both operands have the same one, and
 // x is read in that order too (from L1). FP32 runs on FFMA in the same layout.
 //

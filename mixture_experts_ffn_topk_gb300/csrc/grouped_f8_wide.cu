@@ -281,8 +281,9 @@ grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
         const uint32_t acc_free = mapa_shared(smem_u32(&S.acc_empty[0]), 0);
         int stage = 0;
         uint32_t phase = 0, block = 0;               // blocks so far: accumulators and phases go by them
-        for (int unit = unit0; unit < total; unit += unit_step) {
-            const Unit u = walk.at(unit);
+        for (int unit = unit0; unit < S.seg.unit[p.E]; unit += unit_step) {
+            // found anew: nothing of the walk stays in registers beside the sums
+            const Unit u = UnitWalk<2, WideParams>(S.seg, p, 0).at(unit);
             float sums[4][32];                           // [chunk of 32 columns][column]
 #pragma unroll
             for (int j = 0; j < 4; ++j)
