@@ -818,8 +818,9 @@ int moe_swiglu_checkpoint_backward(const void *grad_h, int64_t ld, const void *c
  *   offsets NULL (every row), or [E + 1] int32: rows from offsets[E] on are
  *           left alone (as in moe_swiglu_checkpoint).
  *   0 <= rows <= 2^31 - 1024, 1 <= K <= 2^24, strides up to 2^32. x needs its
- *   elements' alignment, codes none; rows of x that all start on 16 bytes, with
- *   rows of codes on 8, are moved in vectors, others by element.
+ *   elements' alignment, codes none, scales and offsets 16 bytes; rows of x that all
+ *   start on 16 bytes, with rows of codes on 8, are moved in vectors, others by
+ *   element.
  * Errors: MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_ALIGN, MOE_ERR_CUDA.
  */
 int moe_quantize_rows(const void *x, int64_t ld, const int32_t *offsets, int64_t E, int64_t rows,
@@ -828,7 +829,9 @@ int moe_quantize_rows(const void *x, int64_t ld, const int32_t *offsets, int64_t
 /*
  * moe_swiglu_quantize -- moe_quantize_rows of h = g / (1 + exp(-g)) * u.
  *   g, u    [rows, I] in dtype, row stride ld (both), read only: the gate and up
- *           products. h is FP32, not rounded before it is quantized.
+ *           products. h is FP32, not rounded before it is quantized (from BF16 and
+ *           F16 rows within 2^-21 (1 + |g|) of itself; 1 / (1 + exp(-g)) below
+ *           2^-126 counts as 0).
  *   codes, scales, offsets, limits and errors as moe_quantize_rows.
  */
 int moe_swiglu_quantize(const void *g, const void *u, int64_t ld, const int32_t *offsets, int64_t E,

@@ -168,15 +168,19 @@ def test_quantized_value_is_near():
 
 @pytest.mark.parametrize("dtype", [BF16, F16, F32])
 @pytest.mark.parametrize("rows,I", SIZES)
-@pytest.mark.parametrize("case", ["spread", "small", "zeros"])
+@pytest.mark.parametrize("case", ["spread", "small", "zeros", "deep"])
 def test_swiglu_quantize(dtype, rows, I, case):
     gu = values(rows, 2 * I, dtype, rows * 17 + I, case)
+    if case == "deep":                 # gates whose sigmoid leaves FP32's normal range
+        gu[:, :I] = (-85 + 30 * gu[:, :I].float().clamp(-0.9, 0.9)).to(dtype)
+        gu[:, I:] *= 1000
     for g, u in ((gu[:, :I], gu[:, I:]), (gu[:, :I].contiguous(), gu[:, I:].contiguous())):
         codes, scales = moe.moe_swiglu_quantize(g, u)
         gd, ud = g.double(), u.double()
         h = gd * torch.sigmoid(gd) * ud
         rel = 16 * 2.0 ** -23 + (0 if dtype == F32 else 1) * 2.0 ** -21 * (1 + gd.abs())
-        slack = h.abs() * rel + 2.0 ** -126          # FP32's subnormals may be flushed
+        # a sigmoid below 2^-126 may count as 0, and so may an h
+        slack = h.abs() * rel + 2.0 ** -126 * (1 + (gd * ud).abs())
         p = torch.zeros((rows, up(I) * B), dtype=torch.float64, device="cuda")
         p[:, :I] = h.abs()
         m = p.view(rows, -1, B).amax(-1).clamp(min=2.0 ** -100)
