@@ -13,8 +13,10 @@
 //
 // What bounds it is the epilogue's latency per block of k: a barrier, 128 columns out
 // of TMEM, 128 multiply-adds (256 issue cycles of an SM partition's two warps), a
-// barrier; some 950 cycles, where the MMAs take 512. Without the multiply-adds 16384
-// rows on 8 experts of 4096 x 4096 take 199 us instead of 241. Tried: paired
+// barrier; some 800 cycles and 100 of a unit's stores, where the MMAs take 512. 16384
+// rows on 8 experts of 4096 x 4096 take 240 us; when the epilogue found its units by
+// itself they took 247, of which 191 were left without TMEM reads and multiply-adds,
+// 216 with the reads alone, 243 with the multiply-adds alone. Tried: paired
 // multiply-adds (320 against 273 us), four groups of epilogue warps with 64 columns
 // each (302), accumulators of 128 columns, four in turn (284).
 //
@@ -23,6 +25,7 @@
 //   warp 2   TMA producer of its 128 rows x 128 k (16 KiB), into the same stages;
 //   warp 1   of the even CTA: tcgen05.mma issuer, K = 32 per instruction, one
 //            accumulator of 256 columns per block, two in turn;
+//   warp 3   scales of its rows, four blocks at a time, and the unit they belong to;
 //   warps 4-7, 8-11  one group per 128 columns: sums stay in registers until the last
 //            block, and rows leave in 32-byte stores.
 //
@@ -54,6 +57,7 @@ struct __align__(1024) Smem {
     uint8_t ring[STAGES * SLOT_BYTES];
     float scale[SCALE_STAGES][ROWS][SCALE_KB];
     float w_scale[SCALE_STAGES][2][SCALE_KB];
+    int4 unit[SCALE_STAGES];             // rows' first and number, first column: of the scales' unit
     uint64_t scale_full[SCALE_STAGES];
     uint64_t scale_empty[SCALE_STAGES];
     uint64_t full[STAGES];
@@ -119,6 +123,7 @@ __device__ __forceinline__ void block_mmas(uint32_t on, uint32_t d, uint32_t alo
           "n"(3 * SB)
         : "memory");
 }
+
 template <bool KN, bool OUT_F32>
 __global__ void __launch_bounds__(THREADS, 1)
 grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_a,
@@ -135,7 +140,7 @@ grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) { mbar_init(&S.full[s], 1); mbar_init(&S.empty[s], 1); }
         for (int a = 0; a < ACCS; ++a) { mbar_init(&S.acc_full[a], 1); mbar_init(&S.acc_empty[a], 2 * EPI_WARPS); }
-        for (int s = 0; s < SCALE_STAGES; ++s) { mbar_init(&S.scale_full[s], 32); mbar_init(&S.scale_empty[s], EPI_WARPS); }
+        for (int s = 0; s < SCALE_STAGES; ++s) { mbar_init(&S.scale_full[s], 33); mbar_init(&S.scale_empty[s], EPI_WARPS); }
         mbar_init(&S.drain, 1);
         S.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -265,6 +270,8 @@ grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
                                         p.w_scales + (KN ? ((int64_t)u.e * num_kb + kb + k) * n_blocks + nb
                                                          : ((int64_t)u.e * n_blocks + nb) * num_kb + kb + k));
                     }
+                    if (lane == 0) S.unit[stage] = make_int4(u.row0, u.rows, u.w0, 0);       // kept by the arrival below
+                    arrive_on(lane == 0, &S.scale_full[stage]);
                     copies_arrive(&S.scale_full[stage]);
                     if (++stage == SCALE_STAGES) { stage = 0; phase ^= 1u; }
                 }
@@ -282,14 +289,17 @@ grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
         int stage = 0;
         uint32_t phase = 0, block = 0;               // blocks so far: accumulators and phases go by them
         for (int unit = unit0; unit < S.seg.unit[p.E]; unit += unit_step) {
-            // found anew: nothing of the walk stays in registers beside the sums
-            const Unit u = UnitWalk<2, WideParams>(S.seg, p, 0).at(unit);
+            // the unit comes with its first scales: to search for it took the epilogue
+            // some 1000 cycles (384 rows x 64 experts, 2048 -> 1408: 112 against 106 us)
+            if (!warp_wait<1>(&S.scale_full[stage], phase, abort_flag, p.status, p.wait_ns)) break;
+            const int4 u = S.unit[stage];        // x, y: first row and number of rows, z: first column
             float sums[4][32];                           // [chunk of 32 columns][column]
 #pragma unroll
             for (int j = 0; j < 4; ++j)
 #pragma unroll
                 for (int i = 0; i < 32; ++i) sums[j][i] = 0.0f;
-            // NJ chunks of 32 columns. Four blocks per round of scales, two of them
+            // NJ chunks of 32 columns: all, or none where the tile ends before this group
+            // (columns past a narrow tile are added up and not stored). Four blocks per round of scales, two of them
             // unrolled: what a block costs beside its multiply-adds is a chain of short
             // instructions (1070 -> 950 cycles per block)
             auto add_blocks = [&](auto chunks) {
@@ -334,17 +344,13 @@ grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
                 }
                 return true;
             };
-            const int nj = min(max(cols_of(u.w0) / 32 - 4 * group, 0), 4);
-            const bool ok = nj == 4   ? add_blocks(std::integral_constant<int, 4>())
-                            : nj == 3 ? add_blocks(std::integral_constant<int, 3>())
-                            : nj == 2 ? add_blocks(std::integral_constant<int, 2>())
-                            : nj == 1 ? add_blocks(std::integral_constant<int, 1>())
-                                      : add_blocks(std::integral_constant<int, 0>());
+            const bool ok = cols_of(u.z) > group * BM ? add_blocks(std::integral_constant<int, 4>())
+                                                      : add_blocks(std::integral_constant<int, 0>());
             if (!ok) break;
-            if (mine >= u.rows) continue;
+            if (mine >= u.y) continue;
             constexpr int ESZ = OUT_F32 ? 4 : 2, PER = 32 / ESZ;         // columns in 32 bytes
-            const int col0 = u.w0 + group * BM;
-            uint8_t *out = p.out + (int64_t)(u.row0 + mine) * p.out_row_bytes + (int64_t)col0 * ESZ;
+            const int col0 = u.z + group * BM;
+            uint8_t *out = p.out + (int64_t)(u.x + mine) * p.out_row_bytes + (int64_t)col0 * ESZ;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
 #pragma unroll
