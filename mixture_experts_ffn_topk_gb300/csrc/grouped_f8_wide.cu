@@ -52,12 +52,17 @@ constexpr int EPI_WARPS = 8;
 constexpr int ACCS = 2;
 constexpr int TMEM_COLS = ACCS * COLS;
 constexpr int SCALE_STAGES = 3, SCALE_KB = 4;        // scales are staged for four blocks at a time
+// Units that the scales' warp announces. It begins a unit when every warp of the
+// epilogue has taken scales of the third unit before it, at the least, and so has read
+// and stored the fourth.
+constexpr int UNITS = 4;
+static_assert(UNITS > SCALE_STAGES && (UNITS & (UNITS - 1)) == 0, "");
 
 struct __align__(1024) Smem {
     uint8_t ring[STAGES * SLOT_BYTES];
     float scale[SCALE_STAGES][ROWS][SCALE_KB];
     float w_scale[SCALE_STAGES][2][SCALE_KB];
-    int4 unit[SCALE_STAGES];             // rows' first and number, first column: of the scales' unit
+    int4 unit[UNITS];                    // first row, rows, first column
     uint64_t scale_full[SCALE_STAGES];
     uint64_t scale_empty[SCALE_STAGES];
     uint64_t full[STAGES];
@@ -252,7 +257,7 @@ grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
             // ------------------------------------------------------ scales
             // of this CTA's rows, four blocks at a time: four lanes to a row
             const int n_blocks = (p.N + BM - 1) / BM, k = lane & 3;
-            int stage = 0;
+            int stage = 0, slot = 0;
             uint32_t phase = 0;
             bool ok = true;
             for (int unit = unit0; unit < total && ok; unit += unit_step) {
@@ -270,11 +275,13 @@ grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
                                         p.w_scales + (KN ? ((int64_t)u.e * num_kb + kb + k) * n_blocks + nb
                                                          : ((int64_t)u.e * n_blocks + nb) * num_kb + kb + k));
                     }
-                    if (lane == 0) S.unit[stage] = make_int4(u.row0, u.rows, u.w0, 0);       // kept by the arrival below
+                    // ahead of the arrival below
+                    if (lane == 0 && kb == 0) S.unit[slot] = make_int4(u.row0, u.rows, u.w0, 0);
                     arrive_on(lane == 0, &S.scale_full[stage]);
                     copies_arrive(&S.scale_full[stage]);
                     if (++stage == SCALE_STAGES) { stage = 0; phase ^= 1u; }
                 }
+                slot = (slot + 1) % UNITS;
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
         }
@@ -283,16 +290,18 @@ grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
         asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int q = warp & 3;                          // TMEM lane quadrant of this warp
         const int group = warp >= 8 ? 1 : 0;             // columns [128 group, + 128)
-        const int mine = rank * ROWS + q * 32 + lane;    // this thread's row of the unit
         const uint32_t tlane = tmem_base + ((uint32_t)(q * 32) << 16) + group * BM;
         const uint32_t acc_free = mapa_shared(smem_u32(&S.acc_empty[0]), 0);
         int stage = 0;
-        uint32_t phase = 0, block = 0;               // blocks so far: accumulators and phases go by them
+        uint32_t phase = 0, block = 0, slot = 0;     // blocks so far: accumulators and phases go by them
         for (int unit = unit0; unit < S.seg.unit[p.E]; unit += unit_step) {
             // the unit comes with its first scales: to search for it took the epilogue
             // some 1000 cycles (384 rows x 64 experts, 2048 -> 1408: 112 against 106 us)
             if (!warp_wait<1>(&S.scale_full[stage], phase, abort_flag, p.status, p.wait_ns)) break;
-            const int4 u = S.unit[stage];        // x, y: first row and number of rows, z: first column
+            // and is read again for its stores, so that it takes no registers beside the
+            // sums (no spills; 1 %)
+            const volatile int4 &u = S.unit[slot];
+            slot = (slot + 1) % UNITS;
             float sums[4][32];                           // [chunk of 32 columns][column]
 #pragma unroll
             for (int j = 0; j < 4; ++j)
@@ -347,6 +356,7 @@ grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
             const bool ok = cols_of(u.z) > group * BM ? add_blocks(std::integral_constant<int, 4>())
                                                       : add_blocks(std::integral_constant<int, 0>());
             if (!ok) break;
+            const int mine = rank * ROWS + q * 32 + lane;            // this thread's row of the unit
             if (mine >= u.y) continue;
             constexpr int ESZ = OUT_F32 ? 4 : 2, PER = 32 / ESZ;         // columns in 32 bytes
             const int col0 = u.z + group * BM;
