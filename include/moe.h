@@ -855,7 +855,9 @@ int moe_quantize_weights(const void *w, int64_t E, int64_t N, int64_t K, int dty
  *             KB = ceil(K / 128).
  *   w         [E, N, K] (MOE_WEIGHT_NK) or [E, K, N] (MOE_WEIGHT_KN) e4m3, dense;
  *             w_scales [E, NB, KB] or [E, KB, NB] FP32, NB = ceil(N / 128).
- *             Any FP32 scales will do, also those of a checkpoint quantized elsewhere.
+ *             Any FP32 scales will do, also those of a checkpoint quantized elsewhere
+ *             and two whose product alone leaves FP32's range: a block counts
+ *             wherever its sum times both scales is an FP32 number.
  *   out       [rows, N] in out_dtype (F32, BF16 or F16), row stride ldo, written
  *             for the rows of every expert: out[r, n] = sum over the blocks b of
  *             a_scales[r, b] w_scales[e, n / 128, b] * (sum over k in b of

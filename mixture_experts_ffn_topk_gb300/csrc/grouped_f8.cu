@@ -20,7 +20,7 @@
 //   warp 2   TMA producer of the unit's rows x 128 k, into the same stages;
 //   warp 1   tcgen05.mma issuer, K = 32 per instruction, one accumulator of 64
 //            columns per block, four in turn;
-//   warp 3   the scales of four blocks at a time, copied into shared memory;
+//   warp 3   products of the rows' scales and the weights', four blocks at a time;
 //   warps 4-7, 8-11  epilogue, 32 columns each: TMEM is read in 8 x 8 blocks, in
 //            which a thread meets two of every eight columns, so that it fetches a
 //            quarter of the scales; sums stay in registers until the last block.
@@ -59,8 +59,9 @@ constexpr int PARTIAL_BYTES = CAP * BM * 4;
 struct __align__(1024) Smem {
     uint8_t ring[RING_BYTES];
     uint8_t stg[2][STG_BYTES];           // one per group of epilogue warps
-    float scale[SCALE_STAGES][SCALE_KB][CAP];
-    float w_scale[SCALE_STAGES][SCALE_KB];
+    float scale[SCALE_STAGES][SCALE_KB][CAP];            // a row's times the weights'
+    int8_t shift[SCALE_STAGES][SCALE_KB][CAP];           // (scales_apart) where plain is 0
+    int plain[SCALE_STAGES];                             // these products need no shift
     uint64_t full[MAX_STAGES];
     uint64_t empty[MAX_STAGES];
     uint64_t acc_full[ACCS];
@@ -108,13 +109,6 @@ __device__ __forceinline__ void fma2(uint64_t &sum, uint32_t v0, uint32_t v1, ui
         : "r"(v0), "r"(v1), "l"(s));
 }
 
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
-{
-    uint64_t r;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
 __device__ __forceinline__ float low(uint64_t v) { return __uint_as_float((uint32_t)v); }
 __device__ __forceinline__ float high(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
 
@@ -160,7 +154,7 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) { mbar_init(&S.full[s], 1); mbar_init(&S.empty[s], 1); }
         for (int a = 0; a < ACCS; ++a) { mbar_init(&S.acc_full[a], 1); mbar_init(&S.acc_empty[a], EPI_WARPS); }
-        for (int s = 0; s < SCALE_STAGES; ++s) { mbar_init(&S.scale_full[s], 32); mbar_init(&S.scale_empty[s], EPI_WARPS); }
+        for (int s = 0; s < SCALE_STAGES; ++s) { mbar_init(&S.scale_full[s], 1); mbar_init(&S.scale_empty[s], EPI_WARPS); }
         mbar_init(&S.drain, 1);
         S.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -264,7 +258,7 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
             __syncwarp();
         } else if (warp == 3) {
             // ------------------------------------------------------ scales
-            // of the unit's rows, four blocks at a time: four lanes to a row
+            // of the unit's rows times the weights', four blocks at a time: four lanes to a row
             const int n_blocks = (p.N + BM - 1) / BM, k = lane & 3;
             int stage = 0;
             uint32_t phase = 0;
@@ -273,22 +267,41 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 const Unit u = walk.at(unit);
                 const int nb = u.w0 / BM < n_blocks ? u.w0 / BM : 0;     // columns past N are not stored
                 for (int kb = kb_begin; kb < kb_end; kb += SCALE_KB) {
+                    float a[CAP / 8], w = 1.0f;
+                    const bool in = kb + k < kb_end;
+                    const float *src = p.a_scales + (int64_t)(u.row0 + lane / 4) * all_kb + kb + k;
+#pragma unroll
+                    for (int i = 0; i < CAP / 8; ++i, src += 8 * all_kb) a[i] = in && lane / 4 + 8 * i < u.rows ? __ldg(src) : 1.0f;
+                    if (in)
+                        w = __ldg(p.w_scales + (KN ? ((int64_t)u.e * all_kb + kb + k) * n_blocks + nb
+                                                   : ((int64_t)u.e * n_blocks + nb) * all_kb + kb + k));
                     ok = warp_wait<1>(&S.scale_empty[stage], phase ^ 1u, abort_flag, p.status, p.wait_ns);
                     if (!ok) break;
-                    if (kb + k < kb_end) {
-                        const float *src = p.a_scales + (int64_t)(u.row0 + lane / 4) * all_kb + kb + k;
-                        float *dst = &S.scale[stage][k][lane / 4];
-                        for (int r = lane / 4; r < u.rows; r += 8, dst += 8, src += 8 * all_kb) copy4_async(dst, src);
-                        if (lane < 4)
-                            copy4_async(&S.w_scale[stage][k],
-                                        p.w_scales + (KN ? ((int64_t)u.e * all_kb + kb + k) * n_blocks + nb
-                                                         : ((int64_t)u.e * n_blocks + nb) * all_kb + kb + k));
+                    bool plain = plain_scale(w);
+#pragma unroll
+                    for (int i = 0; i < CAP / 8; ++i) {
+                        plain = plain && plain_scale(a[i]);
+                        S.scale[stage][k][lane / 4 + 8 * i] = a[i] * w;
                     }
-                    copies_arrive(&S.scale_full[stage]);
+                    plain = __all_sync(0xffffffffu, plain);
+                    if (!plain) {                // rare: the products themselves
+                        plain = true;
+                        src -= CAP * all_kb;
+#pragma unroll 1
+                        for (int r = lane / 4; r < CAP; r += 8, src += 8 * all_kb) {
+                            const float v = in && r < u.rows ? __ldg(src) : 1.0f;
+                            const int which = scales_apart(v, w, S.scale[stage][k][r]);
+                            S.shift[stage][k][r] = (int8_t)which;
+                            plain = plain && which == 0;
+                        }
+                        plain = __all_sync(0xffffffffu, plain);
+                    }
+                    if (lane == 0) S.plain[stage] = plain;
+                    __syncwarp();
+                    arrive_on(lane == 0, &S.scale_full[stage]);
                     if (++stage == SCALE_STAGES) { stage = 0; phase ^= 1u; }
                 }
             }
-            asm volatile("cp.async.wait_all;" ::: "memory");
         }
     } else {
         // ------------------------------------------------------ epilogue
@@ -316,16 +329,24 @@ grouped_f8_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_consta
                 if (u.rows > group * 32) {
                     const uint32_t tbase = tlane + (uint32_t)(acc * CAP);
                     const float *sc = S.scale[stage][k] + group * 32 + 2 * (lane & 3);
-                    const float w = S.w_scale[stage][k];
-                    const uint64_t w2 = (uint64_t)__float_as_uint(w) << 32 | __float_as_uint(w);
+                    const int plain = S.plain[stage];
                     uint32_t v[2][16];
                     tmem_ld_blocks32(tbase, v[0]);
                     tmem_ld_blocks32(tbase + (16u << 16), v[1]);
                     uint64_t s2[4];
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) s2[i] = mul2(*reinterpret_cast<const uint64_t *>(sc + i * 8), w2);
+                    for (int i = 0; i < 4; ++i) s2[i] = *reinterpret_cast<const uint64_t *>(sc + i * 8);
                     tmem_ld_wait16(v[0]);
                     tmem_ld_wait16(v[1]);
+                    if (!plain) {
+                        const int8_t *shift = S.shift[stage][k] + group * 32 + 2 * (lane & 3);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const float f = shift_of(shift[i / 4 * 8 + (i & 1)]);
+                            v[0][i] = __float_as_uint(__uint_as_float(v[0][i]) * f);
+                            v[1][i] = __float_as_uint(__uint_as_float(v[1][i]) * f);
+                        }
+                    }
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
 #pragma unroll

@@ -1,6 +1,8 @@
 // grouped_f8.cuh -- what the two forms of the 8-bit grouped product share.
 #pragma once
 
+#include <cfloat>
+
 #include "common.cuh"
 #include "grouped_issue.cuh"
 #include "grouped_units.cuh"
@@ -62,16 +64,42 @@ __device__ __forceinline__ bool warp_wait_both(uint64_t *a, uint32_t pa, uint64_
     return warp_wait<1>(a, pa, abort_flag, status, limit_ns) && warp_wait<1>(b, pb, abort_flag, status, limit_ns);
 }
 
+// A block's two scales as one number s and a power of two k, so that (v k) s is v times
+// both, rounded once, where v is a block's sum: 0, or 2^-18 (the least product of two
+// codes) to 2^25 in magnitude. k is 1 where a w is a normal number, or 0 because a scale
+// is. A product below 2^-126 comes 2^100 times too large with k = 2^-100, one above
+// FP32's largest the other way round: v k is exact and normal in both. From 2^228 on
+// s is FP32's largest: (v k) s is infinite with all v but 0, as it should be.
+// Returns -1, 0 or 1 for the three k.
+constexpr float kScaleUp = 1.2676506002282294e30f, kScaleDown = 7.888609052210118e-31f;  // 2^100, 2^-100
+
+__device__ __forceinline__ int scales_apart(float a, float w, float &s)
+{
+    s = a * w;
+    const float lo = fabsf(a) < fabsf(w) ? a : w, hi = fabsf(a) < fabsf(w) ? w : a;
+    if (fabsf(s) < FLT_MIN && lo != 0.0f) {
+        s = (lo * kScaleUp) * hi;
+        return -1;
+    }
+    if (isinf(s) && !isinf(hi)) {
+        s = fminf(fmaxf((hi * kScaleDown) * lo, -FLT_MAX), FLT_MAX);
+        return 1;
+    }
+    return 0;
+}
+
+__device__ __forceinline__ float shift_of(int which) { return which == 0 ? 1.0f : which < 0 ? kScaleDown : kScaleUp; }
+
+// Whether the product of any two such scales is a normal number: 2^-63 <= |v| < 2^63.
+__device__ __forceinline__ bool plain_scale(float v)
+{
+    return (__float_as_uint(v) << 1) - (64u << 24) < (126u << 24);
+}
+
 // 4 bytes of global memory into shared memory, asynchronously.
 __device__ __forceinline__ void copy4_async(float *dst, const float *src)
 {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-
-// This thread's copies so far arrive on the barrier when they have landed.
-__device__ __forceinline__ void copies_arrive(uint64_t *bar)
-{
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
 // Bytes, row-major, of two or three dimensions, in boxes of 128 bytes by box_rows.

@@ -62,6 +62,7 @@ struct __align__(1024) Smem {
     uint8_t ring[STAGES * SLOT_BYTES];
     float scale[SCALE_STAGES][ROWS][SCALE_KB];
     float w_scale[SCALE_STAGES][2][SCALE_KB];
+    int plain[SCALE_STAGES];             // the products of these scales need no shift (scales_apart)
     int4 unit[UNITS];                    // first row, rows, first column
     uint64_t scale_full[SCALE_STAGES];
     uint64_t scale_empty[SCALE_STAGES];
@@ -145,7 +146,7 @@ grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) { mbar_init(&S.full[s], 1); mbar_init(&S.empty[s], 1); }
         for (int a = 0; a < ACCS; ++a) { mbar_init(&S.acc_full[a], 1); mbar_init(&S.acc_empty[a], 2 * EPI_WARPS); }
-        for (int s = 0; s < SCALE_STAGES; ++s) { mbar_init(&S.scale_full[s], 33); mbar_init(&S.scale_empty[s], EPI_WARPS); }
+        for (int s = 0; s < SCALE_STAGES; ++s) { mbar_init(&S.scale_full[s], 1); mbar_init(&S.scale_empty[s], EPI_WARPS); }
         mbar_init(&S.drain, 1);
         S.abort = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -255,11 +256,40 @@ grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
             __syncwarp();
         } else if (warp == 3) {
             // ------------------------------------------------------ scales
-            // of this CTA's rows, four blocks at a time: four lanes to a row
+            // of this CTA's rows, four blocks at a time: four lanes to a row. A stage is
+            // handed over when the next one's copies are under way; whether its products
+            // stay within FP32's range is found here, where there is time for it (in the
+            // epilogue the same took 6 to 8 % of the whole)
             const int n_blocks = (p.N + BM - 1) / BM, k = lane & 3;
-            int stage = 0, slot = 0;
+            int stage = 0, slot = 0, last = -1, last_rows = 0, last_n = 0;
             uint32_t phase = 0;
             bool ok = true;
+            auto hand_over = [&]() {
+                __syncwarp();
+                bool plain = lane >= 8 || k >= last_n || plain_scale(S.w_scale[last][lane >> 2 & 1][k]);
+#pragma unroll
+                for (int i = 0; i < ROWS / 32; ++i) {
+                    const float4 s = *reinterpret_cast<const float4 *>(S.scale[last][lane + 32 * i]);
+                    plain = plain && (lane + 32 * i >= last_rows ||
+                                      (plain_scale(s.x) && (last_n < 2 || plain_scale(s.y)) &&
+                                       (last_n < 3 || plain_scale(s.z)) && (last_n < 4 || plain_scale(s.w))));
+                }
+                plain = __all_sync(0xffffffffu, plain);
+                if (!plain) {                    // rare: the products themselves
+                    plain = true;
+#pragma unroll 1
+                    for (int r = lane; r < last_rows; r += 32)
+#pragma unroll 1
+                        for (int b = 0; b < SCALE_KB && b < last_n; ++b)
+                            for (int g = 0; g < 2; ++g) {
+                                float s;
+                                plain = plain && scales_apart(S.scale[last][r][b], S.w_scale[last][g][b], s) == 0;
+                            }
+                    plain = __all_sync(0xffffffffu, plain);
+                }
+                if (lane == 0) S.plain[last] = plain;
+                arrive_on(lane == 0, &S.scale_full[last]);
+            };
             for (int unit = unit0; unit < total && ok; unit += unit_step) {
                 const Unit u = walk.at(unit);
                 const int rows = min(u.rows - rank * ROWS, ROWS), nb = min(u.w0 / BM + (lane >> 2 & 1), n_blocks - 1);
@@ -275,15 +305,21 @@ grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
                                         p.w_scales + (KN ? ((int64_t)u.e * num_kb + kb + k) * n_blocks + nb
                                                          : ((int64_t)u.e * n_blocks + nb) * num_kb + kb + k));
                     }
-                    // ahead of the arrival below
+                    asm volatile("cp.async.commit_group;" ::: "memory");
                     if (lane == 0 && kb == 0) S.unit[slot] = make_int4(u.row0, u.rows, u.w0, 0);
-                    arrive_on(lane == 0, &S.scale_full[stage]);
-                    copies_arrive(&S.scale_full[stage]);
+                    if (last >= 0) {
+                        asm volatile("cp.async.wait_group 1;" ::: "memory");
+                        hand_over();
+                    }
+                    last = stage;
+                    last_rows = rows;
+                    last_n = num_kb - kb;
                     if (++stage == SCALE_STAGES) { stage = 0; phase ^= 1u; }
                 }
                 slot = (slot + 1) % UNITS;
             }
             asm volatile("cp.async.wait_all;" ::: "memory");
+            if (ok && last >= 0) hand_over();
         }
     } else {
         // ------------------------------------------------------ epilogue
@@ -308,48 +344,73 @@ grouped_f8_wide_kernel(const __grid_constant__ CUtensorMap map_w, const __grid_c
 #pragma unroll
                 for (int i = 0; i < 32; ++i) sums[j][i] = 0.0f;
             // NJ chunks of 32 columns: all, or none where the tile ends before this group
-            // (columns past a narrow tile are added up and not stored). Four blocks per round of scales, two of them
-            // unrolled: what a block costs beside its multiply-adds is a chain of short
-            // instructions (1070 -> 950 cycles per block)
+            // (columns past a narrow tile are added up and not stored). Four blocks per
+            // round of scales, two of them unrolled: what a block costs beside its
+            // multiply-adds is a chain of short instructions (1070 -> 950 cycles per block)
             auto add_blocks = [&](auto chunks) {
                 constexpr int NJ = decltype(chunks)::value;
-                for (int kb = 0; kb < num_kb; kb += SCALE_KB) {
-                    if (!warp_wait<1>(&S.scale_full[stage], phase, abort_flag, p.status, p.wait_ns)) return false;
-                    const float4 sa = *reinterpret_cast<const float4 *>(S.scale[stage][q * 32 + lane]);
-                    const float4 sw = *reinterpret_cast<const float4 *>(S.w_scale[stage][group]);
-                    float s4[SCALE_KB] = {sa.x * sw.x, sa.y * sw.y, sa.z * sw.z, sa.w * sw.w};
+                // a block's columns, on their way out of TMEM 16 at a time while the 16
+                // before are added up; SHIFT: times k first
+                auto add_block = [&](auto shift, float s, float k) {
+                    const uint32_t acc = block & 1u;
+                    if (!__all_sync(0xffffffffu, mbar_try_wait(&S.acc_full[acc], block >> 1 & 1u)) &&
+                        !warp_wait<1>(&S.acc_full[acc], block >> 1 & 1u, abort_flag, p.status, p.wait_ns))
+                        return false;
+                    tc_fence_after();
+                    const uint32_t tbase = tlane + acc * COLS;
+                    uint32_t v[2][16];
+                    if constexpr (NJ > 0) tmem_ld16(tbase, v[0]);
+#pragma unroll
+                    for (int j = 0; j < 2 * NJ; ++j) {
+                        tmem_ld_wait16(v[j & 1]);
+                        if (j + 1 < 2 * NJ) tmem_ld16(tbase + (j + 1) * 16, v[(j + 1) & 1]);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float f = __uint_as_float(v[j & 1][i]);
+                            if constexpr (decltype(shift)::value) f *= k;
+                            sums[j / 2][j % 2 * 16 + i] = fmaf(f, s, sums[j / 2][j % 2 * 16 + i]);
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    arrive_relaxed_on(lane == 0, acc_free + acc * 8);
+                    ++block;
+                    return true;
+                };
+                auto release = [&]() {
                     __syncwarp();
                     arrive_on(lane == 0, &S.scale_empty[stage]);
                     if (++stage == SCALE_STAGES) { stage = 0; phase ^= 1u; }
+                };
+                int kb = 0;
+                for (; kb < num_kb; kb += SCALE_KB) {
+                    if (!warp_wait<1>(&S.scale_full[stage], phase, abort_flag, p.status, p.wait_ns)) return false;
+                    const float4 sa = *reinterpret_cast<const float4 *>(S.scale[stage][q * 32 + lane]);
+                    const float4 sw = *reinterpret_cast<const float4 *>(S.w_scale[stage][group]);
+                    if (!S.plain[stage]) break;
+                    float s4[SCALE_KB] = {sa.x * sw.x, sa.y * sw.y, sa.z * sw.z, sa.w * sw.w};
+                    release();
                     const int n = num_kb - kb;
 #pragma unroll 2
                     for (int b = 0; b < SCALE_KB; ++b) {
                         if (b >= n) break;
-                        const uint32_t acc = block & 1u;
-                        if (!__all_sync(0xffffffffu, mbar_try_wait(&S.acc_full[acc], block >> 1 & 1u)) &&
-                            !warp_wait<1>(&S.acc_full[acc], block >> 1 & 1u, abort_flag, p.status, p.wait_ns))
-                            return false;
-                        tc_fence_after();
-                        const uint32_t tbase = tlane + acc * COLS;
                         const float s = s4[0];
 #pragma unroll
                         for (int i = 0; i + 1 < SCALE_KB; ++i) s4[i] = s4[i + 1];
-                        // 16 columns are on their way while the 16 before are added up
-                        uint32_t v[2][16];
-                        if constexpr (NJ > 0) tmem_ld16(tbase, v[0]);
-#pragma unroll
-                        for (int j = 0; j < 2 * NJ; ++j) {
-                            tmem_ld_wait16(v[j & 1]);
-                            if (j + 1 < 2 * NJ) tmem_ld16(tbase + (j + 1) * 16, v[(j + 1) & 1]);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                sums[j / 2][j % 2 * 16 + i] = fmaf(__uint_as_float(v[j & 1][i]), s, sums[j / 2][j % 2 * 16 + i]);
-                        }
-                        tc_fence_before();
-                        __syncwarp();
-                        arrive_relaxed_on(lane == 0, acc_free + acc * 8);
-                        ++block;
+                        if (!add_block(std::false_type(), s, 1.0f)) return false;
                     }
+                }
+                // the rest of a unit in which a product of scales leaves FP32's range
+#pragma unroll 1
+                for (; kb < num_kb; kb += SCALE_KB) {
+                    if (!warp_wait<1>(&S.scale_full[stage], phase, abort_flag, p.status, p.wait_ns)) return false;
+#pragma unroll 1
+                    for (int b = 0; b < SCALE_KB && kb + b < num_kb; ++b) {
+                        float s;
+                        const float k = shift_of(scales_apart(S.scale[stage][q * 32 + lane][b], S.w_scale[stage][group][b], s));
+                        if (!add_block(std::true_type(), s, k)) return false;
+                    }
+                    release();
                 }
                 return true;
             };

@@ -478,3 +478,59 @@ def test_rows_behind_2_gib():
     ref, size = ref_product(codes[-3:], scales[-3:], offsets_of([3]), w[1:], sw[1:], False)
     check(out[-3:], ref, slack_of(size, K), BF16, "last rows")
     assert torch.all(out[:-3] == 0) and torch.all(whole[:, N:] == 0)
+
+
+# Three forms by sizes: a cluster shares k, few rows per expert, many.
+FORMS = {"split": (1, 40, 144, 528), "few_rows": (64, 1300, 400, 528), "many_rows": (8, 1700, 1504, 528)}
+
+
+@pytest.mark.parametrize("form", sorted(FORMS))
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("case", ["small", "large", "zeros", "subnormal"])
+def test_products_of_scales_outside_fp32s_range(form, transposed, case):
+    """A block's contribution may be an ordinary number where the product of its two
+    scales alone is below FP32's normal numbers or above its largest. Beside the usual
+    slack, each block's use rounds to a multiple of 2^-149."""
+    E, rows, N, K = FORMS[form]
+    off = offsets_of(np.random.RandomState(3).multinomial(rows, np.ones(E) / E))
+    a, sa, w, sw = operands(rows, E, N, K, transposed, 17)
+    third = torch.arange(rows, device="cuda").view(-1, 1) % 3     # lanes of a warp differ
+    pick = lambda *p: torch.tensor(p, dtype=torch.float64, device="cuda")[third]
+    if case == "small":                # 2^-140 and less; sums of 2^-120
+        sw *= 2.0 ** -63
+        sa = (sa.double() * pick(2.0 ** 60, 2.0 ** -63, 2.0 ** -30)).float()
+    elif case == "large":              # 2^129 to 2^131; codes of a few 2^-9: sums of a block below 2^-7
+        a, w = (a.float() * 2.0 ** -13).to(F8), (w.float() * 2.0 ** -14).to(F8)
+        sw = (1 + torch.rand(sw.shape, generator=gen(5), device="cuda")) * 2.0 ** 64
+        sa = ((1 + torch.rand(sa.shape, generator=gen(6), device="cuda")).double() * pick(2.0 ** 65, 2.0 ** -60, 2.0 ** 40)).float()
+    elif case == "zeros":              # blocks of zero codes under scales whose product is 2^150
+        zero = (torch.arange(rows, device="cuda").view(-1, 1) + torch.arange(up(K), device="cuda")) % 2 == 0
+        a = torch.where(zero.repeat_interleave(B, 1)[:, :K], torch.zeros((), device="cuda"), a.float()).to(F8)
+        sa = torch.where(zero, sa * 2.0 ** 96, sa * 2.0 ** -54)
+        sw *= 2.0 ** 67
+    else:                              # scales that are subnormal or 0
+        sa = (sa.double() * pick(2.0 ** -136, 0.0, 1.0)).float()
+        sw *= 2.0 ** 100
+    ref, size = ref_product(a, sa, off, w, sw, transposed)
+    assert torch.isfinite(ref).all() and ref.abs().max() < 2.0 ** 126
+    for out_dtype in (F32, BF16):
+        out = moe.moe_grouped_gemm_f8(a, sa, off, w, sw, transposed=transposed, out_dtype=out_dtype)
+        check(out, ref, slack_of(size, K) + (up(K) + 2) * 2.0 ** -149, out_dtype, f"{case} {out_dtype}")
+
+
+@pytest.mark.parametrize("form", sorted(FORMS))
+def test_scales_that_are_not_finite(form):
+    """Infinite and NaN scales as FP32 arithmetic has them: a NaN scale, and an infinite
+    one over a block of zeros, make the row NaN, an infinite one over other sums an
+    infinity or NaN; other rows stay as they were."""
+    E, rows, N, K = FORMS[form]
+    off = offsets_of(np.random.RandomState(3).multinomial(rows, np.ones(E) / E))
+    a, sa, w, sw = operands(rows, E, N, K, False, 18)
+    want = moe.moe_grouped_gemm_f8(a, sa, off, w, sw, out_dtype=F32)
+    a.view(torch.uint8)[7, B:2 * B] = 0
+    sa[3, 2], sa[7, 1], sa[11, 0] = float("nan"), float("inf"), float("-inf")
+    got = moe.moe_grouped_gemm_f8(a, sa, off, w, sw, out_dtype=F32)
+    assert torch.isnan(got[3]).all() and torch.isnan(got[7]).all() and not torch.isfinite(got[11]).any()
+    same = torch.ones(rows, dtype=torch.bool, device="cuda")
+    same[[3, 7, 11]] = False
+    assert torch.equal(got[same], want[same])
