@@ -534,3 +534,70 @@ def test_scales_that_are_not_finite(form):
     same = torch.ones(rows, dtype=torch.bool, device="cuda")
     same[[3, 7, 11]] = False
     assert torch.equal(got[same], want[same])
+
+
+# At least 64 rows per expert: ten and more units per pair of CTAs, with one round of
+# staged scales per unit (K up to 512), two and more.
+@pytest.mark.parametrize("K", [16, 64, 128, 400, 512, 528, 1040])
+@pytest.mark.parametrize("N,transposed", [(3000, False), (2992, True)])
+@pytest.mark.parametrize("E", [16, 61])
+def test_many_units_of_experts_of_many_rows(E, N, K, transposed):
+    rows = 16384
+    r = np.random.RandomState(E + K)
+    counts = r.multinomial(rows - E, r.dirichlet(np.ones(E)))
+    counts[0], counts[1] = counts[0] + counts[1], 0        # one without rows
+    first = 5
+    off = offsets_of(counts, first)
+    a, sa, w, sw = operands(rows, E, N, K, transposed, E + N + K, pad=16)
+    sa *= 0.25                                             # F16 outputs stay finite
+    s = slice(first, first + int(counts.sum()))
+    ref, size = ref_product(a, sa, off, w, sw, transposed)
+    for out_dtype in (BF16, F16, F32):
+        whole = torch.full((rows, N + 8), -7.0, dtype=out_dtype, device="cuda")
+        out = moe.moe_grouped_gemm_f8(a, sa, off, w, sw, transposed=transposed, out=whole[:, :N])
+        check(out[s], ref[s], slack_of(size[s], K), out_dtype, str(out_dtype))
+        assert torch.all(whole[:first] == -7) and torch.all(whole[s.stop:] == -7) and torch.all(whole[:, N:] == -7)
+        again = moe.moe_grouped_gemm_f8(a, sa, off, w, sw, transposed=transposed, out_dtype=out_dtype)
+        assert torch.equal(out[s], again[s])               # bit-reproducible
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+@pytest.mark.parametrize("E,rows,N,K", [(16, 16384, 2992, 400), (16, 16384, 2992, 128), (256, 6000, 2000, 400)])
+def test_small_integers_over_many_units(E, rows, N, K, transposed):
+    """As test_small_integers_come_out_exactly, with many units per CTA in both forms."""
+    g = gen(2)
+    a = torch.randint(-8, 9, (rows, K), generator=g, device="cuda").float().to(F8)
+    w = torch.randint(-8, 9, (E, K, N) if transposed else (E, N, K), generator=g, device="cuda").float().to(F8)
+    sa = torch.exp2(torch.randint(-2, 3, (rows, up(K)), generator=g, device="cuda").float())
+    sw = torch.exp2(torch.randint(-2, 3, (E, up(w.shape[1]), up(w.shape[2])), generator=g, device="cuda").float())
+    off = offsets_of(np.random.RandomState(E).multinomial(rows, np.ones(E) / E))
+    ref, _ = ref_product(a, sa, off, w, sw, transposed)
+    out = moe.moe_grouped_gemm_f8(a, sa, off, w, sw, transposed=transposed, out_dtype=F32)
+    assert torch.equal(out.double(), ref)
+
+
+@pytest.mark.parametrize("transposed", [False, True])
+def test_many_units_on_streams_and_in_graphs(transposed):
+    """Overlapping, captured and replayed products of more than one unit per CTA, a long
+    and a short k in turn."""
+    E, rows, N = 16, 16384, 2992
+    off = offsets_of(np.random.RandomState(4).multinomial(rows, np.ones(E) / E))
+    sets = [operands(rows, E, N, K, transposed, K) for K in (128, 528)]
+
+    def call(stream=None):
+        return [moe.moe_grouped_gemm_f8(a, sa, off, w, sw, transposed=transposed, stream=stream)
+                for a, sa, w, sw in sets]
+    want = [t.clone() for t in call()]
+    torch.cuda.synchronize()
+    got = [call(s) for s in [torch.cuda.Stream() for _ in range(3)] for _ in range(3)]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for r in got for x, y in zip(r, want))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        r = call()
+    for _ in range(3):
+        for t in r:
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(r, want))
