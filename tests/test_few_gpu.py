@@ -364,3 +364,129 @@ def test_outputs_given_and_refused():
         L.few(torch.zeros((33, 64), dtype=BF16, device="cuda"), torch.zeros((33, 4), device="cuda"), 2, False)
     with pytest.raises(moe.MoeError):
         L.few(x, logits, 5, False)
+
+
+# ------------------------------------------------------------------ exact layers
+
+class ExactLayer:
+    """A layer in which nothing is rounded before y. x is 1 or 2. A row of gate has eight
+    values of 8 (where some fall on one place, of 8, 16 or 32, so that g >= 32 all the
+    same): FP32's SiLU(g) is then g itself, as exp(-g) < 2^-25 vanishes beside 1. A row
+    of up has eight of +-1. g and u have four bits each (or are a power of two), so that
+    h fits the 8 bits of BF16; |h| <= 2048. down is 0 or +-2^-6: an expert's sums are
+    whole multiples of 2^-3. 8-bit weights: the same values, as codes times scales of
+    2^-2 to 2^2."""
+
+    def __init__(self, E, H, I, dtype, f8, seed):
+        g = gen(seed)
+        self.E, self.H, self.I, self.dtype = E, H, I, dtype
+        kind = F8 if f8 else dtype
+        self.q, self.s = [], []
+        self.nonzero = []                                 # of gate and up: places and values
+        for which, (N, K) in enumerate(((I, H), (I, H), (H, I))):
+            r = torch.randint(-2, 3, (E, up_(N), up_(K)), generator=g, device="cuda") if f8 else None
+            q = torch.empty((E, N, K), dtype=kind, device="cuda")
+            if which < 2:
+                at = torch.randint(0, K, (E, N, 8), generator=g, device="cuda").sort(-1).values
+                first = torch.ones_like(at, dtype=torch.bool)
+                first[..., 1:] = at[..., 1:] != at[..., :-1]
+                if which == 0:
+                    v = 8.0 * first
+                    n = first.sum(-1, keepdim=True)      # x >= 1: g >= 8 n
+                    v = v * torch.where(n >= 4, 1.0, torch.where(n >= 2, 2.0, 4.0))
+                else:
+                    v = torch.where(torch.rand(at.shape, generator=g, device="cuda") < 0.5, -1.0, 1.0) * first
+                self.nonzero.append((at, v))
+                if f8:
+                    e, n = torch.arange(E, device="cuda").view(-1, 1, 1), torch.arange(N, device="cuda").view(1, -1, 1)
+                    v = v * torch.exp2(-r[e, n // B, at // B].float())
+                for s in range(E):
+                    m = torch.zeros((N, K), dtype=torch.float32 if N * K < 1 << 26 else BF16, device="cuda")
+                    m.scatter_add_(1, at[s], v[s].to(m.dtype))
+                    q[s] = m.to(kind)
+            else:
+                for s in range(E):
+                    for n0 in range(0, N, 4096):
+                        n1 = min(N, n0 + 4096)
+                        m = torch.randint(-1, 2, (n1 - n0, K), generator=g, device="cuda", dtype=torch.int8).float() * 2.0 ** -6
+                        if f8:
+                            n, k = torch.arange(n0, n1, device="cuda") // B, torch.arange(K, device="cuda") // B
+                            m *= torch.exp2(-r[s][n][:, k].float())
+                        q[s, n0:n1] = m.to(kind)
+            self.q.append(q)
+            self.s.append(torch.exp2(r.float()) if f8 else None)
+
+    def scales(self):
+        return dict(zip(("gate_scales", "up_scales", "down_scales"), self.s))
+
+    def x(self, T, seed):
+        return torch.randint(1, 3, (T, self.H), generator=gen(seed), device="cuda").to(self.dtype)
+
+    def ref(self, x, ids, w):
+        """sum over j of w[t, j] times the expert's output, in 64 bits, before the last rounding."""
+        T, k = ids.shape
+        h = torch.zeros((T, k, self.I), dtype=torch.float64, device="cuda")
+        for t in range(T):
+            for j in range(k):
+                g, u = ((x[t].double()[at[ids[t, j]]] * v[ids[t, j]].double()).sum(-1) for at, v in self.nonzero)
+                assert g.min() >= 32
+                h[t, j] = g * u
+        assert torch.equal(h, h.to(self.dtype).double())
+        y = torch.zeros((T, self.H), dtype=torch.float64, device="cuda")
+        size = torch.zeros_like(y)
+        w = w.double()
+        for e in range(self.E):
+            t, j = torch.nonzero(ids == e, as_tuple=True)
+            if not t.numel():
+                continue
+            for n0 in range(0, self.H, 2048):
+                m = self.q[2][e, n0:n0 + 2048].double()
+                if self.s[2] is not None:
+                    s = self.s[2][e].double().repeat_interleave(B, 0)[n0:n0 + m.shape[0]]
+                    m = m * s.repeat_interleave(B, 1)[:, :self.I]
+                # whole multiples of 2^-3, exact in FP32 in any order of summation
+                assert (h[t, j].abs() @ m.abs().T).max() * 8 < 2.0 ** 24
+                o = (h[t, j] @ m.T) * w[t, j].unsqueeze(-1)
+                y[:, n0:n0 + 2048].index_add_(0, t, o)
+                size[:, n0:n0 + 2048].index_add_(0, t, o.abs())
+        assert size.max() * 32 < 2.0 ** 24                # and of 2^-5, with weights
+        return y
+
+
+def exact_layer(T, k, E, H, I, dtype, f8, same_expert=False):
+    """Compares bit for bit. Routing weights: 2^-2 to 2^1, of either sign."""
+    L = ExactLayer(E, H, I, dtype, f8, T + E + H + I)
+    x = L.x(T, I)
+    g = gen(H)
+    ids = (torch.full((T, k), E - 1, device="cuda") if same_expert else
+           torch.rand((T, E), generator=g, device="cuda").argsort(1)[:, :k])
+    w = torch.exp2(torch.randint(-2, 2, (T, k), generator=g, device="cuda").float())
+    w *= torch.randint(0, 2, (T, k), generator=g, device="cuda") * 2 - 1
+    ref = L.ref(x, ids, w)
+    got = moe.moe_forward_few_routed(x, ids.int(), w, *L.q, **L.scales())
+    assert torch.equal(got, ref.float().to(dtype))
+    assert (ref != 0).double().mean() > 0.5               # zeros, or a pair left out, would not pass
+
+
+@pytest.mark.parametrize("dtype,f8", KINDS)
+@pytest.mark.parametrize("T,k,E,H,I", [
+    (1, 1, 1, 128, 128), (2, 6, 64, 272, 144), (8, 8, 8, 512, 64), (5, 2, 8, 1024, 512), (7, 3, 5, 48, 1040),
+    (17, 2, 3, 2048, 32), (32, 8, 40, 144, 272), (12, 8, 8, 640, 256), (24, 4, 4, 256, 640), (32, 8, 8, 1024, 384),
+    (32, 32, 33, 7168, 32), (32, 32, 32, 8192, 64), (32, 16, 17, 16384, 96)])
+def test_exact_layers(dtype, f8, T, k, E, H, I):
+    """Bit for bit, also where an expert's pairs make several chunks and where a CTA's
+    outputs take several passes (the last three)."""
+    exact_layer(T, k, E, H, I, dtype, f8)
+
+
+@pytest.mark.parametrize("dtype,f8", KINDS)
+def test_exact_layer_of_one_expert(dtype, f8):
+    """64 pairs of one expert: four to eight chunks."""
+    exact_layer(32, 2, 3, 1024, 256, dtype, f8, same_expert=True)
+
+
+@pytest.mark.parametrize("dtype,f8", [(BF16, False), (F32, False), (BF16, True)])
+def test_the_largest_sizes_exactly(dtype, f8):
+    """H and I at their limit, every output bit for bit."""
+    exact_layer(2, 1, 1, 65536, 65536, dtype, f8)
+    torch.cuda.empty_cache()
