@@ -873,8 +873,12 @@ int moe_grouped_gemm_f8(const uint8_t *a, int64_t lda, const float *a_scales, co
 
 /* ======================================================================
  * The whole layer for a few tokens (a decode step), in two kernels: routing, the
- * gate and up products and SwiGLU; the down product and the combine. It reads the
- * touched experts' matrices once and is bound by that.
+ * gate and up products and SwiGLU; the down product and the combine. It is bound by
+ * reading the touched experts' matrices: once for each 8 of an expert's (token, slot)
+ * pairs, or each 16 with BF16 / F16 weights and T * top_k >= 4 E. Up to 32 tokens that
+ * is faster than moe_forward, on F32 weights 3 times and more; on a few large experts in
+ * BF16 the two meet (8 of 4096 x 14336, top_k 2: 433 against 446 us for 9 tokens, 449
+ * against 448 for 16, 460 against 450 for 32).
  * ====================================================================== */
 
 /*
