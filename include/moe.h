@@ -830,8 +830,8 @@ int moe_quantize_rows(const void *x, int64_t ld, const int32_t *offsets, int64_t
  * moe_swiglu_quantize -- moe_quantize_rows of h = g / (1 + exp(-g)) * u.
  *   g, u    [rows, I] in dtype, row stride ld (both), read only: the gate and up
  *           products. h is FP32, not rounded before it is quantized (from BF16 and
- *           F16 rows within 2^-21 (1 + |g|) of itself; 1 / (1 + exp(-g)) below
- *           2^-126 counts as 0).
+ *           F16 rows within 2^-21 (1 + |g|) of itself). 1 / (1 + exp(-g)) below
+ *           2^-126 (of F32 rows 2^-128, where exp(-g) overflows) counts as 0.
  *   codes, scales, offsets, limits and errors as moe_quantize_rows.
  */
 int moe_swiglu_quantize(const void *g, const void *u, int64_t ld, const int32_t *offsets, int64_t E,
