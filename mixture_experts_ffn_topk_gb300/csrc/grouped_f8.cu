@@ -28,7 +28,9 @@
 // CTA with its own blocks; the FP32 partial sums meet through distributed shared
 // memory, each CTA adding its share of the rows in rank order.
 //
-// Bound by HBM where experts have few rows.
+// Bound by HBM where experts have few rows: 1024 rows on 256 experts of 7168 x 2048
+// 540 us, the copy bandwidth. Many small matrices cost more than their bytes: 64
+// experts of 2048 x 2048, 4 rows each, 48 us for 40 of bytes.
 //
 // Every wait is bounded (wait_ns); on expiry the kernel records ST_TIMEOUT, stops
 // issuing work, drains its own copies and MMAs, frees TMEM and exits.
@@ -557,9 +559,11 @@ cudaError_t launch_grouped_gemm_f8(const GroupedF8 &g, unsigned *status, cudaStr
     int split = 1;
     while (split < 8 && units * split * 2 <= sms && num_kb >= split * 2 * 2) split *= 2;
     if (split > 1) return launch_form<true>(g, split, status, s);
-    // The two forms, by the average rows of an expert: us at 4, 32, 48, 64, 96, 192
-    // rows, on 64 experts of N = K = 2048 (16 of N = K = 4096): this one 64 65 66 79
-    // 105 177 (68 70 70 74 97 160), the wide one 76 79 79 79 83 85 (81 81 81 81 83 85).
+    // The two forms, by the average rows of an expert, each row's expert drawn evenly:
+    // us at 32, 48, 56, 64, 72, 96 rows, on 64 experts of N = K = 2048 (16 of N = K =
+    // 4096): this one 50 51 57 74 87 93 (54 55 54 73 83 84), the wide one 65 65 65 66
+    // 66 66 (65 66 66 66 66 67). It is units of more than 64 rows that cost this form a
+    // second pass over the weights: with exactly 64 rows in each expert it takes 52 (55).
     if (g.rows >= 64 * (int64_t)g.E) return launch_grouped_gemm_f8_wide(g, status, s);
     return launch_form<false>(g, 1, status, s);
 }

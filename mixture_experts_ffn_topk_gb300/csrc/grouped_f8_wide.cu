@@ -8,15 +8,17 @@
 // multiply-add per value and nothing else. (With rows as columns each column has a
 // scale of its own, and fetching those from shared memory, 512 bytes per warp for
 // every 16-byte broadcast, took 1000 cycles of a block whose MMAs take 512.) An
-// expert's last unit may leave half a tile idle; with 64 rows per expert and less the
-// other form is faster.
+// expert's last unit may leave half a tile idle: with up to 64 rows in each expert the
+// other form is faster, with 64 on average and rows as a router spreads them this one
+// (launch_grouped_gemm_f8).
 //
 // What bounds it is the epilogue's latency per block of k: a barrier, 128 columns out
 // of TMEM, 128 multiply-adds (256 issue cycles of an SM partition's two warps), a
 // barrier; some 800 cycles and 100 of a unit's stores, where the MMAs take 512. 16384
-// rows on 8 experts of 4096 x 4096 take 240 us; when the epilogue found its units by
-// itself they took 247, of which 191 were left without TMEM reads and multiply-adds,
-// 216 with the reads alone, 243 with the multiply-adds alone. Tried: paired
+// rows on 8 experts of 4096 x 4096 take 218 us in a graph of ten calls (214 without
+// scales_apart: one flag to read and one branch per four blocks). In an older form,
+// of 247 us by single calls, 191 were left without TMEM reads and multiply-adds, 216
+// with the reads alone, 243 with the multiply-adds alone. Tried: paired
 // multiply-adds (320 against 273 us), four groups of epilogue warps with 64 columns
 // each (302), accumulators of 128 columns, four in turn (284).
 //
